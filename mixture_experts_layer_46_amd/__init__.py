@@ -8,6 +8,9 @@ workspace and passes pointers and the current stream; it has no other compute pa
 
 x [T, H] (bf16 or fp32), w_gate [H, E] fp32, w_in / w_up [E, H, F], w_out [E, F, H]
 (w_up None for the two-layer SiLU FFN), bias [E] fp32 or None.
+
+ops.py holds the operators that training the layer (forward_train) and serving it with
+8-bit experts (forward_int8) need, exported here too.
 """
 from __future__ import annotations
 
@@ -16,10 +19,13 @@ import torch
 from . import _lib
 from ._lib import (MOE_BF16, MOE_F32, MOE_FFN_SILU2, MOE_FFN_SWIGLU, MOE_FLAG_BIAS_SELECT_ONLY,
                    MOE_FLAG_NO_RENORM, MoeError, Shape, capacity_rows)
+from . import ops
+from .ops import *  # noqa: F401,F403  (ops.__all__)
 
 __all__ = ["forward", "route", "route_from_logits", "permute", "grouped_ffn", "combine",
            "router_stats", "make_shape", "Workspace", "Shape", "MoeError", "forward_intermediates",
            "MOE_FLAG_BIAS_SELECT_ONLY", "MOE_FLAG_NO_RENORM", "capacity_rows"]
+__all__ += ops.__all__
 
 
 def _dtype_code(t: torch.Tensor) -> int:

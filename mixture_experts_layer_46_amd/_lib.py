@@ -1,4 +1,4 @@
-"""ctypes binding of libmoe.so (include/moe.h).
+"""ctypes binding of libmoe.so (include/moe.h, include/moe_ops.h).
 
 Argument marshalling only: tensors become device pointers, the current torch stream
 becomes the hipStream_t, and every step of the layer runs in the library's kernels.
@@ -25,7 +25,12 @@ EXPORTS = ["moe_workspace_size", "moe_workspace_layout", "moe_capacity_rows", "m
            "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_forward", "moe_forward_timed",
            "moe_forward_noalloc", "moe_router_stats", "moe_status_str", "moe_last_error",
            "moe_peak_mfma_bf16",
-           "moe_peak_hbm_read", "moe_peak_hbm_copy"]
+           "moe_peak_hbm_read", "moe_peak_hbm_copy",
+           "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw", "moe_grouped_mm_int8",
+           "moe_quantize_rows", "moe_quantize_experts", "moe_dropout", "moe_gated_act",
+           "moe_gated_act_grad", "moe_combine_grad"]
+
+MOE_MM_ZERO_REST = 0x1
 
 MOE_STAGE_EVENTS = 6
 
@@ -42,6 +47,16 @@ class MoeWorkspaceParts(ctypes.Structure):
                 ("topk_w", ctypes.c_size_t), ("counts", ctypes.c_size_t), ("offsets", ctypes.c_size_t),
                 ("sorted_token", ctypes.c_size_t), ("row_of_pair", ctypes.c_size_t),
                 ("h", ctypes.c_size_t), ("y", ctypes.c_size_t), ("total", ctypes.c_size_t)]
+
+
+class MmShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class DropoutSpec(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("step", ctypes.c_uint64),
+                ("step_device", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -80,6 +95,20 @@ def load(path: str = LIB_PATH):
         "moe_forward_noalloc": [sp, vp, f32p, f32p, vp, vp, vp, vp, st],
         "moe_router_stats": [sp, f32p, f32p, i32p, i32p, f32p, st],
     }
+    mp, dp = ctypes.POINTER(MmShape), ctypes.POINTER(DropoutSpec)
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    sig.update({
+        "moe_grouped_mm": [mp, vp, vp, i32p, vp, st],
+        "moe_grouped_mm_dx": [mp, vp, vp, i32p, vp, st],
+        "moe_grouped_mm_dw": [mp, vp, vp, i32p, vp, st],
+        "moe_grouped_mm_int8": [mp, vp, f32p, vp, f32p, i32p, vp, st],
+        "moe_quantize_rows": [i32, i64, i32, vp, vp, f32p, st],
+        "moe_quantize_experts": [i32, i32, i32, i32, vp, vp, f32p, st],
+        "moe_dropout": [i32, i64, dp, vp, vp, st],
+        "moe_gated_act": [i32, i64, i32, dp, vp, i64, vp, i64, vp, st],
+        "moe_gated_act_grad": [i32, i64, i32, dp, vp, vp, i64, vp, i64, vp, i64, vp, i64, st],
+        "moe_combine_grad": [i32, i64, i32, i32, i64, vp, vp, i32p, f32p, vp, f32p, st],
+    })
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -206,6 +235,13 @@ def forward(shape: Shape, x, w_gate, bias, w_in, w_up, w_out, out, workspace, st
     _check("moe_forward_timed", load().moe_forward_timed(ctypes.byref(s), _ptr(x), _ptr(w_gate), _ptr(bias),
                                                          _ptr(w_in), _ptr(w_up), _ptr(w_out), _ptr(out),
                                                          _ptr(workspace), nbytes, arr, _stream(stream)))
+
+
+def call(name: str, *args):
+    """One call of an operator of moe_ops.h; raises MoeError on a non-OK status."""
+    code = getattr(load(), name)(*args)
+    if code != 0:
+        raise MoeError(name, code, load().moe_last_error().decode())
 
 
 NOALLOC_SCRATCH_BYTES = 256 << 20

@@ -1,0 +1,44 @@
+// Host-side launchers of the training and 8-bit operators (moe_ops.h).  Each enqueues on
+// `st` and returns the launch status; arguments were checked by the C ABI layer.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+struct MmArgs {
+    const void *a, *b;            // operands (see the kinds in mm_simple.hip)
+    void* c;
+    const int32_t* offsets;
+    const float *xs, *ws;         // int8: row and column scales
+    int rows, E, K, N;
+    int zero_rest;
+};
+
+// kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8
+hipError_t launch_mm_simple(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
+
+hipError_t launch_quantize_rows(const void* x, int dtype, long long rows, int K, int8_t* q, float* scale,
+                                hipStream_t st);
+hipError_t launch_quantize_experts(const void* w, int dtype, int E, int K, int N, int8_t* q, float* scale,
+                                   hipStream_t st);
+
+struct DropArgs {
+    uint32_t thr;                 // elements whose 16-bit number is below are dropped (0..65536)
+    float scale;
+    uint64_t seed, step;
+    const uint64_t* step_ptr;     // NULL, or a device word added to step
+};
+hipError_t launch_dropout(const void* x, void* y, int dtype, long long n, const DropArgs& d, hipStream_t st);
+hipError_t launch_gated_act(const void* a, long long lda, const void* b, long long ldb, void* h, int dtype,
+                            long long rows, int F, const DropArgs& d, hipStream_t st);
+hipError_t launch_gated_act_grad(const void* dh, const void* a, long long lda, const void* b, long long ldb, void* da,
+                                 long long ldda, void* db, long long lddb, int dtype, long long rows, int F,
+                                 const DropArgs& d, hipStream_t st);
+
+hipError_t launch_combine_grad(const void* dout, const void* y_perm, const int32_t* row_of_pair, const float* w,
+                               void* dy_perm, float* dw, long long T, int k, int H, int dtype, long long rows,
+                               hipStream_t st);
+
+}  // namespace moe

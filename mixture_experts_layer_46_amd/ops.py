@@ -1,0 +1,549 @@
+"""Operators beside the layer forward: what training the layer and serving it with 8-bit
+experts need.  Each runs in libmoe.so (include/moe_ops.h); this module checks arguments,
+allocates outputs and passes pointers and the stream, as the package's other wrappers do.
+
+    y  = grouped_mm(x, w, offsets)                  ragged rows times their expert's matrix
+    dx = grouped_mm_dx(dy, w, offsets)              its gradients (grouped_mm is
+    dw = grouped_mm_dw(x, dy, offsets)              differentiable by itself, too)
+    h  = gated_act(a, b, p, seed, step)             SiLU(a) * b with dropout; differentiable
+    da, db = gated_act_grad(dh, a, b, p, seed, step)
+    y  = dropout(x, p, seed, step)                  differentiable
+    dy_perm, dw = combine_grad(dout, y_perm, row_of_pair, topk_w)
+    q, scale = quantize_rows(x)                     8-bit rows, a scale per token
+    q, scale = quantize_experts(w)                  8-bit experts, a scale per output channel
+    y  = grouped_mm_int8(xq, x_scale, wq, w_scale, offsets)
+
+and the layers made of them:
+
+    forward_train(x, w_gate, w_in, w_up, w_out, top_k, ...)   differentiable
+    forward_int8(x, w_gate, experts, top_k, ...)              experts = quantize_ffn(w_in, w_up, w_out)
+
+Work is enqueued on the current stream of the tensors' device, which need not be the
+current device.  Tensors that another stream wrote or will use are the caller's to order,
+as everywhere in torch.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+from ._lib import (MOE_BF16, MOE_F32, MOE_FLAG_BIAS_SELECT_ONLY, MOE_FLAG_NO_RENORM, MOE_MM_ZERO_REST, DropoutSpec,
+                   MmShape)
+
+__all__ = ["grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "grouped_mm_int8", "quantize_rows", "quantize_experts",
+           "dropout", "gated_act", "gated_act_grad", "combine_grad", "QuantizedExperts", "quantize_ffn",
+           "grouped_ffn_int8", "forward_int8", "forward_train"]
+
+_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_NULL_CONTEXT = contextlib.nullcontext()
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError(f"{name}: unsupported element type {t.dtype}")
+    return c
+
+
+def _check(t, name, dtype, shape):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _place(**ts):
+    """All on one GPU and contiguous; returns a context that makes it the current device."""
+    dev = None
+    for name, t in ts.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU (there is no CPU path)")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+    return _device(dev)
+
+
+def _device(dev):
+    return _NULL_CONTEXT if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _dims(t, n, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} dimensions")
+
+
+def _mm_shape(rows, E, K, N, dtype, out_dtype, rest):
+    return ctypes.byref(MmShape(rows, E, K, N, dtype, out_dtype, MOE_MM_ZERO_REST if rest else 0))
+
+
+# ------------------------------------------------------------------- grouped products
+def _mm(x, w, offsets, out, transposed, xname, oname):
+    _dims(w, 3, "w")
+    E, K, N = w.shape
+    _dims(x, 2, xname)
+    cin, cout = (N, K) if transposed else (K, N)
+    R = x.shape[0]
+    code = _code(x, xname)
+    _check(x, xname, x.dtype, (R, cin))
+    _check(w, "w", x.dtype, (E, K, N))
+    _check(offsets, "offsets", torch.int32, (E + 1,))
+    rest = out is None
+    if out is not None:
+        _check(out, oname, x.dtype, (R, cout))
+    with _place(**{xname: x, "w": w, "offsets": offsets, oname: out}):
+        if out is None:
+            out = torch.empty((R, cout), dtype=x.dtype, device=x.device)
+        _lib.call("moe_grouped_mm_dx" if transposed else "moe_grouped_mm", _mm_shape(R, E, K, N, code, code, rest),
+                  x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream())
+    return out
+
+
+class _GroupedMM(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return _mm(x, w, offsets, None, False, "x", "out")
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = grouped_mm_dx(dy, w, offsets) if ctx.needs_input_grad[0] else None
+        dw = grouped_mm_dw(x, dy, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dw, None
+
+
+def grouped_mm(x, w, offsets, out=None):
+    """y[r] = x[r] @ w[e] for the rows r of every group e, the rows [offsets[e], offsets[e+1]).
+
+    x [R, K] and w [E, K, N] bf16 or fp32, offsets [E+1] int32 (permute's); y [R, N] in x's
+    type, summed in fp32 and rounded once.  Rows that lie in no group are zeros, or with
+    `out` given left as they were.  Differentiable in x and w (without `out`)."""
+    if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(w, "requires_grad", False)):
+        if out is not None:
+            raise ValueError("out cannot be given where a gradient is recorded")
+        return _GroupedMM.apply(x, w, offsets)
+    return _mm(x, w, offsets, out, False, "x", "out")
+
+
+def grouped_mm_dx(dy, w, offsets, out=None):
+    """The gradient of grouped_mm by x: dx[r] = dy[r] @ w[e]^T; dy [R, N], w [E, K, N] -> [R, K].
+    Rows that lie in no group are zeros, or with `out` given left as they were."""
+    return _mm(dy, w, offsets, out, True, "dy", "out")
+
+
+def grouped_mm_dw(x, dy, offsets, out=None, dtype=None):
+    """The gradient of grouped_mm by w: dw[e] = x_e^T @ dy_e over the rows of group e (zeros
+    for a group without rows); x [R, K], dy [R, N] -> [E, K, N] in x's type, or for bf16 in
+    fp32 with dtype=torch.float32 (or an fp32 `out`)."""
+    _dims(x, 2, "x")
+    _dims(dy, 2, "dy")
+    R, K = x.shape
+    N = dy.shape[1]
+    code = _code(x, "x")
+    _check(dy, "dy", x.dtype, (R, N))
+    _dims(offsets, 1, "offsets")
+    E = offsets.shape[0] - 1
+    _check(offsets, "offsets", torch.int32, (E + 1,))
+    if dtype is None:
+        dtype = out.dtype if out is not None else x.dtype
+    if dtype != x.dtype and dtype != torch.float32:
+        raise ValueError(f"dtype must be {x.dtype} or torch.float32, got {dtype}")
+    if out is not None:
+        _check(out, "out", dtype, (E, K, N))
+    with _place(x=x, dy=dy, offsets=offsets, out=out):
+        if out is None:
+            out = torch.empty((E, K, N), dtype=dtype, device=x.device)
+        _lib.call("moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
+                  offsets.data_ptr(), out.data_ptr(), _stream())
+    return out
+
+
+# -------------------------------------------------------------------- 8-bit integers
+def quantize_rows(x):
+    """8-bit rows of x [R, K] (bf16 or fp32): (q [R, K] int8, scale [R] fp32) with
+    scale = max|row| / 127 and q = row / scale to the nearest integer, ties to even.  A row
+    with an infinity or a NaN gets scale NaN and q 0."""
+    _dims(x, 2, "x")
+    code = _code(x, "x")
+    R, K = x.shape
+    with _place(x=x):
+        q = torch.empty((R, K), dtype=torch.int8, device=x.device)
+        scale = torch.empty(R, dtype=torch.float32, device=x.device)
+        _lib.call("moe_quantize_rows", code, R, K, x.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream())
+    return q, scale
+
+
+def quantize_experts(w):
+    """8-bit expert matrices of w [E, K, N] (bf16 or fp32), made once: (q [E, N, K] int8,
+    scale [E, N] fp32), each output channel quantised over K as quantize_rows does a row."""
+    _dims(w, 3, "w")
+    code = _code(w, "w")
+    E, K, N = w.shape
+    with _place(w=w):
+        q = torch.empty((E, N, K), dtype=torch.int8, device=w.device)
+        scale = torch.empty((E, N), dtype=torch.float32, device=w.device)
+        _lib.call("moe_quantize_experts", code, E, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream())
+    return q, scale
+
+
+def grouped_mm_int8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out=None):
+    """y[r] = (xq[r] @ wq[e]^T) * x_scale[r] * w_scale[e] for the rows r of every group e: the
+    product exact in int32, the scales in fp32, one rounding to `dtype` (bf16 or fp32).
+
+    xq [R, K] int8, x_scale [R] fp32, wq [E, N, K] int8, w_scale [E, N] fp32, offsets [E+1]
+    int32 -> [R, N].  Rows that lie in no group are zeros, or with `out` given left as they
+    were."""
+    _dims(xq, 2, "xq")
+    _dims(wq, 3, "wq")
+    R, K = xq.shape
+    E, N, _ = wq.shape
+    _check(xq, "xq", torch.int8, (R, K))
+    _check(x_scale, "x_scale", torch.float32, (R,))
+    _check(wq, "wq", torch.int8, (E, N, K))
+    _check(w_scale, "w_scale", torch.float32, (E, N))
+    _check(offsets, "offsets", torch.int32, (E + 1,))
+    rest = out is None
+    if out is not None:
+        dtype = out.dtype
+        _check(out, "out", dtype, (R, N))
+    if dtype not in _CODES:
+        raise TypeError(f"unsupported output type {dtype}")
+    with _place(xq=xq, x_scale=x_scale, wq=wq, w_scale=w_scale, offsets=offsets, out=out):
+        if out is None:
+            out = torch.empty((R, N), dtype=dtype, device=xq.device)
+        _lib.call("moe_grouped_mm_int8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
+                  x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream())
+    return out
+
+
+# --------------------------------------------------------------------------- dropout
+def _spec(p, seed, step, dev):
+    """The dropout's parameters; a tensor `step` is read on the device when the kernel runs."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p = {p} must lie in [0, 1]")
+    ptr = None
+    if isinstance(step, torch.Tensor):
+        if step.dtype != torch.int64 or step.numel() != 1 or step.device != dev:
+            raise ValueError(f"a tensor step must hold one int64 on {dev}")
+        ptr, step = step.data_ptr(), 0
+    return ctypes.byref(DropoutSpec(p, seed & 0xFFFFFFFFFFFFFFFF, step & 0xFFFFFFFFFFFFFFFF, ptr))
+
+
+def _dropout(x, p, seed, step, out):
+    code = _code(x, "x")
+    if out is not None:
+        _check(out, "out", x.dtype, x.shape)
+    with _place(x=x, out=out):
+        if out is None:
+            out = torch.empty_like(x)
+        _lib.call("moe_dropout", code, x.numel(), _spec(p, seed, step, x.device), x.data_ptr(), out.data_ptr(),
+                  _stream())
+    return out
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, step):
+        ctx.p, ctx.seed, ctx.step = p, seed, _kept_step(step)
+        return _dropout(x, p, seed, step, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        return _dropout(dy.contiguous(), ctx.p, ctx.seed, ctx.step, None), None, None, None
+
+
+def _kept_step(step):
+    """The step as the backward pass will need it: a tensor may be advanced in between."""
+    return step.clone() if isinstance(step, torch.Tensor) else step
+
+
+def dropout(x, p, seed, step=0, out=None):
+    """Counter-based dropout of x (bf16 or fp32, any shape): the element of row-major index i is
+    kept and multiplied by 65536 / (65536 - t), t = round(65536 p), where the generator's
+    16-bit number i of (seed, step) is at least t, else 0.  The mask is never stored: the
+    gradient draws it again.  Use another `step` for every tensor and training step.
+
+    `step` is an integer, or a tensor of one int64 on the GPU that the kernel reads (so that
+    a captured call draws another mask at each replay).  `out` may be x.  Differentiable in
+    x (without `out`)."""
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x is required")
+    if torch.is_grad_enabled() and x.requires_grad:
+        if out is not None:
+            raise ValueError("out cannot be given where a gradient is recorded")
+        return _Dropout.apply(x, p, seed, step)
+    return _dropout(x, p, seed, step, out)
+
+
+def _row_stride(t, name):
+    """Elements from one row of t [R, F] to the next: the last dimension is dense, rows may be
+    apart (the halves of a packed [R, 2 F] tensor)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU (there is no CPU path)")
+    R, F = t.shape
+    if F > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    ld = t.stride(0) if R > 1 else F
+    if ld < F:
+        raise ValueError(f"the rows of {name} overlap (stride {ld} < {F})")
+    return ld
+
+
+def _act_args(a, b):
+    _dims(a, 2, "a")
+    code = _code(a, "a")
+    lda, ldb = _row_stride(a, "a"), 0
+    if b is not None:
+        _check(b, "b", a.dtype, a.shape)
+        ldb = _row_stride(b, "b")
+        if b.device != a.device:
+            raise ValueError(f"b is on {b.device}, a on {a.device}")
+    return code, lda, ldb
+
+
+def _gated_act(a, b, p, seed, step, out):
+    code, lda, ldb = _act_args(a, b)
+    R, F = a.shape
+    if out is not None:
+        _check(out, "out", a.dtype, (R, F))
+        _place(out=out)
+        if out.device != a.device:
+            raise ValueError(f"out is on {out.device}, a on {a.device}")
+    with _device(a.device):
+        if out is None:
+            out = torch.empty((R, F), dtype=a.dtype, device=a.device)
+        _lib.call("moe_gated_act", code, R, F, _spec(p, seed, step, a.device), a.data_ptr(), lda,
+                  None if b is None else b.data_ptr(), ldb, out.data_ptr(), _stream())
+    return out
+
+
+class _GatedAct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, a, b, p, seed, step):
+        ctx.save_for_backward(a, b)
+        ctx.p, ctx.seed, ctx.step = p, seed, _kept_step(step)
+        return _gated_act(a, b, p, seed, step, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        a, b = ctx.saved_tensors
+        da, db = gated_act_grad(dh.contiguous(), a, b, ctx.p, ctx.seed, ctx.step)
+        return da, db, None, None, None
+
+
+def gated_act(a, b=None, p=0.0, seed=0, step=0, out=None):
+    """h = SiLU(a) * b with counter-based dropout (p, seed, step as in dropout): the experts'
+    activation; b None: SiLU(a).  a, b [R, F] bf16 or fp32, dense along F, rows may be apart
+    (halves of a packed tensor); h [R, F] dense.  Differentiable in a and b (without `out`)."""
+    if torch.is_grad_enabled() and (getattr(a, "requires_grad", False) or getattr(b, "requires_grad", False)):
+        if out is not None:
+            raise ValueError("out cannot be given where a gradient is recorded")
+        return _GatedAct.apply(a, b, p, seed, step)
+    return _gated_act(a, b, p, seed, step, out)
+
+
+def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
+    """(da, db) of gated_act for the gradient dh [R, F] (db None when b is).  `out` = (da, db):
+    tensors to write, which may be halves of one packed gradient."""
+    code, lda, ldb = _act_args(a, b)
+    R, F = a.shape
+    _check(dh, "dh", a.dtype, (R, F))
+    _place(dh=dh)
+    if dh.device != a.device:
+        raise ValueError(f"dh is on {dh.device}, a on {a.device}")
+    with _device(a.device):
+        if out is None:
+            da = torch.empty((R, F), dtype=a.dtype, device=a.device)
+            db = None if b is None else torch.empty((R, F), dtype=a.dtype, device=a.device)
+        else:
+            da, db = out
+            _check(da, "da", a.dtype, (R, F))
+            if (db is None) != (b is None):
+                raise ValueError("db must be given exactly when b is")
+            if db is not None:
+                _check(db, "db", a.dtype, (R, F))
+            for t, name in ((da, "da"), (db, "db")):
+                if t is not None and t.device != a.device:
+                    raise ValueError(f"{name} is on {t.device}, a on {a.device}")
+        _lib.call("moe_gated_act_grad", code, R, F, _spec(p, seed, step, a.device), dh.data_ptr(), a.data_ptr(), lda,
+                  None if b is None else b.data_ptr(), ldb, da.data_ptr(), _row_stride(da, "da"),
+                  None if db is None else db.data_ptr(), 0 if db is None else _row_stride(db, "db"), _stream())
+    return da, db
+
+
+# --------------------------------------------------------------------------- combine
+def combine_grad(dout, y_perm, row_of_pair, topk_w):
+    """The gradient of combine: (dy_perm [R, H], dtopk_w [T, k]) for dout [T, H], y_perm [R, H]
+    (bf16 or fp32), row_of_pair [T*k] int32 and topk_w [T, k] fp32.  A dropped pair (row -1)
+    has dtopk_w 0; rows of dy_perm that no pair names are unset."""
+    _dims(dout, 2, "dout")
+    _dims(y_perm, 2, "y_perm")
+    _dims(topk_w, 2, "topk_w")
+    code = _code(dout, "dout")
+    T, H = dout.shape
+    R, k = y_perm.shape[0], topk_w.shape[1]
+    _check(y_perm, "y_perm", dout.dtype, (R, H))
+    _check(topk_w, "topk_w", torch.float32, (T, k))
+    _check(row_of_pair, "row_of_pair", torch.int32, (T * k,))
+    with _place(dout=dout, y_perm=y_perm, row_of_pair=row_of_pair, topk_w=topk_w):
+        dy = torch.empty((R, H), dtype=dout.dtype, device=dout.device)
+        dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+        _lib.call("moe_combine_grad", code, T, k, H, R, dout.data_ptr(), y_perm.data_ptr(), row_of_pair.data_ptr(),
+                  topk_w.data_ptr(), dy.data_ptr(), dw.data_ptr(), _stream())
+    return dy, dw
+
+
+# ------------------------------------------------------- the layer with 8-bit experts
+class QuantizedExperts(NamedTuple):
+    """The experts' 8-bit matrices (quantize_ffn): (q [E, N, K] int8, scale [E, N] fp32) each."""
+    w_in: tuple
+    w_up: Optional[tuple]
+    w_out: tuple
+
+
+def quantize_ffn(w_in, w_up, w_out) -> QuantizedExperts:
+    """The experts of forward (w_in, w_up [E, H, F], w_up None for the two-layer SiLU FFN;
+    w_out [E, F, H]) as 8-bit matrices, made once.  H and F multiples of 16."""
+    return QuantizedExperts(quantize_experts(w_in), None if w_up is None else quantize_experts(w_up),
+                            quantize_experts(w_out))
+
+
+def grouped_ffn_int8(x_perm, offsets, experts: QuantizedExperts):
+    """The grouped expert FFN on 8-bit experts: the rows x_perm [R, H] and the activated hidden
+    rows are quantised per token, both projections run in 8-bit integers.  Returns [R, H] in
+    x_perm's type; rows that lie in no group are zeros."""
+    q, s = quantize_rows(x_perm)
+    a = grouped_mm_int8(q, s, *experts.w_in, offsets, dtype=x_perm.dtype)
+    b = None if experts.w_up is None else grouped_mm_int8(q, s, *experts.w_up, offsets, dtype=x_perm.dtype)
+    q, s = quantize_rows(gated_act(a, b))
+    return grouped_mm_int8(q, s, *experts.w_out, offsets, dtype=x_perm.dtype)
+
+
+def forward_int8(x, w_gate, experts: QuantizedExperts, top_k, bias=None, flags=0, capacity_factor=None, out=None):
+    """The whole layer (forward) with 8-bit experts (quantize_ffn); the routing stays fp32."""
+    import mixture_experts_layer_46_amd as M
+    T, H, E, _ = M._check_layer(x, w_gate, bias, out=out, top_k=top_k, experts=False)
+    if out is None:
+        out = torch.empty_like(x)
+    if T == 0:
+        return out
+    with _place(x=x, w_gate=w_gate, bias=bias, out=out):
+        _, idx, w = M.route(x, w_gate, top_k, bias=bias, flags=flags)
+        g = M.permute(idx, E, x=x, capacity=_lib.capacity_rows(capacity_factor, T, top_k, E))
+        y = grouped_ffn_int8(g["x_perm"], g["offsets"], experts)
+        return M.combine(y, g["row_of_pair"], w, out=out)
+
+
+# ----------------------------------------------------------------- the layer, trained
+class _Route(torch.autograd.Function):
+    """Gates of the chosen experts.  g = softmax over the chosen logits (the renormalised
+    gates are that), so dl_j = g_j (dg_j - sum_i g_i dg_i), and by the gate projection
+    dW_g = x^T dl, dx = dl W_g^T: two grouped products of one group, in fp32."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, bias, top_k, flags):
+        import mixture_experts_layer_46_amd as M
+        logits, idx, g = M.route(x, w_gate, top_k, bias=bias, flags=flags)
+        ctx.save_for_backward(x, w_gate, idx, g)
+        ctx.flags = flags
+        ctx.mark_non_differentiable(idx, logits)
+        return g, idx, logits
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dg, _didx, _dlogits):
+        x, w_gate, idx, g = ctx.saved_tensors
+        T, H = x.shape
+        E = w_gate.shape[1]
+        Ep = (E + 7) // 8 * 8                             # the products take multiples of 8
+        dl = torch.zeros((T, Ep), dtype=torch.float32, device=x.device)
+        dl.scatter_(1, idx.long(), g * (dg - (g * dg).sum(dim=1, keepdim=True)))
+        one = torch.arange(2, dtype=torch.int32, device=x.device) * T
+        dx = dw = db = None
+        if ctx.needs_input_grad[0]:
+            wp = w_gate if Ep == E else torch.nn.functional.pad(w_gate, (0, Ep - E))
+            dx = grouped_mm_dx(dl, wp.unsqueeze(0), one).to(x.dtype)
+        if ctx.needs_input_grad[1]:
+            dw = grouped_mm_dw(x.float(), dl, one)[0, :, :E]
+        if ctx.needs_input_grad[2]:
+            db = torch.zeros(E, dtype=torch.float32, device=x.device)
+            if not ctx.flags & MOE_FLAG_BIAS_SELECT_ONLY:
+                db = dl[:, :E].sum(dim=0)
+        return dx, dw, db, None, None
+
+
+class _Permute(torch.autograd.Function):
+    """Grouped rows of x; its gradient adds each token's rows (the combine with weights 1)."""
+
+    @staticmethod
+    def forward(ctx, x, idx, E, capacity):
+        import mixture_experts_layer_46_amd as M
+        r = M.permute(idx, E, x=x, capacity=capacity)
+        ctx.save_for_backward(r["row_of_pair"])
+        ctx.k = idx.shape[1]
+        ctx.mark_non_differentiable(r["offsets"], r["row_of_pair"])
+        return r["x_perm"], r["offsets"], r["row_of_pair"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dx_perm, _o, _r):
+        import mixture_experts_layer_46_amd as M
+        (row_of_pair,) = ctx.saved_tensors
+        T = row_of_pair.numel() // ctx.k
+        ones = torch.ones((T, ctx.k), dtype=torch.float32, device=dx_perm.device)
+        return M.combine(dx_perm.contiguous(), row_of_pair, ones), None, None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y_perm, row_of_pair, topk_w):
+        import mixture_experts_layer_46_amd as M
+        ctx.save_for_backward(y_perm, row_of_pair, topk_w)
+        return M.combine(y_perm, row_of_pair, topk_w)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        dy, dw = combine_grad(dout.contiguous(), *ctx.saved_tensors)
+        return dy, None, dw
+
+
+def forward_train(x, w_gate, w_in, w_up, w_out, top_k, bias=None, dropout_p=0.0, seed=0, step=0, flags=0,
+                  capacity_factor=None):
+    """The whole layer (forward), differentiable in x, w_gate, w_in, w_up, w_out and bias, with
+    dropout of the experts' activated hidden rows (dropout_p, seed, step as in dropout; the
+    hidden rows are the tensor, in grouped order).  Returns out [T, H].  The choice of the
+    experts has no gradient; the gates have.  MOE_FLAG_NO_RENORM is not supported."""
+    import mixture_experts_layer_46_amd as M
+    T, H, E, F = M._check_layer(x, w_gate, bias, w_in, w_up, w_out, None, top_k)
+    if flags & MOE_FLAG_NO_RENORM:
+        raise ValueError("forward_train has the gradient of renormalised gates only")
+    if T == 0:
+        raise ValueError("forward_train needs at least one token")
+    with _place(x=x, w_gate=w_gate, bias=bias, w_in=w_in, w_up=w_up, w_out=w_out):
+        g, idx, _ = _Route.apply(x, w_gate, bias, top_k, flags)
+        x_perm, offsets, row_of_pair = _Permute.apply(x, idx, E, _lib.capacity_rows(capacity_factor, T, top_k, E))
+        a = grouped_mm(x_perm, w_in, offsets)
+        b = None if w_up is None else grouped_mm(x_perm, w_up, offsets)
+        h = gated_act(a, b, dropout_p, seed, step)
+        return _Combine.apply(grouped_mm(h, w_out, offsets), row_of_pair, g)
