@@ -19,6 +19,8 @@ struct MmArgs {
 // kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8
 hipError_t launch_mm_simple(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
 
+hipError_t launch_mm(int kind, int out_dtype, const MmArgs& a, hipStream_t st);      // bf16 and int8
+
 hipError_t launch_quantize_rows(const void* x, int dtype, long long rows, int K, int8_t* q, float* scale,
                                 hipStream_t st);
 hipError_t launch_quantize_experts(const void* w, int dtype, int E, int K, int N, int8_t* q, float* scale,

@@ -104,6 +104,12 @@ moe_status check_ld(int64_t ld, int32_t F, const char* name) {
     return MOE_OK;
 }
 
+// kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8
+hipError_t run_mm(int kind, const moe_mm_shape& s, const MmArgs& a, hipStream_t st) {
+    if (kind != 3 && s.dtype == MOE_F32) return launch_mm_simple(kind, s.dtype, s.out_dtype, a, st);
+    return launch_mm(kind, s.out_dtype, a, st);
+}
+
 }  // namespace
 
 }  // namespace moe
@@ -120,7 +126,7 @@ moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, const void* 
     REQ(w, "w");
     REQ(offsets, "offsets");
     REQ(y, "y");
-    HIPCHK(launch_mm_simple(0, shape->dtype, shape->out_dtype, mm_args(*shape, x, w, y, offsets), stream), "grouped_mm");
+    HIPCHK(run_mm(0, *shape, mm_args(*shape, x, w, y, offsets), stream), "grouped_mm");
     return MOE_OK;
 }
 
@@ -132,7 +138,7 @@ moe_status moe_grouped_mm_dx(const moe_mm_shape* shape, const void* dy, const vo
     REQ(w, "w");
     REQ(offsets, "offsets");
     REQ(dx, "dx");
-    HIPCHK(launch_mm_simple(1, shape->dtype, shape->out_dtype, mm_args(*shape, dy, w, dx, offsets), stream),
+    HIPCHK(run_mm(1, *shape, mm_args(*shape, dy, w, dx, offsets), stream),
            "grouped_mm_dx");
     return MOE_OK;
 }
@@ -146,7 +152,7 @@ moe_status moe_grouped_mm_dw(const moe_mm_shape* shape, const void* x, const voi
     }
     REQ(offsets, "offsets");
     REQ(dw, "dw");
-    HIPCHK(launch_mm_simple(2, shape->dtype, shape->out_dtype, mm_args(*shape, x, dy, dw, offsets), stream),
+    HIPCHK(run_mm(2, *shape, mm_args(*shape, x, dy, dw, offsets), stream),
            "grouped_mm_dw");
     return MOE_OK;
 }
@@ -191,7 +197,7 @@ moe_status moe_grouped_mm_int8(const moe_mm_shape* shape, const int8_t* xq, cons
     MmArgs a = mm_args(*shape, xq, wq, y, offsets);
     a.xs = x_scale;
     a.ws = w_scale;
-    HIPCHK(launch_mm_simple(3, MOE_BF16, shape->out_dtype, a, stream), "grouped_mm_int8");
+    HIPCHK(run_mm(3, *shape, a, stream), "grouped_mm_int8");
     return MOE_OK;
 }
 
