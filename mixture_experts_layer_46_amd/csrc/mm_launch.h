@@ -8,7 +8,7 @@
 namespace moe {
 
 struct MmArgs {
-    const void *a, *b;            // operands (see the kinds in mm_simple.hip)
+    const void *a, *b;            // operands (see the kinds in mm_tile.h)
     void* c;
     const int32_t* offsets;
     const float *xs, *ws;         // int8: row and column scales
@@ -17,9 +17,13 @@ struct MmArgs {
 };
 
 // kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8
-hipError_t launch_mm_simple(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
 
-hipError_t launch_mm(int kind, int out_dtype, const MmArgs& a, hipStream_t st);      // bf16 and int8
+hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
+// its forms: 256 x 256 tiles (bf16, int8); tiles of 64 or 128; 16, 32 or 64 rows with the
+// contraction split over 4 or 8 wavefronts (not kind 2)
+hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t st);
+hipError_t launch_mm_mid(int tile, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
+hipError_t launch_mm_thin(int rows, int waves, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
 
 hipError_t launch_quantize_rows(const void* x, int dtype, long long rows, int K, int8_t* q, float* scale,
                                 hipStream_t st);

@@ -106,8 +106,7 @@ moe_status check_ld(int64_t ld, int32_t F, const char* name) {
 
 // kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8
 hipError_t run_mm(int kind, const moe_mm_shape& s, const MmArgs& a, hipStream_t st) {
-    if (kind != 3 && s.dtype == MOE_F32) return launch_mm_simple(kind, s.dtype, s.out_dtype, a, st);
-    return launch_mm(kind, s.out_dtype, a, st);
+    return launch_mm(kind, s.dtype, s.out_dtype, a, st);
 }
 
 }  // namespace
