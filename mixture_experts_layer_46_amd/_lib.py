@@ -237,9 +237,15 @@ def forward(shape: Shape, x, w_gate, bias, w_in, w_up, w_out, out, workspace, st
                                                          _ptr(workspace), nbytes, arr, _stream(stream)))
 
 
+_functions = {}
+
+
 def call(name: str, *args):
     """One call of an operator of moe_ops.h; raises MoeError on a non-OK status."""
-    code = getattr(load(), name)(*args)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
+    code = fn(*args)
     if code != 0:
         raise MoeError(name, code, load().moe_last_error().decode())
 

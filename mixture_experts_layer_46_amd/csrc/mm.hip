@@ -1,15 +1,21 @@
 // Grouped products, large tiles: 256 x 256 on the matrix cores (mm_tile.h has the kinds, the
 // operand layouts and the loads).
 //
-// Eight wavefronts in two groups of four (one of each per SIMD); a group owns half the
-// tile's rows as 128 x 64 wavefront tiles, 128 accumulator registers each.  The groups run
-// half a step out of phase: while one reads its operands from LDS and starts the loads of
-// a later step, the other's matrix instructions run.  Operands go into four LDS stages,
-// three steps ahead; every wavefront issues the same number of loads per step, so one
-// constant vmcnt waits for the step that is needed next.
+// Eight wavefronts, 2 x 4 over the tile: 128 x 64 wavefront tiles of 128 accumulator
+// registers, two wavefronts per SIMD.  Operands go into four LDS stages.  Two forms of the
+// inner loop:
+//   woven       within a step every wavefront multiplies the operands it holds in registers,
+//               reads the next step's from LDS and starts the loads of the fourth step after,
+//               spread between the matrix instructions; one barrier a step.
+//   step-apart  the wavefronts of the upper and of the lower rows (one of each per SIMD) run
+//               half a step out of phase: while one reads its operands and starts loads, the
+//               other's matrix instructions run; two barriers a step.
+// Operands in `columns` layout take twice the LDS reads, which the step-apart form cannot
+// hide in half a step: woven there (kinds 0 and 2; 8 experts, 8192 rows, 4096 <-> 14336: 912
+// against 947 us and 975 against 1042), step-apart for kinds 1 and 3 (994 against 1016, int8
+// 506 against 515; 4096^3: 107.6 against 113.2).
 #include "mm_tile.h"
 
-#include <stdlib.h>
 namespace moe {
 
 namespace {
@@ -23,8 +29,56 @@ static_assert(kStages * kStage <= (int)kLds, "the stages fit below the staging t
 constexpr int kLoads = 2;                     // loads of one operand per wavefront and step
 constexpr int kVmcnt = 4 * kLoads;            // loads of the two steps after the awaited one
 
-// The steps of one group.  Between two barriers one group is in its read phase (R) and the
-// other in its matrix phase (M):
+template <typename O>
+constexpr bool kApart = !O::kACols && !O::kBCols;
+template <typename O>
+using OpA = Operand<O::ES, O::kACols, kT, kLoads>;
+template <typename O>
+using OpB = Operand<O::ES, O::kBCols, kT, kLoads>;
+
+// One step: the products of the operands in registers, with the next step's operands read
+// from stage `rd` and a later step's loads started into stage `wr` in between (two reads
+// after each of six row blocks, the loads after the third and the fifth: measured against
+// denser and later placements, 1-4% on the large shapes).  The matrix instruction takes the
+// B operand first, so that a lane's four sums are four columns of one row.
+// The stages are separate __restrict__ arguments: otherwise the compiler takes the
+// transposing reads to touch what is in flight, and waits for every load before them.
+template <typename O>
+__device__ __attribute__((always_inline)) inline void step(const lds_char* __restrict__ rd, lds_char* __restrict__ wr,
+                                                           int kload, int nblk, int wm, int wn, int wave,
+                                                           const OpA<O>& oa, const OpB<O>& ob,
+                                                           const Reader<O::ES, O::kACols, kT>& ra,
+                                                           const Reader<O::ES, O::kBCols, kT>& rb,
+                                                           const u32x4_t (&af)[8], const u32x4_t (&bf)[4],
+                                                           u32x4_t (&an)[8], u32x4_t (&bn)[4],
+                                                           typename O::Acc (&acc)[8][4]) {
+    asm volatile("" : "+s"(nblk));    // compared anew at each row block (a scalar compare; kept masks cost vector ones)
+    wait_lds();                       // this step's operands are in registers: their stage is free
+    wait_vmcnt<kVmcnt>();             // this wavefront's loads of the next step have landed
+    lds_barrier();                    // everyone's
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (__builtin_expect(i < nblk, 1)) {                  // a full tile falls through
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mma<O::ELEM>(bf[j], af[i], acc[i][j]);
+        }
+#pragma unroll
+        for (int q = 2 * i; q < 2 * i + 2; ++q) {
+            if (q < 4) bn[q] = rb(rd + kT * 64, wn * 4 + q);
+            else if (q < 12) an[q - 4] = ra(rd, wm * 8 + q - 4);
+        }
+        if (i == 2) oa.load(wr, wave * kLoads, kload);
+        if (i == 4) ob.load(wr + kT * 64, wave * kLoads, kload);
+    }
+    // the sums live in accumulator registers, next to the two sets of operands
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+// The steps of one of the two wavefront groups, in step-apart form (below).  Between two
+// barriers one group is in its read phase (R) and the other in its matrix phase (M):
 //   group 0:  R0 | M0 | R1 | M1 | ... | M(KT-1) | (idle)
 //   group 1: (idle) | R0 | M0 | R1 | ... | R(KT-1) | M(KT-1)
 // R(k) starts the loads of step k + 3 into the stage that held step k - 1, which both groups
@@ -33,8 +87,7 @@ constexpr int kVmcnt = 4 * kLoads;            // loads of the two steps after th
 // by group 1 at the end of R(k).
 template <typename O, int GROUP>
 __device__ __attribute__((always_inline)) inline void steps(lds_char* lds, int KT, int nblk, int ablk, int wn, int wave,
-                                                            const Operand<O::ES, O::kACols, kT, kLoads>& oa,
-                                                            const Operand<O::ES, O::kBCols, kT, kLoads>& ob,
+                                                            const OpA<O>& oa, const OpB<O>& ob,
                                                             const Reader<O::ES, O::kACols, kT>& ra,
                                                             const Reader<O::ES, O::kBCols, kT>& rb,
                                                             typename O::Acc (&acc)[8][4]) {
@@ -46,12 +99,12 @@ __device__ __attribute__((always_inline)) inline void steps(lds_char* lds, int K
         wait_lds();
         if constexpr (GROUP == 1) wait_vmcnt<kVmcnt>();
         lds_barrier();
-        // a full tile falls through the guards
+        asm volatile("" : "+s"(nblk));
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (__builtin_expect(i < nblk, 1)) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mma<O::ELEM>(af[i], bf[j], acc[i][j]);
+                for (int j = 0; j < 4; ++j) acc[i][j] = mma<O::ELEM>(bf[j], af[i], acc[i][j]);
             }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -66,78 +119,101 @@ __device__ __attribute__((always_inline)) inline void steps(lds_char* lds, int K
 template <typename O, typename OUT>
 __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__          // the host pass needs the signature only
-    using ACC = typename O::Acc;
     extern __shared__ uint4 smem[];
-    __shared__ int pre[257];
+    __shared__ Groups groups;
     lds_char* lds = (lds_char*)smem;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
-    const int grp = wave >> 2, wn = wave & 3, l16 = lane & 15, lq = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), wm = wave >> 2, wn = wave & 3;
+    const int l16 = lane & 15, lq = lane >> 4;
 
+    const int w = item_of_block(blockIdx.x, gridDim.x);
+    if (w >= count_items<O, kT, kT, OUT>(a, groups)) return;
     Tile2 t;
-    if (!find_tile<O, kT, kT, OUT>(a, pre, t)) return;
+    tile_of_item<O, kT, kT>(a, groups, w, t);
     auto oa = operand_a<O, kT, kLoads>(a, t);
     auto ob = operand_b<O, kT, kLoads>(a, t);
     oa.plan(wave * kLoads, lane, t.ni);
     ob.plan(wave * kLoads, lane, t.nj);
 
-    // rows split evenly over the two groups, in 16-row blocks
-    const int half = min(128, (t.ni + 31) / 32 * 16), row0 = grp * half;
-    const int nblk = max(0, min(half, t.ni - row0) + 15) / 16;
-    ACC acc[8][4];
+    // this wavefront's rows, in 16-row blocks: the tile's, split evenly over the two groups
+    // where one group's products wait for the other's
+    const int half = kApart<O> ? min(128, (t.ni + 31) / 32 * 16) : 128, row0 = uni(wm * half);
+    const int nblk = uni(max(0, min(half, t.ni - row0) + 15) / 16);
+    typename O::Acc acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = ACC{0, 0, 0, 0};
+        for (int j = 0; j < 4; ++j) acc[i][j] = typename O::Acc{0, 0, 0, 0};
 
     const int KT = (t.C + O::kStep - 1) / O::kStep;
     if (KT > 0) {
         const Reader<O::ES, O::kACols, kT> ra(lane);
         const Reader<O::ES, O::kBCols, kT> rb(lane);
+        if constexpr (kApart<O>) {
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
-            oa.load(lds + s * kStage, wave * kLoads, s);
-            ob.load(lds + s * kStage + kT * 64, wave * kLoads, s);
+            for (int s = 0; s < 3; ++s) {
+                oa.load(lds + s * kStage, wave * kLoads, s);
+                ob.load(lds + s * kStage + kT * 64, wave * kLoads, s);
+            }
+            wait_vmcnt<kVmcnt>();
+            lds_barrier();
+            if (wm == 0) steps<O, 0>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
+            else steps<O, 1>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
+        } else {
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) {
+                oa.load(lds + s * kStage, wave * kLoads, s);
+                ob.load(lds + s * kStage + kT * 64, wave * kLoads, s);
+            }
+            wait_vmcnt<3 * 2 * kLoads>();
+            lds_barrier();
+            u32x4_t a0[8], b0[4], a1[8], b1[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a0[i] = ra(lds, wm * 8 + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b0[j] = rb(lds + kT * 64, wn * 4 + j);
+            // two steps a turn (an odd last one multiplies the zeros that its loads read)
+            for (int kt = 0; kt < KT; kt += 2) {
+                lds_char *s0 = lds + (kt & 3) * kStage, *s1 = lds + ((kt + 1) & 3) * kStage, *s2 = lds + ((kt + 2) & 3) * kStage;
+                step<O>(s1, s0, kt + 4, nblk, wm, wn, wave, oa, ob, ra, rb, a0, b0, a1, b1, acc);
+                step<O>(s2, s1, kt + 5, nblk, wm, wn, wave, oa, ob, ra, rb, a1, b1, a0, b0, acc);
+            }
         }
-        wait_vmcnt<kVmcnt>();
-        lds_barrier();
-        if (grp == 0) steps<O, 0>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
-        else steps<O, 1>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the last loads (zeros) land before LDS is reused
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the last loads (zeros) land before LDS is reused
         __syncthreads();
     }
 
-    // epilogue: scales (int8), one rounding, whole rows through LDS
+    // The tile: scales (int8), one rounding.  Lane l holds row l & 15 and columns 4 (l >> 4)
+    // .. + 3 of each 16 x 16 block; bf16 goes out as whole rows through LDS.
     const int J = O::KIND == 1 ? a.K : a.N;
-    float wsc[4] = {1.f, 1.f, 1.f, 1.f};
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) u32x2_t lds_u2;
+    f32x4_t wsc[4];
     if constexpr (O::ELEM == Elem::i8)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int col = wn * 64 + 16 * j + l16;
-            wsc[j] = col < t.nj ? a.ws[(long long)t.e * a.N + t.j0 + col] : 0.f;
+            const int col = wn * 64 + 16 * j + 4 * lq;
+            wsc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (col < t.nj) wsc[j] = *reinterpret_cast<const f32x4_t*>(a.ws + (long long)t.e * a.N + t.j0 + col);
         }
-    typedef __attribute__((address_space(3))) bf16_t lds_bf16;
-    lds_bf16* sC = reinterpret_cast<lds_bf16*>(lds);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (i >= nblk) break;
-        const int r = row0 + 16 * i + 4 * lq;
-        float xsc[4] = {1.f, 1.f, 1.f, 1.f};
-        if constexpr (O::ELEM == Elem::i8)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) xsc[v] = a.xs[t.i0 + min(r + v, t.ni - 1)];
+        const int r = row0 + 16 * i + l16;
+        float xsc = 1.f;
+        if constexpr (O::ELEM == Elem::i8) xsc = r < t.ni ? a.xs[t.i0 + r] : 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int col = wn * 64 + 16 * j + l16;
+            const int col = wn * 64 + 16 * j + 4 * lq;
+            f32x4_t x;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                float val = (float)acc[i][j][v];
-                if constexpr (O::ELEM == Elem::i8) val = val * xsc[v] * wsc[j];
-                if constexpr (sizeof(OUT) == 2) {
-                    sC[(r + v) * kCS + col] = f32_to_bf16(val);
-                } else {
-                    if (r + v < t.ni && col < t.nj) ((float*)a.c)[(t.crow + r + v) * J + t.j0 + col] = val;
-                }
+                x[v] = (float)acc[i][j][v];
+                if constexpr (O::ELEM == Elem::i8) x[v] = x[v] * xsc * wsc[j][v];
             }
+            if constexpr (sizeof(OUT) == 2)
+                *(lds_u2*)(lds + (r * kCS + col) * 2) = u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+            else if (r < t.ni && col < t.nj)
+                *reinterpret_cast<f32x4_t*>((float*)a.c + (t.crow + r) * J + t.j0 + col) = x;
         }
     }
     if constexpr (sizeof(OUT) == 2) {
@@ -145,9 +221,8 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
         for (int c = tid; c < t.ni * 32; c += 512) {
             const int r = c >> 5, cc = (c & 31) * 8;
             if (cc < t.nj)
-                __builtin_nontemporal_store(
-                    *reinterpret_cast<const __attribute__((address_space(3))) u32x4_t*>(sC + r * kCS + cc),
-                    reinterpret_cast<u32x4_t*>((bf16_t*)a.c + (t.crow + r) * J + t.j0 + cc));
+                __builtin_nontemporal_store(*(const __attribute__((address_space(3))) u32x4_t*)(lds + (r * kCS + cc) * 2),
+                                            reinterpret_cast<u32x4_t*>((bf16_t*)a.c + (t.crow + r) * J + t.j0 + cc));
         }
     }
 #endif
@@ -155,10 +230,9 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
 
 template <typename O, typename OUT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
-    auto kern = k_mm<O, OUT>;
-    hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+    hipError_t e = allow_lds<k_mm<O, OUT>>(kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)mm_blocks(a, O::KIND, kT, kT)), dim3(512), kLds, st, a);
+    hipLaunchKernelGGL((k_mm<O, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, kT, kT)), dim3(512), kLds, st, a);
     return hipGetLastError();
 }
 
@@ -174,17 +248,5 @@ hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t
     }
 }
 
-
-hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
-    // TUNING
-    const char* f = getenv("MM_FORM");
-    if (f) {
-        if (f[0] == 'L' && (dtype == MOE_BF16 || kind == 3)) return launch_mm_large(kind, out_dtype, a, st);
-        if (f[0] == 'M') return launch_mm_mid(atoi(f + 1), kind, dtype, out_dtype, a, st);
-        if (f[0] == 'T' && kind != 2) return launch_mm_thin(atoi(f + 2), f[1] - '0', kind, dtype, out_dtype, a, st);
-    }
-    if (dtype == MOE_F32 && kind != 3) return launch_mm_mid(128, kind, dtype, out_dtype, a, st);
-    return launch_mm_large(kind, out_dtype, a, st);
-}
 
 }  // namespace moe

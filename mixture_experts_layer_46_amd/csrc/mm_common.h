@@ -12,36 +12,47 @@ __device__ __forceinline__ void group_rows(const int32_t* __restrict__ offsets, 
     r1 = min(max(offsets[e + 1], r0), rows);
 }
 
-// Row tiles of all groups, without a tile list in memory: pre[e] = tiles of the groups
-// before e (BM rows each), pre[E] = all.  Every workgroup computes it from the offsets (at
-// most 256 groups, four per lane of one wavefront), which saves the launch and the
-// workspace of a list.  Call with all threads; `pre` holds 257 ints of LDS.
-__device__ __forceinline__ void build_row_tiles(const int32_t* __restrict__ offsets, int E, int rows, int BM,
-                                                int* pre) {
+// The groups as every workgroup keeps them in LDS: their rows, and the row tiles before each
+// (pre[e]; pre[E] = all).  Computed from the offsets by every workgroup (at most 256 groups,
+// four per lane of one wavefront), which saves the launch and the workspace of a tile list.
+struct Groups {
+    int r0[256], r1[256], pre[257];
+};
+
+// Fills `g` for tiles of BM rows.  Call with all threads.
+__device__ __forceinline__ void load_groups(const int32_t* __restrict__ offsets, int E, int rows, int BM, Groups& g) {
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
         int n[4], sum = 0;
+        // groups 4 lane .. 4 lane + 3: five offsets, the loads all in flight together
+        int off[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) off[i] = offsets[min(4 * lane + i, E)];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = 4 * lane + i;
-            int r0 = 0, r1 = 0;
-            if (e < E) group_rows(offsets, e, rows, r0, r1);
-            n[i] = (r1 - r0 + BM - 1) / BM;
+            const int e = 4 * lane + i, r0 = min(max(off[i], 0), rows), r1 = min(max(off[i + 1], r0), rows);
+            if (e < E) {
+                g.r0[e] = r0;
+                g.r1[e] = r1;
+            }
+            n[i] = e < E ? (r1 - r0 + BM - 1) / BM : 0;
             sum += n[i];
         }
         int incl = sum;
+        if (E > 3) {                                  // else lane 0 holds them all
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int v = __shfl_up(incl, off);
-            if (lane >= off) incl += v;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(incl, o);
+                if (lane >= o) incl += v;
+            }
         }
         int p = incl - sum;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (4 * lane + i <= E) pre[4 * lane + i] = p;
+            if (4 * lane + i <= E) g.pre[4 * lane + i] = p;
             p += n[i];
         }
-        if (lane == 63 && E == 256) pre[256] = incl;
+        if (lane == 63 && E == 256) g.pre[256] = incl;
     }
     __syncthreads();
 }

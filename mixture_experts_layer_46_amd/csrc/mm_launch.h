@@ -2,6 +2,8 @@
 // `st` and returns the launch status; arguments were checked by the C ABI layer.
 #pragma once
 
+#include <atomic>
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -16,19 +18,35 @@ struct MmArgs {
     int zero_rest;
 };
 
-// kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8
-
+// kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8; in the form that suits the sizes
 hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
-// its forms: 256 x 256 tiles (bf16, int8); tiles of 64 or 128; 16, 32 or 64 rows with the
-// contraction split over 4 or 8 wavefronts (not kind 2)
+// whether a launch can hold the call's workgroups
+bool mm_fits(int kind, int dtype, const MmArgs& a);
+// the forms: 256 x 256 tiles (bf16, int8); tiles of 64 or 128; 16 or 32 rows with the
+// contraction split over 8 or 4 wavefronts (not kind 2)
 hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t st);
 hipError_t launch_mm_mid(int tile, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
-hipError_t launch_mm_thin(int rows, int waves, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
+hipError_t launch_mm_thin(int rows, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
 
 hipError_t launch_quantize_rows(const void* x, int dtype, long long rows, int K, int8_t* q, float* scale,
                                 hipStream_t st);
 hipError_t launch_quantize_experts(const void* w, int dtype, int E, int K, int N, int8_t* q, float* scale,
                                    hipStream_t st);
+
+// Lets kernel KERN use `bytes` of dynamic LDS on the current device (asked of the runtime once
+// per kernel and device).
+template <auto KERN>
+hipError_t allow_lds(size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute((const void*)KERN, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 struct DropArgs {
     uint32_t thr;                 // elements whose 16-bit number is below are dropped (0..65536)

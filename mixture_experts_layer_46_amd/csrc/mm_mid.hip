@@ -30,13 +30,15 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
     using L = Mid<O, BM, BN, S>;
     using ACC = typename O::Acc;
     extern __shared__ uint4 smem[];
-    __shared__ int pre[257];
+    __shared__ Groups groups;
     lds_char* lds = (lds_char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, lq = lane >> 4;
 
     Tile2 t;
-    if (!find_tile<O, BM, BN, OUT>(a, pre, t)) return;
+    const int w = item_of_block(blockIdx.x, gridDim.x);
+    if (w >= count_items<O, BM, BN, OUT>(a, groups)) return;
+    tile_of_item<O, BM, BN>(a, groups, w, t);
     auto oa = operand_a<O, BM, L::NA>(a, t);
     auto ob = operand_b<O, BN, L::NB>(a, t);
     oa.plan(wave * L::NA, lane, t.ni);
@@ -68,12 +70,7 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
             read_and_load<O, BM, BN, 4>(lds + st * L::kStage, lds + nx * L::kStage, kt + S - 1, row0 / 16, wn * L::FN, wave, oa,
                                      ob, ra, rb, af, bf);
             wait_lds();
-#pragma unroll
-            for (int i = 0; i < L::FM; ++i)
-                if (__builtin_expect(i < nblk, 1)) {
-#pragma unroll
-                    for (int j = 0; j < L::FN; ++j) acc[i][j] = mma<O::ELEM>(af[i], bf[j], acc[i][j]);
-                }
+            mma_step<O::ELEM>(af, bf, acc, nblk);
             st = st + 1 == S ? 0 : st + 1;
             nx = nx + 1 == S ? 0 : nx + 1;
         }
@@ -130,11 +127,10 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
 
 template <typename O, int BM, int BN, int S, typename OUT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
-    auto kern = k_mm_mid<O, BM, BN, S, OUT>;
     constexpr size_t lds = Mid<O, BM, BN, S>::kLds;
-    hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipError_t e = allow_lds<k_mm_mid<O, BM, BN, S, OUT>>(lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)mm_blocks(a, O::KIND, BM, BN)), dim3(256), lds, st, a);
+    hipLaunchKernelGGL((k_mm_mid<O, BM, BN, S, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, BM, BN)), dim3(256), lds, st, a);
     return hipGetLastError();
 }
 

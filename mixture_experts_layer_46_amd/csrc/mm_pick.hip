@@ -1,0 +1,109 @@
+// Which form of the grouped products' kernels a call takes (mm.hip, mm_mid.hip, mm_thin.hip).
+//
+// The group sizes stay on the device, so the choice is made from what the host knows: the
+// rows, the groups and the matrix sizes.  Each form's time is estimated as rounds of
+// workgroups over the card's CUs, a round costing a fixed part plus its steps of 64 bytes,
+// each step the larger of its latency when a workgroup is alone and of its share of a full
+// CU; the bytes that every form has to move bound the whole from below.
+//
+// The three constants of a form were fitted to some 5000 random calls (1-256 groups, 1-60000
+// rows, matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every
+// form.  Over those calls the form picked is 3.7% (16- and 8-bit operands), 1.9% (their
+// weight gradient), 4.7% and 1.4% (fp32) slower than the best one in the geometric mean;
+// the best single form would be 25%, 14%, 45% and 2% slower.
+#include <algorithm>
+#include <cmath>
+
+#include "common.h"
+#include "launch.h"
+#include "mm_launch.h"
+
+namespace moe {
+
+namespace {
+
+enum Form { LARGE, MID128, MID64, THIN32, THIN16, FORMS };
+
+struct Shape {
+    int bm, bn;           // tile
+    int per_cu;           // workgroups a CU holds
+    int split;            // wavefronts that share the contraction
+    int threads;
+};
+constexpr Shape kShape[FORMS] = {{256, 256, 1, 1, 512}, {128, 128, 2, 1, 256}, {64, 64, 4, 1, 256}, {32, 64, 2, 4, 256},
+                                 {16, 64, 1, 8, 512}};
+
+struct Cost {
+    double fixed, step, busy;     // us: per workgroup; per step alone; per step and workgroup of a full CU
+};
+// the forms that do not exist (fp32 LARGE, THIN weight gradients) have no cost
+constexpr Cost kRows16[FORMS] = {{3.4, .42, .25}, {2.3, .27, .28}, {2.05, .125, .116}, {2.1, .25, .32}, {2.4, .51, .05}};
+constexpr Cost kWeights16[FORMS] = {{4.8, .70, .31}, {2.6, .43, .29}, {1.7, .23, .117}, {}, {}};
+constexpr Cost kRows32[FORMS] = {{}, {2.1, .69, .55}, {1.66, .33, .21}, {2.5, .53, .55}, {2.6, .68, .22}};
+constexpr Cost kWeights32[FORMS] = {{}, {2.6, .45, 1.34}, {1.4, .47, .31}, {}, {}};
+constexpr double kBytesPerUs = 5.2e6;
+
+const Cost* costs(int kind, int dtype) {
+    const bool f32 = kind != 3 && dtype == MOE_F32;
+    return kind == 2 ? (f32 ? kWeights32 : kWeights16) : (f32 ? kRows32 : kRows16);
+}
+
+long long blocks_of(int kind, const MmArgs& a, const Shape& s) {
+    const long long J = kind == 1 ? a.K : a.N;
+    const long long ni = kind == 2 ? (long long)a.E * ((a.K + s.bm - 1) / s.bm)
+                                   : ((long long)a.rows + s.bm - 1) / s.bm + std::min(a.rows, a.E);
+    return ni * ((J + s.bn - 1) / s.bn);
+}
+
+// A launch holds at most 2^32 threads in a dimension.
+bool fits(int kind, const MmArgs& a, int form) { return blocks_of(kind, a, kShape[form]) * kShape[form].threads < (1ll << 32); }
+
+double estimate(int kind, int dtype, const MmArgs& a, int form) {
+    const Shape& s = kShape[form];
+    const Cost& c = costs(kind, dtype)[form];
+    const int es = kind == 3 ? 1 : dtype == MOE_F32 ? 4 : 2;
+    const double E = a.E, K = a.K, N = a.N, R = std::max(a.rows, 1);
+    const double groups = std::min(E, R), mean = R / groups;             // groups that can have rows
+    const double J = kind == 1 ? K : N, C = kind == 1 ? N : kind == 2 ? mean : K;
+    double tiles;                                                        // expected row tiles
+    if (kind == 2) tiles = E * std::ceil(K / s.bm);
+    else if (a.E == 1) tiles = std::ceil(R / s.bm);
+    else tiles = mean > .75 * s.bm ? groups * std::max(1., mean / s.bm + .5) : groups;
+    const double per_cu = tiles * std::ceil(J / s.bn) / device_cu_count();
+    const double steps = std::ceil(std::ceil(C * es / 64) / s.split);
+    double t;
+    if (per_cu <= s.per_cu) {
+        t = c.fixed + steps * std::max(c.step, std::ceil(per_cu) * c.busy);
+    } else {
+        const double r = per_cu / s.per_cu;
+        t = (r < 2 ? 2 : r + .4) * (c.fixed + steps * std::max(c.step, s.per_cu * c.busy));
+    }
+    const double bytes = (R * K + R * N) * es + (kind == 2 ? E : groups) * K * N * es, m = bytes / kBytesPerUs;
+    return std::max(t, m) + .2 * std::min(t, m);
+}
+
+}  // namespace
+
+bool mm_fits(int kind, int dtype, const MmArgs& a) {
+    return fits(kind, a, kind != 3 && dtype == MOE_F32 ? MID128 : LARGE);
+}
+
+hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
+    int best = -1;
+    double t_best = 0;
+    for (int f = 0; f < FORMS; ++f) {
+        if (costs(kind, dtype)[f].fixed == 0 || !fits(kind, a, f)) continue;
+        const double t = estimate(kind, dtype, a, f);
+        if (best < 0 || t < t_best) best = f, t_best = t;
+    }
+    switch (best) {
+        case LARGE: return launch_mm_large(kind, out_dtype, a, st);
+        case MID128: return launch_mm_mid(128, kind, dtype, out_dtype, a, st);
+        case MID64: return launch_mm_mid(64, kind, dtype, out_dtype, a, st);
+        case THIN32: return launch_mm_thin(32, kind, dtype, out_dtype, a, st);
+        case THIN16: return launch_mm_thin(16, kind, dtype, out_dtype, a, st);
+    }
+    return hipErrorInvalidConfiguration;                                  // mm_fits refuses such calls before
+}
+
+}  // namespace moe

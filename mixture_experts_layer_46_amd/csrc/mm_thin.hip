@@ -1,4 +1,4 @@
-// Grouped products with few rows per group (kinds 0, 1 and 3 of mm_tile.h): 16, 32 or 64
+// Grouped products with few rows per group (kinds 0, 1 and 3 of mm_tile.h): 16 or 32
 // rows by 64 columns, the contraction split over the workgroup's wavefronts.
 //
 // Such products stream the matrices once and do little else, so what counts is the bytes in
@@ -50,12 +50,14 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
     using L = Thin<RB, W, S>;
     using ACC = typename O::Acc;
     extern __shared__ uint4 smem[];
-    __shared__ int pre[257];
+    __shared__ Groups groups;
     lds_char* lds = (lds_char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), l16 = lane & 15, lq = lane >> 4;
 
     Tile2 t;
-    if (!find_tile<O, L::BM, kBN, OUT>(a, pre, t)) return;
+    const int w = item_of_block(blockIdx.x, gridDim.x);
+    if (w >= count_items<O, L::BM, kBN, OUT>(a, groups)) return;
+    tile_of_item<O, L::BM, kBN>(a, groups, w, t);
     auto oa = operand_a<O, L::BM, L::NA>(a, t);
     auto ob = operand_b<O, kBN, L::NB>(a, t);
     oa.plan(0, lane, t.ni);
@@ -79,10 +81,7 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
     for (int kt = wave; kt < KT; kt += W) {
         u32x4_t af[RB], bf[4];
         load_and_read<O, RB, W, S>(ring + st * L::kStage, ring + nx * L::kStage, kt + (S - 1) * W, oa, ob, ra, rb, af, bf);
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mma<O::ELEM>(af[i], bf[j], acc[i][j]);
+        mma_step<O::ELEM>(af, bf, acc, RB);
         st = st + 1 == S ? 0 : st + 1;
         nx = nx + 1 == S ? 0 : nx + 1;
     }
@@ -141,11 +140,10 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
 
 template <typename O, int RB, int W, int S, typename OUT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
-    auto kern = k_mm_thin<O, RB, W, S, OUT>;
     constexpr size_t lds = Thin<RB, W, S>::kLds;
-    hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipError_t e = allow_lds<k_mm_thin<O, RB, W, S, OUT>>(lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)mm_blocks(a, O::KIND, 16 * RB, kBN)), dim3(W * 64), lds, st, a);
+    hipLaunchKernelGGL((k_mm_thin<O, RB, W, S, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, 16 * RB, kBN)), dim3(W * 64), lds, st, a);
     return hipGetLastError();
 }
 
@@ -161,16 +159,11 @@ hipError_t go_kind(int kind, int dtype, int out_dtype, const MmArgs& a, hipStrea
 
 }  // namespace
 
-// Stages: as many as leave room for a second workgroup on the CU (four wavefronts), or as
-// fit (eight).
-hipError_t launch_mm_thin(int rows, int waves, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
-    if (waves == 4)
-        return rows == 16   ? go_kind<1, 4, 4>(kind, dtype, out_dtype, a, st)
-               : rows == 32 ? go_kind<2, 4, 3>(kind, dtype, out_dtype, a, st)
-                            : go_kind<4, 4, 3>(kind, dtype, out_dtype, a, st);
-    return rows == 16   ? go_kind<1, 8, 3>(kind, dtype, out_dtype, a, st)
-           : rows == 32 ? go_kind<2, 8, 3>(kind, dtype, out_dtype, a, st)
-                        : go_kind<4, 8, 2>(kind, dtype, out_dtype, a, st);
+// 16 rows: eight wavefronts, for the fewest workgroups; 32 rows: four, and two workgroups a
+// CU.  Three stages each.  Measured against 16 rows with four wavefronts and 64 rows with
+// four or eight, which no rule on the sizes made pay.
+hipError_t launch_mm_thin(int rows, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
+    return rows == 16 ? go_kind<1, 8, 3>(kind, dtype, out_dtype, a, st) : go_kind<2, 4, 3>(kind, dtype, out_dtype, a, st);
 }
 
 }  // namespace moe

@@ -157,17 +157,37 @@ struct Reader {
 
 template <Elem E, typename ACC>
 __device__ __forceinline__ ACC mma(u32x4_t a, u32x4_t b, ACC c) {
-    if constexpr (E == Elem::bf16) {
+    if constexpr (E == Elem::bf16)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
                                                        c, 0, 0, 0);
-    } else if constexpr (E == Elem::i8) {
+    else
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0,
                                                      0, 0);
+}
+
+// One step's products of a wavefront: its first `nblk` row blocks (a full tile falls through
+// the guards).  fp32 takes four instructions per pair of blocks, which follow each other
+// only after every other pair's, so that none waits for the one before it.
+template <Elem E, typename ACC, int FM, int FN>
+__device__ __forceinline__ void mma_step(const u32x4_t (&af)[FM], const u32x4_t (&bf)[FN], ACC (&acc)[FM][FN], int nblk) {
+    if constexpr (E == Elem::f32) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                if (__builtin_expect(i < nblk, 1)) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(af[i][s]), __uint_as_float(bf[j][s]),
+                                                                         acc[i][j], 0, 0, 0);
+                }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
-        return c;
+        for (int i = 0; i < FM; ++i)
+            if (__builtin_expect(i < nblk, 1)) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mma<E>(af[i], bf[j], acc[i][j]);
+            }
     }
 }
 
@@ -189,8 +209,8 @@ __device__ __attribute__((always_inline)) inline void read_and_load(const lds_ch
     ob.load(wr + TA * 64, wave * (TB / 16 / W), kt);
 }
 
-// Work item of a workgroup.  Workgroups are dealt to the eight XCDs in turn; 32 consecutive
-// items go to one XCD, so that the tiles they share meet in its L2.
+// Work item of block b of a grid of `grid` blocks.  Workgroups are dealt to the eight XCDs in
+// turn; 32 consecutive items go to one XCD, so that the tiles they share meet in its L2.
 __device__ __forceinline__ int item_of_block(int b, int grid) {
     return b < (grid & ~255) ? (b & ~255) | ((b & 7) << 5) | ((b >> 3) & 31) : b;
 }
@@ -211,13 +231,26 @@ struct Tile2 {
     uint64_t abase, bbase;        // first bytes of the operands
 };
 
-// Returns false when there is no item w.  Group rows are cut evenly: a group of r rows gets
-// ceil(r / BM) tiles of about r / tiles rows each, in multiples of 16 (a group a little
-// above a multiple of BM then has no nearly empty tile).
+// Work items of a launch (all its tiles); fills `g` and, if asked, zeros the rows of no group.
+// Call with all threads.
 template <typename O, int BM, int BN, typename OUT>
-__device__ __forceinline__ bool find_tile(const MmArgs& a, int* pre, Tile2& t) {
+__device__ __forceinline__ int count_items(const MmArgs& a, Groups& g) {
     const int J = O::KIND == 1 ? a.K : a.N, NJ = (J + BN - 1) / BN;
-    const int w = item_of_block(blockIdx.x, gridDim.x);
+    if constexpr (O::KIND == 2) {
+        return a.E * ((a.K + BM - 1) / BM) * NJ;             // the tiles of every expert's matrix, rows or not
+    } else {
+        load_groups(a.offsets, a.E, a.rows, BM, g);
+        if (a.zero_rest) zero_rest(a.offsets, a.E, a.rows, a.c, (long long)J * sizeof(OUT), blockIdx.x, gridDim.x);
+        return uni(g.pre[a.E]) * NJ;
+    }
+}
+
+// Tile of work item w.  Group rows are cut evenly: a group of r rows gets ceil(r / BM) tiles
+// of about r / tiles rows each, in multiples of 16 (a group a little above a multiple of BM
+// then has no nearly empty tile).  64 experts of 256 +- 16 rows, 2048 -> 1408: 180 -> 166 us.
+template <typename O, int BM, int BN>
+__device__ __forceinline__ void tile_of_item(const MmArgs& a, const Groups& g, int w, Tile2& t) {
+    const int J = O::KIND == 1 ? a.K : a.N, NJ = (J + BN - 1) / BN;
     int it, jt, r0, r1;
     if constexpr (O::KIND == 2) {
         const int NI = (a.K + BM - 1) / BM;
@@ -225,21 +258,20 @@ __device__ __forceinline__ bool find_tile(const MmArgs& a, int* pre, Tile2& t) {
         tile_coords(w - t.e * NI * NJ, NI, NJ, it, jt);
         group_rows(a.offsets, t.e, a.rows, r0, r1);
         r0 = uni(r0);
+        r1 = uni(r1);
         t.i0 = uni(it * BM);
         t.j0 = uni(jt * BN);
         t.ni = min(BM, a.K - t.i0);
-        t.C = uni(r1) - r0;
+        t.C = r1 - r0;
         t.crow = (long long)t.e * a.K + t.i0;
         t.abase = (uint64_t)a.a + ((uint64_t)r0 * a.K + t.i0) * O::ES;
         t.bbase = (uint64_t)a.b + ((uint64_t)r0 * a.N + t.j0) * O::ES;
     } else {
-        build_row_tiles(a.offsets, a.E, a.rows, BM, pre);
-        if (a.zero_rest) zero_rest(a.offsets, a.E, a.rows, a.c, (long long)J * sizeof(OUT), blockIdx.x, gridDim.x);
-        if (w >= (long long)pre[a.E] * NJ) return false;
-        t.e = uni(group_of_tile(pre, a.E, w / NJ));
-        const int p0 = pre[t.e], tiles = pre[t.e + 1] - p0;
+        t.e = uni(group_of_tile(g.pre, a.E, w / NJ));
+        const int p0 = uni(g.pre[t.e]), tiles = uni(g.pre[t.e + 1]) - p0;
         tile_coords(w - p0 * NJ, tiles, NJ, it, jt);
-        group_rows(a.offsets, t.e, a.rows, r0, r1);
+        r0 = uni(g.r0[t.e]);
+        r1 = uni(g.r1[t.e]);
         const int h = ((r1 - r0 + tiles - 1) / tiles + 15) / 16 * 16;       // at most BM
         t.i0 = uni(min(r0 + it * h, r1));
         t.j0 = uni(jt * BN);
@@ -253,7 +285,6 @@ __device__ __forceinline__ bool find_tile(const MmArgs& a, int* pre, Tile2& t) {
     t.abase = uni(t.abase);
     t.bbase = uni(t.bbase);
     t.nj = min(BN, J - t.j0);
-    return true;
 }
 
 template <typename O, int T, int N>

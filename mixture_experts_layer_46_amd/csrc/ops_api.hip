@@ -104,9 +104,12 @@ moe_status check_ld(int64_t ld, int32_t F, const char* name) {
     return MOE_OK;
 }
 
-// kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8
-hipError_t run_mm(int kind, const moe_mm_shape& s, const MmArgs& a, hipStream_t st) {
-    return launch_mm(kind, s.dtype, s.out_dtype, a, st);
+moe_status run_mm(int kind, const moe_mm_shape& s, const MmArgs& a, hipStream_t st, const char* where) {
+    if (!mm_fits(kind, s.dtype, a))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: too many output tiles for one launch (rows=%lld E=%d K=%d N=%d)", where,
+                    (long long)s.rows, s.E, s.K, s.N);
+    HIPCHK(launch_mm(kind, s.dtype, s.out_dtype, a, st), where);
+    return MOE_OK;
 }
 
 }  // namespace
@@ -125,8 +128,7 @@ moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, const void* 
     REQ(w, "w");
     REQ(offsets, "offsets");
     REQ(y, "y");
-    HIPCHK(run_mm(0, *shape, mm_args(*shape, x, w, y, offsets), stream), "grouped_mm");
-    return MOE_OK;
+    return run_mm(0, *shape, mm_args(*shape, x, w, y, offsets), stream, "grouped_mm");
 }
 
 moe_status moe_grouped_mm_dx(const moe_mm_shape* shape, const void* dy, const void* w, const int32_t* offsets, void* dx,
@@ -137,9 +139,7 @@ moe_status moe_grouped_mm_dx(const moe_mm_shape* shape, const void* dy, const vo
     REQ(w, "w");
     REQ(offsets, "offsets");
     REQ(dx, "dx");
-    HIPCHK(run_mm(1, *shape, mm_args(*shape, dy, w, dx, offsets), stream),
-           "grouped_mm_dx");
-    return MOE_OK;
+    return run_mm(1, *shape, mm_args(*shape, dy, w, dx, offsets), stream, "grouped_mm_dx");
 }
 
 moe_status moe_grouped_mm_dw(const moe_mm_shape* shape, const void* x, const void* dy, const int32_t* offsets, void* dw,
@@ -151,9 +151,7 @@ moe_status moe_grouped_mm_dw(const moe_mm_shape* shape, const void* x, const voi
     }
     REQ(offsets, "offsets");
     REQ(dw, "dw");
-    HIPCHK(run_mm(2, *shape, mm_args(*shape, x, dy, dw, offsets), stream),
-           "grouped_mm_dw");
-    return MOE_OK;
+    return run_mm(2, *shape, mm_args(*shape, x, dy, dw, offsets), stream, "grouped_mm_dw");
 }
 
 moe_status moe_quantize_rows(int32_t dtype, int64_t rows, int32_t K, const void* x, int8_t* q, float* scale,
@@ -196,8 +194,7 @@ moe_status moe_grouped_mm_int8(const moe_mm_shape* shape, const int8_t* xq, cons
     MmArgs a = mm_args(*shape, xq, wq, y, offsets);
     a.xs = x_scale;
     a.ws = w_scale;
-    HIPCHK(run_mm(3, *shape, a, stream), "grouped_mm_int8");
-    return MOE_OK;
+    return run_mm(3, *shape, a, stream, "grouped_mm_int8");
 }
 
 moe_status moe_dropout(int32_t dtype, int64_t n, const moe_dropout_spec* spec, const void* x, void* y,

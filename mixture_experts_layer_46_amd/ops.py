@@ -54,7 +54,7 @@ def _check(t, name, dtype, shape):
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -79,8 +79,9 @@ def _device(dev):
     return _NULL_CONTEXT if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _stream(dev) -> int:
+    """The current stream of device `dev` (its handle alone: a Stream object costs microseconds)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _dims(t, n, name):
@@ -108,9 +109,9 @@ def _mm(x, w, offsets, out, transposed, xname, oname):
         _check(out, oname, x.dtype, (R, cout))
     with _place(**{xname: x, "w": w, "offsets": offsets, oname: out}):
         if out is None:
-            out = torch.empty((R, cout), dtype=x.dtype, device=x.device)
+            out = x.new_empty((R, cout))
         _lib.call("moe_grouped_mm_dx" if transposed else "moe_grouped_mm", _mm_shape(R, E, K, N, code, code, rest),
-                  x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream())
+                  x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream(x.device))
     return out
 
 
@@ -172,7 +173,7 @@ def grouped_mm_dw(x, dy, offsets, out=None, dtype=None):
         if out is None:
             out = torch.empty((E, K, N), dtype=dtype, device=x.device)
         _lib.call("moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
-                  offsets.data_ptr(), out.data_ptr(), _stream())
+                  offsets.data_ptr(), out.data_ptr(), _stream(x.device))
     return out
 
 
@@ -187,7 +188,7 @@ def quantize_rows(x):
     with _place(x=x):
         q = torch.empty((R, K), dtype=torch.int8, device=x.device)
         scale = torch.empty(R, dtype=torch.float32, device=x.device)
-        _lib.call("moe_quantize_rows", code, R, K, x.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream())
+        _lib.call("moe_quantize_rows", code, R, K, x.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream(x.device))
     return q, scale
 
 
@@ -200,7 +201,7 @@ def quantize_experts(w):
     with _place(w=w):
         q = torch.empty((E, N, K), dtype=torch.int8, device=w.device)
         scale = torch.empty((E, N), dtype=torch.float32, device=w.device)
-        _lib.call("moe_quantize_experts", code, E, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream())
+        _lib.call("moe_quantize_experts", code, E, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream(w.device))
     return q, scale
 
 
@@ -230,7 +231,7 @@ def grouped_mm_int8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out
         if out is None:
             out = torch.empty((R, N), dtype=dtype, device=xq.device)
         _lib.call("moe_grouped_mm_int8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
-                  x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream())
+                  x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream(xq.device))
     return out
 
 
@@ -255,7 +256,7 @@ def _dropout(x, p, seed, step, out):
         if out is None:
             out = torch.empty_like(x)
         _lib.call("moe_dropout", code, x.numel(), _spec(p, seed, step, x.device), x.data_ptr(), out.data_ptr(),
-                  _stream())
+                  _stream(x.device))
     return out
 
 
@@ -330,9 +331,9 @@ def _gated_act(a, b, p, seed, step, out):
             raise ValueError(f"out is on {out.device}, a on {a.device}")
     with _device(a.device):
         if out is None:
-            out = torch.empty((R, F), dtype=a.dtype, device=a.device)
+            out = a.new_empty((R, F))
         _lib.call("moe_gated_act", code, R, F, _spec(p, seed, step, a.device), a.data_ptr(), lda,
-                  None if b is None else b.data_ptr(), ldb, out.data_ptr(), _stream())
+                  None if b is None else b.data_ptr(), ldb, out.data_ptr(), _stream(a.device))
     return out
 
 
@@ -373,8 +374,8 @@ def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
         raise ValueError(f"dh is on {dh.device}, a on {a.device}")
     with _device(a.device):
         if out is None:
-            da = torch.empty((R, F), dtype=a.dtype, device=a.device)
-            db = None if b is None else torch.empty((R, F), dtype=a.dtype, device=a.device)
+            da = a.new_empty((R, F))
+            db = None if b is None else a.new_empty((R, F))
         else:
             da, db = out
             _check(da, "da", a.dtype, (R, F))
@@ -387,7 +388,7 @@ def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
                     raise ValueError(f"{name} is on {t.device}, a on {a.device}")
         _lib.call("moe_gated_act_grad", code, R, F, _spec(p, seed, step, a.device), dh.data_ptr(), a.data_ptr(), lda,
                   None if b is None else b.data_ptr(), ldb, da.data_ptr(), _row_stride(da, "da"),
-                  None if db is None else db.data_ptr(), 0 if db is None else _row_stride(db, "db"), _stream())
+                  None if db is None else db.data_ptr(), 0 if db is None else _row_stride(db, "db"), _stream(a.device))
     return da, db
 
 
@@ -406,10 +407,10 @@ def combine_grad(dout, y_perm, row_of_pair, topk_w):
     _check(topk_w, "topk_w", torch.float32, (T, k))
     _check(row_of_pair, "row_of_pair", torch.int32, (T * k,))
     with _place(dout=dout, y_perm=y_perm, row_of_pair=row_of_pair, topk_w=topk_w):
-        dy = torch.empty((R, H), dtype=dout.dtype, device=dout.device)
+        dy = torch.empty_like(y_perm)
         dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
         _lib.call("moe_combine_grad", code, T, k, H, R, dout.data_ptr(), y_perm.data_ptr(), row_of_pair.data_ptr(),
-                  topk_w.data_ptr(), dy.data_ptr(), dw.data_ptr(), _stream())
+                  topk_w.data_ptr(), dy.data_ptr(), dw.data_ptr(), _stream(dout.device))
     return dy, dw
 
 
