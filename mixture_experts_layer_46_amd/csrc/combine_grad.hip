@@ -29,14 +29,16 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
         return uint4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
 }
 
-template <bool BF16>
+// P threads per token: a workgroup, or for short rows one wavefront (4 tokens a workgroup).
+template <bool BF16, int P>
 __global__ __launch_bounds__(256) void k_combine_grad(const uint4* __restrict__ dout, const uint4* __restrict__ y,
                                                       const int32_t* __restrict__ row_of_pair,
                                                       const float* __restrict__ w, uint4* __restrict__ dy,
-                                                      float* __restrict__ dw, int k, int chunks, int rows) {
+                                                      float* __restrict__ dw, long long T, int k, int chunks, int rows) {
     constexpr int NV = BF16 ? 8 : 4;
-    const long long t = blockIdx.x;
     __shared__ float part[4][8];
+    const long long t = (long long)blockIdx.x * (256 / P) + threadIdx.x / P;
+    if (P == 64 && t >= T) return;                     // a whole wavefront
     int row[8];
     float g[8], dot[8];
 #pragma unroll
@@ -46,7 +48,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(const uint4* __restrict__ 
         g[j] = j < k ? w[t * k + j] : 0.f;
         dot[j] = 0.f;
     }
-    for (int c = threadIdx.x; c < chunks; c += 256) {
+    for (int c = threadIdx.x % P; c < chunks; c += P) {
         float d[8];
         unpack<BF16>(dout[t * chunks + c], d);
         uint4 v[8];
@@ -69,15 +71,33 @@ __global__ __launch_bounds__(256) void k_combine_grad(const uint4* __restrict__ 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+        if (j >= k) break;
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) dot[j] += __shfl_xor(dot[j], off);
-        if (lane == 0) part[wave][j] = dot[j];
+        if constexpr (P > 64) {
+            if (lane == 0) part[wave][j] = dot[j];
+        } else {
+            if (lane == j) dw[t * k + j] = dot[j];
+        }
     }
-    __syncthreads();
-    if ((int)threadIdx.x < k) {
-        const int j = threadIdx.x;
-        dw[t * k + j] = ((part[0][j] + part[1][j]) + part[2][j]) + part[3][j];
+    if constexpr (P > 64) {
+        __syncthreads();
+        if ((int)threadIdx.x < k) {
+            const int j = threadIdx.x;
+            dw[t * k + j] = ((part[0][j] + part[1][j]) + part[2][j]) + part[3][j];
+        }
     }
+}
+
+template <bool BF16>
+void go(const void* dout, const void* y_perm, const int32_t* row_of_pair, const float* w, void* dy_perm, float* dw,
+        long long T, int k, int chunks, long long rows, hipStream_t st) {
+    if (chunks <= 128)
+        hipLaunchKernelGGL((k_combine_grad<BF16, 64>), dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, (const uint4*)dout,
+                           (const uint4*)y_perm, row_of_pair, w, (uint4*)dy_perm, dw, T, k, chunks, (int)rows);
+    else
+        hipLaunchKernelGGL((k_combine_grad<BF16, 256>), dim3((unsigned)T), dim3(256), 0, st, (const uint4*)dout,
+                           (const uint4*)y_perm, row_of_pair, w, (uint4*)dy_perm, dw, T, k, chunks, (int)rows);
 }
 
 }  // namespace
@@ -85,12 +105,8 @@ __global__ __launch_bounds__(256) void k_combine_grad(const uint4* __restrict__ 
 hipError_t launch_combine_grad(const void* dout, const void* y_perm, const int32_t* row_of_pair, const float* w,
                                void* dy_perm, float* dw, long long T, int k, int H, int dtype, long long rows,
                                hipStream_t st) {
-    if (dtype == MOE_BF16)
-        hipLaunchKernelGGL(k_combine_grad<true>, dim3((unsigned)T), dim3(256), 0, st, (const uint4*)dout,
-                           (const uint4*)y_perm, row_of_pair, w, (uint4*)dy_perm, dw, k, H / 8, (int)rows);
-    else
-        hipLaunchKernelGGL(k_combine_grad<false>, dim3((unsigned)T), dim3(256), 0, st, (const uint4*)dout,
-                           (const uint4*)y_perm, row_of_pair, w, (uint4*)dy_perm, dw, k, H / 4, (int)rows);
+    if (dtype == MOE_BF16) go<true>(dout, y_perm, row_of_pair, w, dy_perm, dw, T, k, H / 8, rows, st);
+    else go<false>(dout, y_perm, row_of_pair, w, dy_perm, dw, T, k, H / 4, rows, st);
     return hipGetLastError();
 }
 

@@ -6,11 +6,11 @@
 // each step the larger of its latency when a workgroup is alone and of its share of a full
 // CU; the bytes that every form has to move bound the whole from below.
 //
-// The three constants of a form were fitted to some 5000 random calls (1-256 groups, 1-60000
-// rows, matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every
-// form.  Over those calls the form picked is 3.7% (16- and 8-bit operands), 1.9% (their
-// weight gradient), 4.7% and 1.4% (fp32) slower than the best one in the geometric mean;
-// the best single form would be 25%, 14%, 45% and 2% slower.
+// The three constants of a form come from some 5000 random calls (1-256 groups, 1-60000 rows,
+// matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every form.
+// Over those calls the form picked is 3.4% (16- and 8-bit operands), 1.7% (their weight
+// gradient), 4.0% and 1.3% (fp32) slower than the best one in the geometric mean; the best
+// single form would be 25%, 14%, 45% and 2% slower.
 #include <algorithm>
 #include <cmath>
 
@@ -37,10 +37,10 @@ struct Cost {
     double fixed, step, busy;     // us: per workgroup; per step alone; per step and workgroup of a full CU
 };
 // the forms that do not exist (fp32 LARGE, THIN weight gradients) have no cost
-constexpr Cost kRows16[FORMS] = {{3.4, .42, .25}, {2.3, .27, .28}, {2.05, .125, .116}, {2.1, .25, .32}, {2.4, .51, .05}};
-constexpr Cost kWeights16[FORMS] = {{4.8, .70, .31}, {2.6, .43, .29}, {1.7, .23, .117}, {}, {}};
-constexpr Cost kRows32[FORMS] = {{}, {2.1, .69, .55}, {1.66, .33, .21}, {2.5, .53, .55}, {2.6, .68, .22}};
-constexpr Cost kWeights32[FORMS] = {{}, {2.6, .45, 1.34}, {1.4, .47, .31}, {}, {}};
+constexpr Cost kRows16[FORMS] = {{3.4, .42, .85}, {2.3, .33, .29}, {2.05, .14, .121}, {2.1, .25, .32}, {2.4, .51, .05}};
+constexpr Cost kWeights16[FORMS] = {{4.8, .70, .90}, {2.6, .56, .32}, {1.6, .23, .141}, {}, {}};
+constexpr Cost kRows32[FORMS] = {{}, {2.1, .95, .95}, {1.66, .33, .25}, {2.5, .53, .55}, {2.6, .68, .22}};
+constexpr Cost kWeights32[FORMS] = {{}, {1.63, .45, 1.09}, {1.0, .47, .244}, {}, {}};
 constexpr double kBytesPerUs = 5.2e6;
 
 const Cost* costs(int kind, int dtype) {

@@ -92,6 +92,7 @@ struct Operand {
                 const int pos = j * 1024 + lane * 16, k = pos / kRowB;
                 int c = (pos % kRowB) / 16;
                 if constexpr (ES == 2) c ^= 2 * blk_swz<kRowB>(k);
+                else c ^= 4 * ((k >> 2) & 3);
                 off[i] = c * (16 / ES) < valid ? (uint32_t)k * ld + (uint32_t)c * 16 : kOOB;
             } else {
                 const int r = j * 16 + (lane >> 2), q = (lane & 3) ^ swa4(r);
@@ -131,6 +132,8 @@ struct Reader {
             g = blk_swz<kRowB>(8 * lq + (l16 >> 2));          // the same for the rows of the second read, 4 further
             rd = (8 * lq + (l16 >> 2)) * kRowB + ((l16 & 3) << 3);
         } else if constexpr (COLS) {
+            static_assert(T % 64 == 0, "blocks trade places in fours");
+            g = lq;
             rd = 4 * lq * kRowB + l16 * 4;
         } else {
             rd = l16 * 64 + ((lq ^ swa4(l16)) << 4);
@@ -147,7 +150,7 @@ struct Reader {
             return __builtin_bit_cast(u32x4_t, v);
         } else if constexpr (COLS) {
             const __attribute__((address_space(3))) uint32_t* p =
-                (const __attribute__((address_space(3))) uint32_t*)(stage + rd + blk * 64);
+                (const __attribute__((address_space(3))) uint32_t*)(stage + rd + ((blk & ~3) | ((blk & 3) ^ g)) * 64);
             return u32x4_t{p[0], p[kRowB / 4], p[2 * (kRowB / 4)], p[3 * (kRowB / 4)]};
         } else {
             return *(const __attribute__((address_space(3))) u32x4_t*)(stage + rd + blk * 1024);
