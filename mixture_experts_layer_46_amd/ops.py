@@ -24,8 +24,8 @@ as everywhere in torch.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -39,7 +39,6 @@ __all__ = ["grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "grouped_mm_int8", "q
            "grouped_ffn_int8", "forward_int8", "forward_train"]
 
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-_NULL_CONTEXT = contextlib.nullcontext()
 
 
 def _code(t: torch.Tensor, name: str) -> int:
@@ -58,30 +57,43 @@ def _check(t, name, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _place(**ts):
-    """All on one GPU and contiguous; returns a context that makes it the current device."""
+def _on(t, name, dev):
+    """t's GPU; raises unless it is `dev` (None: any)."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be on the GPU (there is no CPU path)")
+    if dev is not None and d != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
+    return d
+
+
+def _dense(t, name, dev=None):
+    """t's GPU; raises unless it is `dev` (None: any) and t is contiguous."""
+    d = _on(t, name, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return d
+
+
+def _launch(dev, name, *args):
+    """One operator on the current stream of GPU `dev` (the stream's handle alone: a Stream
+    object costs microseconds), which need not be the current device."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        _lib.call(name, *args, stream)
+    else:
+        with torch.cuda.device(dev):
+            _lib.call(name, *args, stream)
+
+
+def _current(**ts):
+    """A context with the tensors' GPU as the current device (the layer's own stages want that);
+    raises unless all are dense on one GPU."""
     dev = None
     for name, t in ts.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on the GPU (there is no CPU path)")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
-    return _device(dev)
-
-
-def _device(dev):
-    return _NULL_CONTEXT if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _stream(dev) -> int:
-    """The current stream of device `dev` (its handle alone: a Stream object costs microseconds)."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+        if t is not None:
+            dev = _dense(t, name, dev)
+    return torch.cuda.device(dev)
 
 
 def _dims(t, n, name):
@@ -89,7 +101,9 @@ def _dims(t, n, name):
         raise ValueError(f"{name} must be a tensor of {n} dimensions")
 
 
+@functools.lru_cache(maxsize=512)
 def _mm_shape(rows, E, K, N, dtype, out_dtype, rest):
+    """The C struct of a product's sizes (read only; kept, since making one costs a microsecond)."""
     return ctypes.byref(MmShape(rows, E, K, N, dtype, out_dtype, MOE_MM_ZERO_REST if rest else 0))
 
 
@@ -105,13 +119,17 @@ def _mm(x, w, offsets, out, transposed, xname, oname):
     _check(w, "w", x.dtype, (E, K, N))
     _check(offsets, "offsets", torch.int32, (E + 1,))
     rest = out is None
-    if out is not None:
+    if not rest:
         _check(out, oname, x.dtype, (R, cout))
-    with _place(**{xname: x, "w": w, "offsets": offsets, oname: out}):
-        if out is None:
-            out = x.new_empty((R, cout))
-        _lib.call("moe_grouped_mm_dx" if transposed else "moe_grouped_mm", _mm_shape(R, E, K, N, code, code, rest),
-                  x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream(x.device))
+    dev = _dense(x, xname)
+    _dense(w, "w", dev)
+    _dense(offsets, "offsets", dev)
+    if rest:
+        out = x.new_empty((R, cout))
+    else:
+        _dense(out, oname, dev)
+    _launch(dev, "moe_grouped_mm_dx" if transposed else "moe_grouped_mm", _mm_shape(R, E, K, N, code, code, rest),
+            x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
 
@@ -169,11 +187,15 @@ def grouped_mm_dw(x, dy, offsets, out=None, dtype=None):
         raise ValueError(f"dtype must be {x.dtype} or torch.float32, got {dtype}")
     if out is not None:
         _check(out, "out", dtype, (E, K, N))
-    with _place(x=x, dy=dy, offsets=offsets, out=out):
-        if out is None:
-            out = torch.empty((E, K, N), dtype=dtype, device=x.device)
-        _lib.call("moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
-                  offsets.data_ptr(), out.data_ptr(), _stream(x.device))
+    dev = _dense(x, "x")
+    _dense(dy, "dy", dev)
+    _dense(offsets, "offsets", dev)
+    if out is None:
+        out = torch.empty((E, K, N), dtype=dtype, device=x.device)
+    else:
+        _dense(out, "out", dev)
+    _launch(dev, "moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
+            offsets.data_ptr(), out.data_ptr())
     return out
 
 
@@ -185,10 +207,10 @@ def quantize_rows(x):
     _dims(x, 2, "x")
     code = _code(x, "x")
     R, K = x.shape
-    with _place(x=x):
-        q = torch.empty((R, K), dtype=torch.int8, device=x.device)
-        scale = torch.empty(R, dtype=torch.float32, device=x.device)
-        _lib.call("moe_quantize_rows", code, R, K, x.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream(x.device))
+    dev = _dense(x, "x")
+    q = torch.empty((R, K), dtype=torch.int8, device=x.device)
+    scale = torch.empty(R, dtype=torch.float32, device=x.device)
+    _launch(dev, "moe_quantize_rows", code, R, K, x.data_ptr(), q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -198,10 +220,10 @@ def quantize_experts(w):
     _dims(w, 3, "w")
     code = _code(w, "w")
     E, K, N = w.shape
-    with _place(w=w):
-        q = torch.empty((E, N, K), dtype=torch.int8, device=w.device)
-        scale = torch.empty((E, N), dtype=torch.float32, device=w.device)
-        _lib.call("moe_quantize_experts", code, E, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream(w.device))
+    dev = _dense(w, "w")
+    q = torch.empty((E, N, K), dtype=torch.int8, device=w.device)
+    scale = torch.empty((E, N), dtype=torch.float32, device=w.device)
+    _launch(dev, "moe_quantize_experts", code, E, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -222,16 +244,22 @@ def grouped_mm_int8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out
     _check(w_scale, "w_scale", torch.float32, (E, N))
     _check(offsets, "offsets", torch.int32, (E + 1,))
     rest = out is None
-    if out is not None:
+    if not rest:
         dtype = out.dtype
         _check(out, "out", dtype, (R, N))
     if dtype not in _CODES:
         raise TypeError(f"unsupported output type {dtype}")
-    with _place(xq=xq, x_scale=x_scale, wq=wq, w_scale=w_scale, offsets=offsets, out=out):
-        if out is None:
-            out = torch.empty((R, N), dtype=dtype, device=xq.device)
-        _lib.call("moe_grouped_mm_int8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
-                  x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream(xq.device))
+    dev = _dense(xq, "xq")
+    _dense(x_scale, "x_scale", dev)
+    _dense(wq, "wq", dev)
+    _dense(w_scale, "w_scale", dev)
+    _dense(offsets, "offsets", dev)
+    if rest:
+        out = torch.empty((R, N), dtype=dtype, device=xq.device)
+    else:
+        _dense(out, "out", dev)
+    _launch(dev, "moe_grouped_mm_int8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
+            x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
 
@@ -242,8 +270,8 @@ def _spec(p, seed, step, dev):
         raise ValueError(f"p = {p} must lie in [0, 1]")
     ptr = None
     if isinstance(step, torch.Tensor):
-        if step.dtype != torch.int64 or step.numel() != 1 or step.device != dev:
-            raise ValueError(f"a tensor step must hold one int64 on {dev}")
+        if step.dtype != torch.int64 or step.numel() != 1 or step.get_device() != dev:
+            raise ValueError(f"a tensor step must hold one int64 on cuda:{dev}")
         ptr, step = step.data_ptr(), 0
     return ctypes.byref(DropoutSpec(p, seed & 0xFFFFFFFFFFFFFFFF, step & 0xFFFFFFFFFFFFFFFF, ptr))
 
@@ -252,11 +280,12 @@ def _dropout(x, p, seed, step, out):
     code = _code(x, "x")
     if out is not None:
         _check(out, "out", x.dtype, x.shape)
-    with _place(x=x, out=out):
-        if out is None:
-            out = torch.empty_like(x)
-        _lib.call("moe_dropout", code, x.numel(), _spec(p, seed, step, x.device), x.data_ptr(), out.data_ptr(),
-                  _stream(x.device))
+    dev = _dense(x, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _dense(out, "out", dev)
+    _launch(dev, "moe_dropout", code, x.numel(), _spec(p, seed, step, dev), x.data_ptr(), out.data_ptr())
     return out
 
 
@@ -298,42 +327,37 @@ def dropout(x, p, seed, step=0, out=None):
 def _row_stride(t, name):
     """Elements from one row of t [R, F] to the next: the last dimension is dense, rows may be
     apart (the halves of a packed [R, 2 F] tensor)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU (there is no CPU path)")
     R, F = t.shape
-    if F > 1 and t.stride(1) != 1:
+    sr, sf = t.stride()
+    if F > 1 and sf != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
-    ld = t.stride(0) if R > 1 else F
+    ld = sr if R > 1 else F
     if ld < F:
         raise ValueError(f"the rows of {name} overlap (stride {ld} < {F})")
     return ld
 
 
 def _act_args(a, b):
+    """(type, GPU, row stride of a, row stride of b, address of b)"""
     _dims(a, 2, "a")
     code = _code(a, "a")
-    lda, ldb = _row_stride(a, "a"), 0
-    if b is not None:
-        _check(b, "b", a.dtype, a.shape)
-        ldb = _row_stride(b, "b")
-        if b.device != a.device:
-            raise ValueError(f"b is on {b.device}, a on {a.device}")
-    return code, lda, ldb
+    dev = _on(a, "a", None)
+    if b is None:
+        return code, dev, _row_stride(a, "a"), 0, None
+    _check(b, "b", a.dtype, a.shape)
+    _on(b, "b", dev)
+    return code, dev, _row_stride(a, "a"), _row_stride(b, "b"), b.data_ptr()
 
 
 def _gated_act(a, b, p, seed, step, out):
-    code, lda, ldb = _act_args(a, b)
+    code, dev, lda, ldb, bp = _act_args(a, b)
     R, F = a.shape
-    if out is not None:
+    if out is None:
+        out = a.new_empty((R, F))
+    else:
         _check(out, "out", a.dtype, (R, F))
-        _place(out=out)
-        if out.device != a.device:
-            raise ValueError(f"out is on {out.device}, a on {a.device}")
-    with _device(a.device):
-        if out is None:
-            out = a.new_empty((R, F))
-        _lib.call("moe_gated_act", code, R, F, _spec(p, seed, step, a.device), a.data_ptr(), lda,
-                  None if b is None else b.data_ptr(), ldb, out.data_ptr(), _stream(a.device))
+        _dense(out, "out", dev)
+    _launch(dev, "moe_gated_act", code, R, F, _spec(p, seed, step, dev), a.data_ptr(), lda, bp, ldb, out.data_ptr())
     return out
 
 
@@ -366,29 +390,31 @@ def gated_act(a, b=None, p=0.0, seed=0, step=0, out=None):
 def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
     """(da, db) of gated_act for the gradient dh [R, F] (db None when b is).  `out` = (da, db):
     tensors to write, which may be halves of one packed gradient."""
-    code, lda, ldb = _act_args(a, b)
+    code, dev, lda, ldb, bp = _act_args(a, b)
     R, F = a.shape
     _check(dh, "dh", a.dtype, (R, F))
-    _place(dh=dh)
-    if dh.device != a.device:
-        raise ValueError(f"dh is on {dh.device}, a on {a.device}")
-    with _device(a.device):
-        if out is None:
-            da = a.new_empty((R, F))
-            db = None if b is None else a.new_empty((R, F))
-        else:
-            da, db = out
-            _check(da, "da", a.dtype, (R, F))
-            if (db is None) != (b is None):
-                raise ValueError("db must be given exactly when b is")
-            if db is not None:
-                _check(db, "db", a.dtype, (R, F))
-            for t, name in ((da, "da"), (db, "db")):
-                if t is not None and t.device != a.device:
-                    raise ValueError(f"{name} is on {t.device}, a on {a.device}")
-        _lib.call("moe_gated_act_grad", code, R, F, _spec(p, seed, step, a.device), dh.data_ptr(), a.data_ptr(), lda,
-                  None if b is None else b.data_ptr(), ldb, da.data_ptr(), _row_stride(da, "da"),
-                  None if db is None else db.data_ptr(), 0 if db is None else _row_stride(db, "db"), _stream(a.device))
+    _dense(dh, "dh", dev)
+    lddb, dbp = 0, None
+    if out is None:
+        da, ldda = a.new_empty((R, F)), F
+        db = None
+        if b is not None:
+            db, lddb = a.new_empty((R, F)), F
+    else:
+        da, db = out
+        _check(da, "da", a.dtype, (R, F))
+        _on(da, "da", dev)
+        ldda = _row_stride(da, "da")
+        if (db is None) != (b is None):
+            raise ValueError("db must be given exactly when b is")
+        if db is not None:
+            _check(db, "db", a.dtype, (R, F))
+            _on(db, "db", dev)
+            lddb = _row_stride(db, "db")
+    if db is not None:
+        dbp = db.data_ptr()
+    _launch(dev, "moe_gated_act_grad", code, R, F, _spec(p, seed, step, dev), dh.data_ptr(), a.data_ptr(), lda, bp, ldb,
+            da.data_ptr(), ldda, dbp, lddb)
     return da, db
 
 
@@ -406,11 +432,14 @@ def combine_grad(dout, y_perm, row_of_pair, topk_w):
     _check(y_perm, "y_perm", dout.dtype, (R, H))
     _check(topk_w, "topk_w", torch.float32, (T, k))
     _check(row_of_pair, "row_of_pair", torch.int32, (T * k,))
-    with _place(dout=dout, y_perm=y_perm, row_of_pair=row_of_pair, topk_w=topk_w):
-        dy = torch.empty_like(y_perm)
-        dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
-        _lib.call("moe_combine_grad", code, T, k, H, R, dout.data_ptr(), y_perm.data_ptr(), row_of_pair.data_ptr(),
-                  topk_w.data_ptr(), dy.data_ptr(), dw.data_ptr(), _stream(dout.device))
+    dev = _dense(dout, "dout")
+    _dense(y_perm, "y_perm", dev)
+    _dense(row_of_pair, "row_of_pair", dev)
+    _dense(topk_w, "topk_w", dev)
+    dy = torch.empty_like(y_perm)
+    dw = torch.empty_like(topk_w)
+    _launch(dev, "moe_combine_grad", code, T, k, H, R, dout.data_ptr(), y_perm.data_ptr(), row_of_pair.data_ptr(),
+            topk_w.data_ptr(), dy.data_ptr(), dw.data_ptr())
     return dy, dw
 
 
@@ -448,7 +477,7 @@ def forward_int8(x, w_gate, experts: QuantizedExperts, top_k, bias=None, flags=0
         out = torch.empty_like(x)
     if T == 0:
         return out
-    with _place(x=x, w_gate=w_gate, bias=bias, out=out):
+    with _current(x=x, w_gate=w_gate, bias=bias, out=out):
         _, idx, w = M.route(x, w_gate, top_k, bias=bias, flags=flags)
         g = M.permute(idx, E, x=x, capacity=_lib.capacity_rows(capacity_factor, T, top_k, E))
         y = grouped_ffn_int8(g["x_perm"], g["offsets"], experts)
@@ -541,7 +570,7 @@ def forward_train(x, w_gate, w_in, w_up, w_out, top_k, bias=None, dropout_p=0.0,
         raise ValueError("forward_train has the gradient of renormalised gates only")
     if T == 0:
         raise ValueError("forward_train needs at least one token")
-    with _place(x=x, w_gate=w_gate, bias=bias, w_in=w_in, w_up=w_up, w_out=w_out):
+    with _current(x=x, w_gate=w_gate, bias=bias, w_in=w_in, w_up=w_up, w_out=w_out):
         g, idx, _ = _Route.apply(x, w_gate, bias, top_k, flags)
         x_perm, offsets, row_of_pair = _Permute.apply(x, idx, E, _lib.capacity_rows(capacity_factor, T, top_k, E))
         a = grouped_mm(x_perm, w_in, offsets)

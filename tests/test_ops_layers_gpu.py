@@ -236,7 +236,7 @@ def test_two_streams(M):
 
 def test_many_rows_past_32_bits(M):
     """Row offsets past 2^32 bytes: the last rows of a tall activation, a tall product and a
-    tall dropout equal the same rows computed alone."""
+    tall dropout are right."""
     say("past 32 bits")
     R, K, N = 530000, 4096, 8                      # x: 4.3 GB
     x = torch.empty((R, K), dtype=bf, device="cuda").normal_()
@@ -244,12 +244,16 @@ def test_many_rows_past_32_bits(M):
     dy = torch.empty((R, N), dtype=bf, device="cuda").normal_()
     off = torch.tensor([0, R - 100, R], dtype=torch.int32, device="cuda")
     tail = torch.tensor([0, 0, 100], dtype=torch.int32, device="cuda")
+    # the rows alone may take another form of the kernel, whose sums run in another order: the
+    # float products are held to the 64-bit ones, by the bounds of the products' own tests
+    from test_ops_gpu import check
+    xt, dyt, w1 = x[-100:].cpu().to(f64), dy[-100:].cpu().to(f64), w[1].cpu().to(f64)
     y = M.grouped_mm(x, w, off)
-    assert torch.equal(y[-100:], M.grouped_mm(x[-100:].contiguous(), w, tail))
+    check(y[-100:], xt @ w1, K * 2.0 ** -23 * (xt.abs() @ w1.abs()), "y")
     dx = M.grouped_mm_dx(dy, w, off)
-    assert torch.equal(dx[-100:], M.grouped_mm_dx(dy[-100:].contiguous(), w, tail))
+    check(dx[-100:], dyt @ w1.T, N * 2.0 ** -23 * (dyt.abs() @ w1.T.abs()), "dx")
     dw = M.grouped_mm_dw(x, dy, off)
-    assert torch.equal(dw[1], M.grouped_mm_dw(x[-100:].contiguous(), dy[-100:].contiguous(), tail)[1])
+    check(dw[1], xt.T @ dyt, 100 * 2.0 ** -23 * (xt.T.abs() @ dyt.abs()), "dw")
     q, s = M.quantize_rows(x)
     q2, s2 = M.quantize_rows(x[-100:].contiguous())
     assert torch.equal(q[-100:], q2) and torch.equal(s[-100:], s2)
