@@ -30,11 +30,12 @@ extern "C" {
 /* A grouped product.  `rows` rows lie in E consecutive groups: group e holds the rows
  * [offsets[e], offsets[e+1]) (offsets [E+1] int32 on the device, as moe_permute writes
  * them).  Group sizes are arbitrary, zero among them; rows before offsets[0] and from
- * offsets[E] on belong to no group.  Offsets must not decrease; each is clamped into
- * [0, rows], so that no value leads outside the buffers.
- * Limits: 0 <= rows < 2^24 * 64; 1 <= E <= 256; K and N multiples of 8, at most 2^20
- * (moe_grouped_mm_int8: K a multiple of 16, at most 131072, so that no 32-bit sum can
- * overflow). */
+ * offsets[E] on belong to no group.  Offsets must not decrease; whatever they hold,
+ * nothing outside the buffers is read or written.
+ * Limits: 0 <= rows < 2^30; 1 <= E <= 256; K and N multiples of 8, at most 2^20; the output's
+ * tiles within one launch (2^23 of 256 x 256, fp32 2^24 of 128 x 128; MOE_ERR_UNSUPPORTED
+ * beyond).  moe_grouped_mm_int8: K a multiple of 16, at most 131056, so that no 32-bit sum
+ * can overflow. */
 typedef struct {
     int64_t  rows;
     int32_t  E, K, N;

@@ -1,10 +1,13 @@
 // Grouped products, tiles of 64 and 128: for groups or matrices too small to fill the chip
 // with 256 x 256 tiles, and for fp32 (mm_tile.h has the kinds, layouts and loads).
 //
-// Four wavefronts, 2 x 2 over the tile; S stages in LDS with the loads S - 1 steps ahead and
-// one barrier per step: a wavefront that passes step k's barrier has finished step k - 1,
-// whose stage the loads of step k + S - 1 then fill.  Two or more workgroups share a CU and
-// cover each other's waits, where the large kernel needs its two groups.
+// Four wavefronts, 2 x 2 over the tile; S stages of U steps in LDS with the loads S - 1 stages
+// ahead and one barrier per stage: a wavefront that passes a stage's barrier has finished
+// the stage before, which the loads then fill.  Two or more workgroups share a CU and cover
+// each other's waits, where the large kernel needs its two groups.  A workgroup alone on its
+// CU runs at the length of its own chain (barrier, LDS reads, products, addresses: some 400
+// cycles a step, the same with every load out of range); reading a step ahead into a second
+// set of registers did not shorten it.
 //
 // fp32 runs the 16x16x4 instruction, at the card's full fp32 rate; its operands cost a
 // fraction of the time that the instructions take, so nothing else is done for it.
@@ -14,20 +17,20 @@ namespace moe {
 
 namespace {
 
-template <typename O, int BM, int BN, int S>
+template <typename O, int BM, int BN, int S, int U>
 struct Mid {
     static constexpr int FM = BM / 32, FN = BN / 32;          // 16-index blocks of a wavefront
     static constexpr int NA = BM / 64, NB = BN / 64;          // loads per wavefront and step
-    static constexpr int kA = BM * 64, kStage = (BM + BN) * 64;
+    static constexpr int kSub = (BM + BN) * 64, kStage = U * kSub;      // bytes of one step; of a stage
     static constexpr int kCS = BN + 8;                        // bf16 per row of the staging tile
     static constexpr size_t kOut = (size_t)BM * kCS * 2;
     static constexpr size_t kLds = kOut > (size_t)S * kStage ? kOut : (size_t)S * kStage;
 };
 
-template <typename O, int BM, int BN, int S, typename OUT>
+template <typename O, int BM, int BN, int S, int U, typename OUT>
 __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__          // the host pass needs the signature only
-    using L = Mid<O, BM, BN, S>;
+    using L = Mid<O, BM, BN, S, U>;
     using ACC = typename O::Acc;
     extern __shared__ uint4 smem[];
     __shared__ Groups groups;
@@ -58,19 +61,22 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
     const int KT = (t.C + O::kStep - 1) / O::kStep;
     if (KT > 0) {
 #pragma unroll
-        for (int s = 0; s < S - 1; ++s) {
-            oa.load(lds + s * L::kStage, wave * L::NA, s);
-            ob.load(lds + s * L::kStage + L::kA, wave * L::NB, s);
+        for (int q = 0; q < (S - 1) * U; ++q) {
+            oa.load(lds + q * L::kSub, wave * L::NA, q);
+            ob.load(lds + q * L::kSub + BM * 64, wave * L::NB, q);
         }
-        int st = 0, nx = S - 1;                               // stage of this step, and of the loads it starts
-        for (int kt = 0; kt < KT; ++kt) {
-            wait_vmcnt<(S - 2) * (L::NA + L::NB)>();
+        int st = 0, nx = S - 1;                               // stage of these steps, and of the loads they start
+        for (int kt = 0; kt < KT; kt += U) {                  // steps past the end multiply the zeros their loads read
+            wait_vmcnt<(S - 2) * U * (L::NA + L::NB)>();
             lds_barrier();
-            u32x4_t af[L::FM], bf[L::FN];
-            read_and_load<O, BM, BN, 4>(lds + st * L::kStage, lds + nx * L::kStage, kt + S - 1, row0 / 16, wn * L::FN, wave, oa,
-                                     ob, ra, rb, af, bf);
+            u32x4_t af[U][L::FM], bf[U][L::FN];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                read_and_load<O, BM, BN, 4>(lds + st * L::kStage + u * L::kSub, lds + nx * L::kStage + u * L::kSub,
+                                            kt + (S - 1) * U + u, row0 / 16, wn * L::FN, wave, oa, ob, ra, rb, af[u], bf[u]);
             wait_lds();
-            mma_step<O::ELEM>(af, bf, acc, nblk);
+#pragma unroll
+            for (int u = 0; u < U; ++u) mma_step<O::ELEM>(af[u], bf[u], acc, nblk);
             st = st + 1 == S ? 0 : st + 1;
             nx = nx + 1 == S ? 0 : nx + 1;
         }
@@ -125,31 +131,43 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
 #endif
 }
 
-template <typename O, int BM, int BN, int S, typename OUT>
+template <typename O, int BM, int BN, int S, int U, typename OUT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
-    constexpr size_t lds = Mid<O, BM, BN, S>::kLds;
-    hipError_t e = allow_lds<k_mm_mid<O, BM, BN, S, OUT>>(lds);
+    constexpr size_t lds = Mid<O, BM, BN, S, U>::kLds;
+    hipError_t e = allow_lds<k_mm_mid<O, BM, BN, S, U, OUT>>(lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mm_mid<O, BM, BN, S, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, BM, BN)), dim3(256), lds, st, a);
+    hipLaunchKernelGGL((k_mm_mid<O, BM, BN, S, U, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, BM, BN)), dim3(256), lds, st, a);
     return hipGetLastError();
 }
 
-template <int BM, int BN, int S>
-hipError_t go_kind(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
-    const bool f = out_dtype == MOE_F32;
-    if (kind == 3) return f ? go<Op<3, Elem::i8>, BM, BN, S, float>(a, st) : go<Op<3, Elem::i8>, BM, BN, S, bf16_t>(a, st);
-    if (dtype == MOE_F32)
-        return kind == 0   ? go<Op<0, Elem::f32>, BM, BN, S, float>(a, st)
-               : kind == 1 ? go<Op<1, Elem::f32>, BM, BN, S, float>(a, st)
-                           : go<Op<2, Elem::f32>, BM, BN, S, float>(a, st);
-    if (kind == 2) return f ? go<Op<2, Elem::bf16>, BM, BN, S, float>(a, st) : go<Op<2, Elem::bf16>, BM, BN, S, bf16_t>(a, st);
-    return kind == 0 ? go<Op<0, Elem::bf16>, BM, BN, S, bf16_t>(a, st) : go<Op<1, Elem::bf16>, BM, BN, S, bf16_t>(a, st);
+template <int BM, int BN, int S, int U>
+hipError_t go_16(int kind, bool f, const MmArgs& a, hipStream_t st) {
+    switch (kind) {
+        case 0: return go<Op<0, Elem::bf16>, BM, BN, S, U, bf16_t>(a, st);
+        case 1: return go<Op<1, Elem::bf16>, BM, BN, S, U, bf16_t>(a, st);
+        case 2: return f ? go<Op<2, Elem::bf16>, BM, BN, S, U, float>(a, st) : go<Op<2, Elem::bf16>, BM, BN, S, U, bf16_t>(a, st);
+        default: return f ? go<Op<3, Elem::i8>, BM, BN, S, U, float>(a, st) : go<Op<3, Elem::i8>, BM, BN, S, U, bf16_t>(a, st);
+    }
+}
+
+template <int BM, int BN>
+hipError_t go_32(int kind, const MmArgs& a, hipStream_t st) {
+    switch (kind) {
+        case 0: return go<Op<0, Elem::f32>, BM, BN, 4, 1, float>(a, st);
+        case 1: return go<Op<1, Elem::f32>, BM, BN, 4, 1, float>(a, st);
+        default: return go<Op<2, Elem::f32>, BM, BN, 4, 1, float>(a, st);
+    }
 }
 
 }  // namespace
 
+// Two steps a barrier for tiles of 64 (16 and 8 bits): 256 rows, 4096 x 4096 transposed 22.8 ->
+// 21.6 us, 512 rows 34.7 -> 32.8, int8 19.0 -> 17.3; tiles of 128 and fp32, whose steps are
+// longer, lose by it (208 rows a group, fp32 weight gradient 89 -> 96).
 hipError_t launch_mm_mid(int tile, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
-    return tile == 64 ? go_kind<64, 64, 4>(kind, dtype, out_dtype, a, st) : go_kind<128, 128, 4>(kind, dtype, out_dtype, a, st);
+    if (kind != 3 && dtype == MOE_F32) return tile == 64 ? go_32<64, 64>(kind, a, st) : go_32<128, 128>(kind, a, st);
+    const bool f = out_dtype == MOE_F32;
+    return tile == 64 ? go_16<64, 64, 3, 2>(kind, f, a, st) : go_16<128, 128, 4, 1>(kind, f, a, st);
 }
 
 }  // namespace moe

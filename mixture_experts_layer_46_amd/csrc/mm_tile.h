@@ -275,9 +275,11 @@ __device__ __forceinline__ void tile_of_item(const MmArgs& a, const Groups& g, i
         tile_coords(w - p0 * NJ, tiles, NJ, it, jt);
         r0 = uni(g.r0[t.e]);
         r1 = uni(g.r1[t.e]);
-        const int h = ((r1 - r0 + tiles - 1) / tiles + 15) / 16 * 16;       // at most BM
-        t.i0 = uni(min(r0 + it * h, r1));
-        t.j0 = uni(jt * BN);
+        // (the clamps do nothing for offsets that do not decrease; for others, whose tile counts
+        // mean nothing, they keep the tile inside the group and the matrix)
+        const int h = min(max(((r1 - r0 + tiles - 1) / max(tiles, 1) + 15) / 16 * 16, 16), BM);
+        t.i0 = uni(min(max(r0 + it * h, r0), r1));
+        t.j0 = uni(min(max(jt, 0), NJ - 1) * BN);
         t.ni = uni(min(h, r1 - t.i0));
         t.C = O::KIND == 1 ? a.N : a.K;
         t.crow = t.i0;

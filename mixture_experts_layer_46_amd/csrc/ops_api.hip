@@ -42,7 +42,7 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
     } while (0)
 
 constexpr int kMaxDim = 1 << 20;          // K, N: 256 rows of fp32 stay below 2 GiB
-constexpr int kMaxInt8K = 131072;         // 127 * 127 * K < 2^31
+constexpr int kMaxInt8K = 131056;         // 128 * 128 * K < 2^31
 constexpr int64_t kMaxGrid = 1 << 24;     // workgroups of 256 threads: 2^32 work items a launch
 constexpr int64_t kMaxElems = 1ll << 34;
 

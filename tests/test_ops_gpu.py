@@ -174,6 +174,32 @@ def test_offsets_are_held_in_bounds(M):
     assert torch.equal(y, good)
 
 
+@pytest.mark.parametrize("off", [[0, 60, 10, 40, 20], [70, 0, 70, 0, 70], [100, 80, 60, 40, 20],
+                                 [-5, 1 << 30, -(1 << 31), (1 << 31) - 1, 3]])
+def test_offsets_that_decrease_stay_in_bounds(M, off):
+    """Decreasing offsets name no groups; the results mean nothing, but nothing outside the
+    output is written: guard rows around it keep their values."""
+    say(f"decreasing offsets {off}")
+    o = torch.tensor(off, dtype=torch.int32).cuda()
+    R, K, N, G = 70, 72, 264, 64
+    for dtype in (bf, f32):
+        x, dy, w = rand((R, K), dtype, 1).cuda(), rand((R, N), dtype, 2).cuda(), rand((4, K, N), dtype, 3).cuda()
+        y = torch.full((R + 2 * G, N), 7.0, dtype=dtype, device="cuda")
+        dx = torch.full((R + 2 * G, K), 7.0, dtype=dtype, device="cuda")
+        dw = torch.full((6, K, N), 7.0, dtype=dtype, device="cuda")
+        M.grouped_mm(x, w, o, out=y[G:G + R])
+        M.grouped_mm_dx(dy, w, o, out=dx[G:G + R])
+        M.grouped_mm_dw(x, dy, o, out=dw[1:5])
+        for t in (y, dx):
+            assert bool((t[:G] == 7).all()) and bool((t[G + R:] == 7).all())
+        assert bool((dw[0] == 7).all()) and bool((dw[5] == 7).all())
+    K = 80
+    xq, wq = torch.ones(R, K, dtype=torch.int8).cuda(), torch.ones(4, N, K, dtype=torch.int8).cuda()
+    y = torch.full((R + 2 * G, N), 7.0, dtype=bf, device="cuda")
+    M.grouped_mm_int8(xq, torch.ones(R).cuda(), wq, torch.ones(4, N).cuda(), o, out=y[G:G + R])
+    assert bool((y[:G] == 7).all()) and bool((y[G + R:] == 7).all())
+
+
 def test_no_rows(M):
     say("no rows")
     for dtype in (bf, f32):
