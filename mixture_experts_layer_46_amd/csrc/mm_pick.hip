@@ -8,8 +8,8 @@
 //
 // The three constants of a form come from some 5000 random calls (1-256 groups, 1-60000 rows,
 // matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every form.
-// Over those calls the form picked is 3.4% (16- and 8-bit operands), 1.7% (their weight
-// gradient), 4.0% and 1.3% (fp32) slower than the best one in the geometric mean; the best
+// Over those calls the form picked is 3.1% (16- and 8-bit operands), 1.7% (their weight
+// gradient), 3.7% and 1.3% (fp32) slower than the best one in the geometric mean; the best
 // single form would be 25%, 14%, 45% and 2% slower.
 #include <algorithm>
 #include <cmath>
@@ -29,9 +29,10 @@ struct Shape {
     int per_cu;           // workgroups a CU holds
     int split;            // wavefronts that share the contraction
     int threads;
+    double rate;          // bytes per us that it reaches when weights streamed once are all there is
 };
-constexpr Shape kShape[FORMS] = {{256, 256, 1, 1, 512}, {128, 128, 2, 1, 256}, {64, 64, 4, 1, 256}, {32, 64, 2, 4, 256},
-                                 {16, 64, 1, 8, 512}};
+constexpr Shape kShape[FORMS] = {{256, 256, 1, 1, 512, 5.0e6}, {128, 128, 2, 1, 256, 5.3e6}, {64, 64, 4, 1, 256, 5.4e6},
+                                 {32, 64, 2, 4, 256, 5.6e6},   {16, 64, 1, 8, 512, 4.9e6}};
 
 struct Cost {
     double fixed, step, busy;     // us: per workgroup; per step alone; per step and workgroup of a full CU
@@ -41,7 +42,7 @@ constexpr Cost kRows16[FORMS] = {{3.4, .42, .85}, {2.3, .33, .29}, {2.05, .14, .
 constexpr Cost kWeights16[FORMS] = {{4.8, .70, .90}, {2.6, .56, .32}, {1.6, .23, .141}, {}, {}};
 constexpr Cost kRows32[FORMS] = {{}, {2.1, .95, .95}, {1.66, .33, .25}, {2.5, .53, .55}, {2.6, .68, .22}};
 constexpr Cost kWeights32[FORMS] = {{}, {1.63, .45, 1.09}, {1.0, .47, .244}, {}, {}};
-constexpr double kBytesPerUs = 5.2e6;
+constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
 const Cost* costs(int kind, int dtype) {
     const bool f32 = kind != 3 && dtype == MOE_F32;
@@ -78,7 +79,7 @@ double estimate(int kind, int dtype, const MmArgs& a, int form) {
         const double r = per_cu / s.per_cu;
         t = (r < 2 ? 2 : r + .4) * (c.fixed + steps * std::max(c.step, s.per_cu * c.busy));
     }
-    const double bytes = (R * K + R * N) * es + (kind == 2 ? E : groups) * K * N * es, m = bytes / kBytesPerUs;
+    const double bytes = (R * K + R * N) * es + (kind == 2 ? E : groups) * K * N * es, m = bytes / (kind == 2 ? kWriteRate : s.rate);
     return std::max(t, m) + .2 * std::min(t, m);
 }
 
