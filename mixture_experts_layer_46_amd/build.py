@@ -19,7 +19,7 @@ SRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "grouped_gemm.hip", "combine.hip", "peaks.hip",
-           "ops_api.hip", "mm.hip", "mm_mid.hip", "mm_thin.hip", "mm_pick.hip",
+           "ops_api.hip", "mm.hip", "mm_stream.hip", "mm_mid.hip", "mm_thin.hip", "mm_pick.hip",
            "quantize.hip", "dropout.hip", "combine_grad.hip"]
 ARCH = "gfx950"
 

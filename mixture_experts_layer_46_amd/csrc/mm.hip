@@ -1,9 +1,6 @@
-// Grouped products, large tiles: 256 x 256 on the matrix cores (mm_tile.h has the kinds, the
-// operand layouts and the loads).
-//
-// Eight wavefronts, 2 x 4 over the tile: 128 x 64 wavefront tiles of 128 accumulator
-// registers, two wavefronts per SIMD.  Operands go into four LDS stages.  Two forms of the
-// inner loop:
+// Grouped products, large tiles: 256 x 256 on the matrix cores, one tile per workgroup
+// (mm_tile.h has the kinds, the operand layouts and the loads, mm_large.h the tile's division).
+// Two forms of the inner loop:
 //   woven       within a step every wavefront multiplies the operands it holds in registers,
 //               reads the next step's from LDS and starts the loads of the fourth step after,
 //               spread between the matrix instructions; one barrier a step.
@@ -14,68 +11,19 @@
 // hide in half a step: woven there (kinds 0 and 2; 8 experts, 8192 rows, 4096 <-> 14336: 912
 // against 947 us and 975 against 1042), step-apart for kinds 1 and 3 (994 against 1016, int8
 // 506 against 515; 4096^3: 107.6 against 113.2).
-#include "mm_tile.h"
+#include "mm_large.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kT = 256;                       // tile rows and columns
-constexpr int kStage = 2 * kT * 64;           // bytes of a step: the A operand, then the B operand
-constexpr int kStages = 4;
+using namespace large;
+
 constexpr int kCS = kT + 8;                   // bf16 per row of the output staging tile
 constexpr size_t kLds = (size_t)kT * kCS * 2; // staging tile; the stages (128 KB) lie inside
 static_assert(kStages * kStage <= (int)kLds, "the stages fit below the staging tile's end");
-constexpr int kLoads = 2;                     // loads of one operand per wavefront and step
-constexpr int kVmcnt = 4 * kLoads;            // loads of the two steps after the awaited one
-
 template <typename O>
 constexpr bool kApart = !O::kACols && !O::kBCols;
-template <typename O>
-using OpA = Operand<O::ES, O::kACols, kT, kLoads>;
-template <typename O>
-using OpB = Operand<O::ES, O::kBCols, kT, kLoads>;
-
-// One step: the products of the operands in registers, with the next step's operands read
-// from stage `rd` and a later step's loads started into stage `wr` in between (two reads
-// after each of six row blocks, the loads after the third and the fifth: measured against
-// denser and later placements, 1-4% on the large shapes).  The matrix instruction takes the
-// B operand first, so that a lane's four sums are four columns of one row.
-// The stages are separate __restrict__ arguments: otherwise the compiler takes the
-// transposing reads to touch what is in flight, and waits for every load before them.
-template <typename O>
-__device__ __attribute__((always_inline)) inline void step(const lds_char* __restrict__ rd, lds_char* __restrict__ wr,
-                                                           int kload, int nblk, int wm, int wn, int wave,
-                                                           const OpA<O>& oa, const OpB<O>& ob,
-                                                           const Reader<O::ES, O::kACols, kT>& ra,
-                                                           const Reader<O::ES, O::kBCols, kT>& rb,
-                                                           const u32x4_t (&af)[8], const u32x4_t (&bf)[4],
-                                                           u32x4_t (&an)[8], u32x4_t (&bn)[4],
-                                                           typename O::Acc (&acc)[8][4]) {
-    asm volatile("" : "+s"(nblk));    // compared anew at each row block (a scalar compare; kept masks cost vector ones)
-    wait_lds();                       // this step's operands are in registers: their stage is free
-    wait_vmcnt<kVmcnt>();             // this wavefront's loads of the next step have landed
-    lds_barrier();                    // everyone's
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (__builtin_expect(i < nblk, 1)) {                  // a full tile falls through
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mma<O::ELEM>(bf[j], af[i], acc[i][j]);
-        }
-#pragma unroll
-        for (int q = 2 * i; q < 2 * i + 2; ++q) {
-            if (q < 4) bn[q] = rb(rd + kT * 64, wn * 4 + q);
-            else if (q < 12) an[q - 4] = ra(rd, wm * 8 + q - 4);
-        }
-        if (i == 2) oa.load(wr, wave * kLoads, kload);
-        if (i == 4) ob.load(wr + kT * 64, wave * kLoads, kload);
-    }
-    // the sums live in accumulator registers, next to the two sets of operands
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
-}
 
 // The steps of one of the two wavefront groups, in step-apart form (below).  Between two
 // barriers one group is in its read phase (R) and the other in its matrix phase (M):
@@ -243,10 +191,16 @@ hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t
     switch (kind) {
         case 0: return go<Op<0, Elem::bf16>, bf16_t>(a, st);
         case 1: return go<Op<1, Elem::bf16>, bf16_t>(a, st);
-        case 2: return f ? go<Op<2, Elem::bf16>, float>(a, st) : go<Op<2, Elem::bf16>, bf16_t>(a, st);
+        case 2: {
+            // Few rows a group: the time is the writing of the matrices, which many workgroups
+            // at once do better (64 experts, 2048 x 1408: 2 rows a group 85 us here, 94 there;
+            // 32 rows 90 and 95; 64 rows 103 and 96; 256 rows 168 and 151).
+            const int groups = a.rows < a.E ? a.rows : a.E;
+            if (a.rows >= 48ll * groups && a.rows > 0) return launch_mm_stream(out_dtype, a, st);
+            return f ? go<Op<2, Elem::bf16>, float>(a, st) : go<Op<2, Elem::bf16>, bf16_t>(a, st);
+        }
         default: return f ? go<Op<3, Elem::i8>, float>(a, st) : go<Op<3, Elem::i8>, bf16_t>(a, st);
     }
 }
-
 
 }  // namespace moe

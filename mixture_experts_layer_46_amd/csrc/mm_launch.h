@@ -24,6 +24,7 @@ hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStr
 bool mm_fits(int kind, int dtype, const MmArgs& a);
 // the forms: 256 x 256 tiles (bf16, int8); tiles of 64 or 128; 16 or 32 rows with the
 // contraction split over 8 or 4 wavefronts (not kind 2)
+hipError_t launch_mm_stream(int out_dtype, const MmArgs& a, hipStream_t st);              // kind 2 of large
 hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t st);
 hipError_t launch_mm_mid(int tile, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
 hipError_t launch_mm_thin(int rows, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);

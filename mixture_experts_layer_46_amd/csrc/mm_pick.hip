@@ -1,4 +1,5 @@
-// Which form of the grouped products' kernels a call takes (mm.hip, mm_mid.hip, mm_thin.hip).
+// Which form of the grouped products' kernels a call takes (mm.hip and mm_stream.hip, mm_mid.hip,
+// mm_thin.hip).
 //
 // The group sizes stay on the device, so the choice is made from what the host knows: the
 // rows, the groups and the matrix sizes.  Each form's time is estimated as rounds of
@@ -6,11 +7,11 @@
 // each step the larger of its latency when a workgroup is alone and of its share of a full
 // CU; the bytes that every form has to move bound the whole from below.
 //
-// The three constants of a form come from some 5000 random calls (1-256 groups, 1-60000 rows,
+// The three constants of a form come from some 10000 random calls (1-256 groups, 1-60000 rows,
 // matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every form.
-// Over those calls the form picked is 3.1% (16- and 8-bit operands), 1.7% (their weight
+// Over those calls the form picked is 3.1% (16- and 8-bit operands), 2.3% (their weight
 // gradient), 3.7% and 1.3% (fp32) slower than the best one in the geometric mean; the best
-// single form would be 25%, 14%, 45% and 2% slower.
+// single form would be 25%, 16%, 45% and 2% slower.
 #include <algorithm>
 #include <cmath>
 
@@ -39,7 +40,7 @@ struct Cost {
 };
 // the forms that do not exist (fp32 LARGE, THIN weight gradients) have no cost
 constexpr Cost kRows16[FORMS] = {{3.4, .42, .85}, {2.3, .33, .29}, {2.05, .14, .121}, {2.1, .25, .32}, {2.4, .51, .05}};
-constexpr Cost kWeights16[FORMS] = {{4.8, .70, .90}, {2.6, .56, .32}, {1.6, .23, .141}, {}, {}};
+constexpr Cost kWeights16[FORMS] = {{4.3, .95, 1.0}, {2.35, .56, .29}, {1.75, .23, .141}, {}, {}};
 constexpr Cost kRows32[FORMS] = {{}, {2.1, .95, .95}, {1.66, .33, .25}, {2.5, .53, .55}, {2.6, .68, .22}};
 constexpr Cost kWeights32[FORMS] = {{}, {1.63, .45, 1.09}, {1.0, .47, .244}, {}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form

@@ -194,19 +194,28 @@ __device__ __forceinline__ void mma_step(const u32x4_t (&af)[FM], const u32x4_t 
     }
 }
 
-// Reads a wavefront's operands of a step from stage `rd` (the A operand's T_A x 64 bytes, then
-// the B operand's) and starts its share of a later step's loads into stage `wr`.  The two are
-// separate __restrict__ arguments: otherwise the compiler takes the transposing reads to touch
-// what is in flight, and waits for every load before them.  W wavefronts share the loads.
+// A wavefront's operands of a step, from a stage of the A operand's T_A x 64 bytes, then the
+// B operand's.
+template <int TA, typename RA, typename RB, int FM, int FN>
+__device__ __attribute__((always_inline)) inline void read_stage(const lds_char* __restrict__ rd, int ablk, int bblk,
+                                                                 const RA& ra, const RB& rb, u32x4_t (&af)[FM],
+                                                                 u32x4_t (&bf)[FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) af[i] = ra(rd, ablk + i);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bf[j] = rb(rd + TA * 64, bblk + j);
+}
+
+// Reads a wavefront's operands of a step from stage `rd` and starts its share of a later
+// step's loads into stage `wr`.  The two are separate __restrict__ arguments: otherwise the
+// compiler takes the transposing reads to touch what is in flight, and waits for every load
+// before them.  W wavefronts share the loads.
 template <typename O, int TA, int TB, int W, typename OA, typename OB, typename RA, typename RB, int FM, int FN>
 __device__ __attribute__((always_inline)) inline void read_and_load(const lds_char* __restrict__ rd,
                                                                     lds_char* __restrict__ wr, int kt, int ablk, int bblk,
                                                                     int wave, const OA& oa, const OB& ob, const RA& ra,
                                                                     const RB& rb, u32x4_t (&af)[FM], u32x4_t (&bf)[FN]) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i) af[i] = ra(rd, ablk + i);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) bf[j] = rb(rd + TA * 64, bblk + j);
+    read_stage<TA>(rd, ablk, bblk, ra, rb, af, bf);
     __builtin_amdgcn_sched_barrier(0);
     oa.load(wr, wave * (TA / 16 / W), kt);
     ob.load(wr + TA * 64, wave * (TB / 16 / W), kt);
