@@ -1,4 +1,4 @@
-// Helpers of the grouped products (mm.hip, mm_f32.hip): row groups and row tiles.
+// Helpers of the grouped products (mm.hip, mm_stream.hip, mm_mid.hip, mm_thin.hip): row groups and row tiles.
 #pragma once
 
 #include "common.h"

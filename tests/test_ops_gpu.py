@@ -322,6 +322,119 @@ def test_grouped_mm_int8(M, counts, K, N, out):
     assert bool((keep[:tail] == 7).all()) and bool((keep[R + tail:] == 7).all())
 
 
+# Calls with enough work for the large tiles, whose kernels the cases above never reach:
+# several rounds of 256 x 256 tiles, a workgroup per tile and a stream of tiles (a weight
+# gradient of many and of few rows a group), and 128 x 128 tiles, with empty groups, groups of
+# one row, and tiles that end early on both sides.
+BIG_CASES = [([1000, 257, 0, 2200, 1, 1542], 2064, 2056), ([0, 700, 1, 5, 2294, 0], 1040, 1032), ([1500, 128, 0, 1, 371], 4112, 1032),
+             ([0, 1, 0, 12, 2, 0, 7], 4112, 216), ([400, 40, 1, 18, 0, 0], 144, 7336), ([3] * 8 + [0] * 20 + [9] * 36, 304, 440),
+             ([60] * 30 + [0] * 4 + [200] * 30, 304, 440), ([45, 0, 33, 64] * 16, 80, 984), ([71], 528, 16184), ([75] * 4, 1872, 2144)]
+BIG_IDS = [f"{sum(c)}rows-{len(c)}groups-{k}x{n}" for c, k, n in BIG_CASES]
+
+
+def on_gpu64(a, b):
+    """a @ b and |a| @ |b| in 64 bits (the references' sizes would take the CPU seconds each)."""
+    a, b = a.to(f64), b.to(f64)
+    return (a @ b).cpu(), (a.abs() @ b.abs()).cpu()
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("counts,K,N", BIG_CASES, ids=BIG_IDS)
+def test_grouped_mm_large_tiles(M, counts, K, N, dtype):
+    say(f"grouped_mm large counts={counts[:8]} K={K} N={N} {dtype}")
+    tail = 5
+    x, dy, w, off = mm_inputs(counts, K, N, dtype, tail)
+    xd, dyd, wd, od = x.cuda(), dy.cuda(), w.cuda(), off.cuda()
+    y, dx = torch.full_like(dyd, 7.0), torch.full_like(xd, 7.0)
+    M.grouped_mm(xd, wd, od, out=y)
+    M.grouped_mm_dx(dyd, wd, od, out=dx)
+    dw = torch.full((len(counts) + 2, K, N), 7.0, dtype=dtype, device="cuda")
+    M.grouped_mm_dw(xd, dyd, od, out=dw[1:-1])
+    dw32 = M.grouped_mm_dw(xd, dyd, od, dtype=f32)
+    torch.cuda.synchronize()
+    for t in (y, dx):
+        assert bool((t[:tail] == 7).all()) and bool((t[tail + sum(counts):] == 7).all())
+    assert bool((dw[0] == 7).all()) and bool((dw[-1] == 7).all())
+    for e, c in enumerate(counts):
+        a, b = int(off[e]), int(off[e + 1])
+        if c == 0:
+            assert not bool(dw[e + 1].any()) and not bool(dw32[e].any())
+            continue
+        ref, mag = on_gpu64(xd[a:b], wd[e])
+        check(y[a:b], ref, K * 2.0 ** -23 * mag, f"y of group {e}")
+        ref, mag = on_gpu64(dyd[a:b], wd[e].T)
+        check(dx[a:b], ref, N * 2.0 ** -23 * mag, f"dx of group {e}")
+        ref, mag = on_gpu64(xd[a:b].T, dyd[a:b])
+        check(dw[e + 1], ref, c * 2.0 ** -23 * mag, f"dw of group {e}")
+        check(dw32[e], ref, c * 2.0 ** -23 * mag, f"dw in fp32 of group {e}")
+    assert torch.equal(dw[1:-1].reshape(-1).view(torch.uint8), M.grouped_mm_dw(xd, dyd, od).reshape(-1).view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "fp32"])
+def test_large_tiles_do_not_mix_groups(M, dtype):
+    """NaN in one group's rows or matrix reaches that group's results and no other's."""
+    say(f"large tiles, NaN in groups {dtype}")
+    counts, K, N = [500, 700, 0, 259, 1200], 2056, 2056
+    x, dy, w, off = mm_inputs(counts, K, N, dtype, 0)
+    x[500:1200:50, 7] = float("nan")
+    dy[:500:100, 9] = float("nan")
+    w[3, 100, 200] = float("inf")
+    x, dy, w, od = x.cuda(), dy.cuda(), w.cuda(), off.cuda()
+    y, dx, dw = M.grouped_mm(x, w, od), M.grouped_mm_dx(dy, w, od), M.grouped_mm_dw(x, dy, od)
+    rows = torch.zeros(sum(counts), dtype=torch.bool, device="cuda")
+    rows[500:1200:50] = True
+    assert bool(y[rows].isnan().all()) and bool(y[~rows][:, :200].isfinite().all()) and bool(y[~rows][:, 201:].isfinite().all())
+    assert not bool(y[1200:1459, 200].isfinite().any()) and bool(y[1459:].isfinite().all())
+    rows[:] = False
+    rows[:500:100] = True
+    assert bool(dx[rows].isnan().all()) and bool(dx[~rows][:, :100].isfinite().all()) and bool(dx[~rows][:, 101:].isfinite().all())
+    assert bool(dw[1, 7].isnan().all()) and bool(dw[0, :, 9].isnan().all())
+    dw[1, 7], dw[0, :, 9] = 0, 0
+    assert bool(dw.isfinite().all()) and not bool(dw[2].any())
+
+
+@pytest.mark.parametrize("off", [[0, 3000, 500, 2000, 1000], [5000, 0, 5000, 0, 5000], [5000, 4000, 3000, 2000, 1000]])
+def test_large_tiles_with_offsets_that_decrease(M, off):
+    """As the small tiles: the results mean nothing, guard rows keep their values."""
+    say(f"large tiles, decreasing offsets {off}")
+    o = torch.tensor(off, dtype=torch.int32).cuda()
+    R, K, N, G = 5000, 2064, 2056, 300
+    for dtype in (bf, f32):
+        x, dy, w = rand((R, K), dtype, 1).cuda(), rand((R, N), dtype, 2).cuda(), rand((4, K, N), dtype, 3).cuda()
+        y = torch.full((R + 2 * G, N), 7.0, dtype=dtype, device="cuda")
+        dx = torch.full((R + 2 * G, K), 7.0, dtype=dtype, device="cuda")
+        dw = torch.full((6, K, N), 7.0, dtype=dtype, device="cuda")
+        M.grouped_mm(x, w, o, out=y[G:G + R])
+        M.grouped_mm_dx(dy, w, o, out=dx[G:G + R])
+        M.grouped_mm_dw(x, dy, o, out=dw[1:5])
+        for t in (y, dx):
+            assert bool((t[:G] == 7).all()) and bool((t[G + R:] == 7).all())
+        assert bool((dw[0] == 7).all()) and bool((dw[5] == 7).all())
+    xq, wq = torch.ones(R, K, dtype=torch.int8).cuda(), torch.ones(4, N, K, dtype=torch.int8).cuda()
+    y = torch.full((R + 2 * G, N), 7.0, dtype=bf, device="cuda")
+    M.grouped_mm_int8(xq, torch.ones(R).cuda(), wq, torch.ones(4, N).cuda(), o, out=y[G:G + R])
+    assert bool((y[:G] == 7).all()) and bool((y[G + R:] == 7).all())
+
+
+@pytest.mark.parametrize("out", [bf, f32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("counts,K,N", [BIG_CASES[i] for i in (0, 1, 2, 5, 6, 8)], ids=[BIG_IDS[i] for i in (0, 1, 2, 5, 6, 8)])
+def test_grouped_mm_int8_large_tiles(M, counts, K, N, out):
+    say(f"grouped_mm_int8 large counts={counts[:8]} K={K} N={N} {out}")
+    g = torch.Generator().manual_seed(K + N)
+    tail, R, E = 2, sum(counts), len(counts)
+    off = offs(counts, tail)
+    xq = torch.randint(-127, 128, (R + 2 * tail, K), dtype=torch.int8, generator=g).cuda()
+    wq = torch.randint(-127, 128, (E, N, K), dtype=torch.int8, generator=g).cuda()
+    xs, ws = (torch.rand(R + 2 * tail, generator=g) + 0.01).cuda(), (torch.rand(E, N, generator=g) * 1e-3).cuda()
+    y = torch.full((R + 2 * tail, N), 7.0, dtype=out, device="cuda")
+    M.grouped_mm_int8(xq, xs, wq, ws, off.cuda(), out=y)
+    assert bool((y[:tail] == 7).all()) and bool((y[R + tail:] == 7).all())
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        ref = ((xq[a:b].to(f64) @ wq[e].to(f64).T) * xs[a:b, None].to(f64) * ws[e].to(f64)).cpu()
+        check(y[a:b], ref, 3.1 * 2.0 ** -24 * ref.abs(), f"y of group {e}")
+
+
 # --------------------------------------------------------------------------- dropout
 def philox(seed, step, blocks):
     """[blocks, 8] 16-bit numbers of Philox4x32-10, in numpy's unsigned 64-bit integers."""
