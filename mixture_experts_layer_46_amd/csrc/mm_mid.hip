@@ -9,8 +9,11 @@
 // cycles a step, the same with every load out of range); reading a step ahead into a second
 // set of registers did not shorten it.
 //
-// fp32 runs the 16x16x4 instruction, at the card's full fp32 rate; its operands cost a
-// fraction of the time that the instructions take, so nothing else is done for it.
+// fp32 runs the 16x16x4 instruction, at the card's full fp32 rate.  Beside it every vector
+// instruction counts: the two never overlap (matrix and vector cycles together made up 91% of
+// all cycles, whatever else changed), so stages are constants of an unrolled loop, operand
+// resources and row guards scalar.  4096 rows, 2048 x 2048: 292 -> 258 us (dw 306 -> 258); 24
+// groups of 203 rows on average, 1032 x 712: 104 -> 90.
 #include "mm_tile.h"
 
 namespace moe {
@@ -50,8 +53,8 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
     const Reader<O::ES, O::kBCols, BN> rb(lane);
 
     // rows split evenly over the two wavefront rows, in 16-row blocks
-    const int half = min(BM / 2, (t.ni + 31) / 32 * 16), row0 = wm * half;
-    const int nblk = max(0, min(half, t.ni - row0) + 15) / 16;
+    const int half = min(BM / 2, (t.ni + 31) / 32 * 16), row0 = uni(wm * half);
+    const int nblk = uni(max(0, min(half, t.ni - row0) + 15) / 16);
     ACC acc[L::FM][L::FN];
 #pragma unroll
     for (int i = 0; i < L::FM; ++i)
@@ -65,20 +68,23 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
             oa.load(lds + q * L::kSub, wave * L::NA, q);
             ob.load(lds + q * L::kSub + BM * 64, wave * L::NB, q);
         }
-        int st = 0, nx = S - 1;                               // stage of these steps, and of the loads they start
-        for (int kt = 0; kt < KT; kt += U) {                  // steps past the end multiply the zeros their loads read
-            wait_vmcnt<(S - 2) * U * (L::NA + L::NB)>();
-            lds_barrier();
-            u32x4_t af[U][L::FM], bf[U][L::FN];
+        for (int kt = 0; kt < KT;) {                          // steps past the end multiply the zeros their loads read
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                read_and_load<O, BM, BN, 4>(lds + st * L::kStage + u * L::kSub, lds + nx * L::kStage + u * L::kSub,
-                                            kt + (S - 1) * U + u, row0 / 16, wn * L::FN, wave, oa, ob, ra, rb, af[u], bf[u]);
-            wait_lds();
+            for (int st = 0; st < S; ++st) {                  // stages as constants: no addresses to compute
+                if (kt >= KT) break;
+                wait_vmcnt<(S - 2) * U * (L::NA + L::NB)>();
+                lds_barrier();
+                u32x4_t af[U][L::FM], bf[U][L::FN];
+                const int nx = (st + S - 1) % S;
 #pragma unroll
-            for (int u = 0; u < U; ++u) mma_step<O::ELEM>(af[u], bf[u], acc, nblk);
-            st = st + 1 == S ? 0 : st + 1;
-            nx = nx + 1 == S ? 0 : nx + 1;
+                for (int u = 0; u < U; ++u)
+                    read_and_load<O, BM, BN, 4>(lds + st * L::kStage + u * L::kSub, lds + nx * L::kStage + u * L::kSub,
+                                                kt + (S - 1) * U + u, row0 / 16, wn * L::FN, wave, oa, ob, ra, rb, af[u], bf[u]);
+                wait_lds();
+#pragma unroll
+                for (int u = 0; u < U; ++u) mma_step<O::ELEM>(af[u], bf[u], acc, nblk);
+                kt += U;
+            }
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the last loads (zeros) land before LDS is reused
         __syncthreads();

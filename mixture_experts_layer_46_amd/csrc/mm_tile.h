@@ -103,19 +103,24 @@ struct Operand {
     }
     __device__ __forceinline__ void load(lds_char* stage, int first, int kt) const {
         if constexpr (COLS) {
-            const int left = (int)n - kt * kStep;
-            const uint32_t bytes = (uint32_t)(left < 0 ? 0 : left > kStep ? kStep : left) * ld;
+            // (as scalar minima: a clamp or a saturating difference would be a vector instruction,
+            // and the resource, then in vector registers, cost a loop over the lanes)
+            uint32_t k0 = min((uint32_t)kt * kStep, n);
+            asm("" : "+s"(k0));
+            const uint32_t bytes = min(n - k0, (uint32_t)kStep) * ld;
             const __amdgpu_buffer_rsrc_t r = make_rsrc((const void*)(base + (uint64_t)kt * kStep * ld), bytes);
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(stage + (first + i) * 1024), 16, off[i], 0, 0, 0);
         } else {
-            const uint32_t k0 = (uint32_t)kt * 64;
+            // the step's place as the scalar offset: a lane's own is fixed, but for the end of the
+            // contraction
+            const uint32_t k0 = min((uint32_t)kt * 64, cbytes), left = cbytes - k0;
             const __amdgpu_buffer_rsrc_t r = make_rsrc((const void*)base, n * ld);
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(stage + (first + i) * 1024), 16,
-                                                         (k0 + kq < cbytes && off[i] != kOOB) ? off[i] + k0 : kOOB, 0, 0, 0);
+                                                         kq < left ? off[i] : kOOB, (int)k0, 0, 0);
         }
     }
 };
@@ -173,9 +178,11 @@ __device__ __forceinline__ ACC mma(u32x4_t a, u32x4_t b, ACC c) {
 // only after every other pair's, so that none waits for the one before it.
 template <Elem E, typename ACC, int FM, int FN>
 __device__ __forceinline__ void mma_step(const u32x4_t (&af)[FM], const u32x4_t (&bf)[FN], ACC (&acc)[FM][FN], int nblk) {
+    // (compared anew each time: a scalar compare; masks that are kept cost vector instructions)
     if constexpr (E == Elem::f32) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s) {
+            if (!__builtin_constant_p(nblk)) asm volatile("" : "+s"(nblk));
 #pragma unroll
             for (int i = 0; i < FM; ++i)
                 if (__builtin_expect(i < nblk, 1)) {
@@ -184,7 +191,9 @@ __device__ __forceinline__ void mma_step(const u32x4_t (&af)[FM], const u32x4_t 
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(af[i][s]), __uint_as_float(bf[j][s]),
                                                                          acc[i][j], 0, 0, 0);
                 }
+        }
     } else {
+        if (!__builtin_constant_p(nblk)) asm volatile("" : "+s"(nblk));
 #pragma unroll
         for (int i = 0; i < FM; ++i)
             if (__builtin_expect(i < nblk, 1)) {
