@@ -161,7 +161,7 @@ hipError_t go_32(int kind, const MmArgs& a, hipStream_t st) {
     switch (kind) {
         case 0: return go<Op<0, Elem::f32>, BM, BN, 4, 1, float>(a, st);
         case 1: return go<Op<1, Elem::f32>, BM, BN, 4, 1, float>(a, st);
-        default: return go<Op<2, Elem::f32>, BM, BN, 4, 1, float>(a, st);
+        default: return go<Op<2, Elem::f32>, 64, 64, 4, 1, float>(a, st);          // the only form of these
     }
 }
 

@@ -9,9 +9,10 @@
 //
 // The three constants of a form come from some 10000 random calls (1-256 groups, 1-60000 rows,
 // matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every form.
-// Over those calls the form picked is 3.1% (16- and 8-bit operands), 2.3% (their weight
-// gradient), 3.7% and 1.3% (fp32) slower than the best one in the geometric mean; the best
-// single form would be 25%, 16%, 45% and 2% slower.
+// Over those calls the form picked is 2.2% (16- and 8-bit operands), 2.4% (their weight
+// gradient) and 1.6% (fp32) slower than the best one in the geometric mean; the best single
+// form would be 20%, 13% and 32% slower.  An fp32 weight gradient has one form: tiles of 64
+// are 0.6% from the best of two.
 #include <algorithm>
 #include <cmath>
 
@@ -38,11 +39,11 @@ constexpr Shape kShape[FORMS] = {{256, 256, 1, 1, 512, 5.0e6}, {128, 128, 2, 1, 
 struct Cost {
     double fixed, step, busy;     // us: per workgroup; per step alone; per step and workgroup of a full CU
 };
-// the forms that do not exist (fp32 LARGE, THIN weight gradients) have no cost
-constexpr Cost kRows16[FORMS] = {{3.4, .42, .85}, {2.3, .33, .29}, {2.05, .14, .121}, {2.1, .25, .32}, {2.4, .51, .05}};
-constexpr Cost kWeights16[FORMS] = {{4.3, .95, 1.0}, {2.35, .56, .29}, {1.75, .23, .141}, {}, {}};
-constexpr Cost kRows32[FORMS] = {{}, {2.1, .95, .95}, {1.66, .33, .25}, {2.5, .53, .55}, {2.6, .68, .22}};
-constexpr Cost kWeights32[FORMS] = {{}, {1.63, .45, 1.09}, {1.0, .47, .244}, {}, {}};
+// the forms that do not exist (fp32 LARGE, THIN weight gradients, fp32 MID128 ones) have no cost
+constexpr Cost kRows16[FORMS] = {{3.7, .38, .64}, {2.1, .37, .25}, {2.1, .16, .14}, {2.8, .25, .35}, {2.2, .69, .05}};
+constexpr Cost kWeights16[FORMS] = {{4.0, .52, 1.0}, {2.35, .40, .27}, {1.6, .20, .13}, {}, {}};
+constexpr Cost kRows32[FORMS] = {{}, {2.7, .95, .71}, {1.3, .40, .17}, {3.3, .62, .50}, {3.0, .71, .22}};
+constexpr Cost kWeights32[FORMS] = {{}, {}, {1.0, .34, .23}, {}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
 const Cost* costs(int kind, int dtype) {
@@ -87,7 +88,9 @@ double estimate(int kind, int dtype, const MmArgs& a, int form) {
 }  // namespace
 
 bool mm_fits(int kind, int dtype, const MmArgs& a) {
-    return fits(kind, a, kind != 3 && dtype == MOE_F32 ? MID128 : LARGE);
+    for (int f = 0; f < FORMS; ++f)
+        if (costs(kind, dtype)[f].fixed != 0 && fits(kind, a, f)) return true;
+    return false;
 }
 
 hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
