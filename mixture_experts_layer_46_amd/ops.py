@@ -422,7 +422,8 @@ def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
 def combine_grad(dout, y_perm, row_of_pair, topk_w):
     """The gradient of combine: (dy_perm [R, H], dtopk_w [T, k]) for dout [T, H], y_perm [R, H]
     (bf16 or fp32), row_of_pair [T*k] int32 and topk_w [T, k] fp32.  A dropped pair (row -1)
-    has dtopk_w 0; rows of dy_perm that no pair names are unset."""
+    has dtopk_w 0; rows of dy_perm that no pair names are unset.  No two pairs may name one
+    row (permute's never do)."""
     _dims(dout, 2, "dout")
     _dims(y_perm, 2, "y_perm")
     _dims(topk_w, 2, "topk_w")
@@ -485,10 +486,22 @@ def forward_int8(x, w_gate, experts: QuantizedExperts, top_k, bias=None, flags=0
 
 
 # ----------------------------------------------------------------- the layer, trained
+def _tall_dw(x, dy):
+    """x^T dy [K, N] of tall fp32 x [T, K], dy [T, N]: a grouped product with the rows cut into
+    enough groups to fill the GPU (512 tiles of 64 x 64), and their results added.  8192 rows,
+    4096 x 64: 171 -> 58 us, 65536 rows, 1024 x 64: 1373 -> 108.  (torch's own sum over the rows would not replay right from a
+    captured graph: it clears memory with a node of its own.)"""
+    T, tiles = x.shape[0], -(-x.shape[1] // 64) * -(-dy.shape[1] // 64)
+    n = max(1, min(512 // tiles, T // 256, 64))
+    cut = torch.arange(n + 1, dtype=torch.int64, device=x.device).mul_(T).div_(n, rounding_mode="floor").int()
+    d = grouped_mm_dw(x, dy, cut)
+    return d[0] if n == 1 else d.sum(dim=0)
+
+
 class _Route(torch.autograd.Function):
     """Gates of the chosen experts.  g = softmax over the chosen logits (the renormalised
     gates are that), so dl_j = g_j (dg_j - sum_i g_i dg_i), and by the gate projection
-    dW_g = x^T dl, dx = dl W_g^T: two grouped products of one group, in fp32."""
+    dW_g = x^T dl, dx = dl W_g^T: grouped products, in fp32."""
 
     @staticmethod
     def forward(ctx, x, w_gate, bias, top_k, flags):
@@ -508,17 +521,18 @@ class _Route(torch.autograd.Function):
         Ep = (E + 7) // 8 * 8                             # the products take multiples of 8
         dl = torch.zeros((T, Ep), dtype=torch.float32, device=x.device)
         dl.scatter_(1, idx.long(), g * (dg - (g * dg).sum(dim=1, keepdim=True)))
-        one = torch.arange(2, dtype=torch.int32, device=x.device) * T
         dx = dw = db = None
         if ctx.needs_input_grad[0]:
             wp = w_gate if Ep == E else torch.nn.functional.pad(w_gate, (0, Ep - E))
+            one = torch.arange(2, dtype=torch.int32, device=x.device) * T
             dx = grouped_mm_dx(dl, wp.unsqueeze(0), one).to(x.dtype)
         if ctx.needs_input_grad[1]:
-            dw = grouped_mm_dw(x.float(), dl, one)[0, :, :E]
+            dw = _tall_dw(x.float(), dl)[:, :E]
         if ctx.needs_input_grad[2]:
-            db = torch.zeros(E, dtype=torch.float32, device=x.device)
-            if not ctx.flags & MOE_FLAG_BIAS_SELECT_ONLY:
-                db = dl[:, :E].sum(dim=0)
+            if ctx.flags & MOE_FLAG_BIAS_SELECT_ONLY:
+                db = torch.zeros(E, dtype=torch.float32, device=x.device)
+            else:
+                db = _tall_dw(torch.ones((T, 8), dtype=torch.float32, device=x.device), dl)[0, :E]
         return dx, dw, db, None, None
 
 
@@ -563,7 +577,10 @@ def forward_train(x, w_gate, w_in, w_up, w_out, top_k, bias=None, dropout_p=0.0,
     """The whole layer (forward), differentiable in x, w_gate, w_in, w_up, w_out and bias, with
     dropout of the experts' activated hidden rows (dropout_p, seed, step as in dropout; the
     hidden rows are the tensor, in grouped order).  Returns out [T, H].  The choice of the
-    experts has no gradient; the gates have.  MOE_FLAG_NO_RENORM is not supported."""
+    experts has no gradient; the gates have.  MOE_FLAG_NO_RENORM is not supported.
+
+    A pass and its gradients may be captured into a graph, as torch asks: with no graph of
+    an uncaptured pass over the same leaves still alive (delete earlier outputs first)."""
     import mixture_experts_layer_46_amd as M
     T, H, E, F = M._check_layer(x, w_gate, bias, w_in, w_up, w_out, None, top_k)
     if flags & MOE_FLAG_NO_RENORM:
