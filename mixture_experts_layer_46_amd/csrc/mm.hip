@@ -1,16 +1,13 @@
 // Grouped products, large tiles: 256 x 256 on the matrix cores, one tile per workgroup
 // (mm_tile.h has the kinds, the operand layouts and the loads, mm_large.h the tile's division).
-// Two forms of the inner loop:
-//   woven       within a step every wavefront multiplies the operands it holds in registers,
-//               reads the next step's from LDS and starts the loads of the fourth step after,
-//               spread between the matrix instructions; one barrier a step.
-//   step-apart  the wavefronts of the upper and of the lower rows (one of each per SIMD) run
-//               half a step out of phase: while one reads its operands and starts loads, the
-//               other's matrix instructions run; two barriers a step.
-// Operands in `columns` layout take twice the LDS reads, which the step-apart form cannot
-// hide in half a step: woven there (kinds 0 and 2; 8 experts, 8192 rows, 4096 <-> 14336: 912
-// against 947 us and 975 against 1042), step-apart for kinds 1 and 3 (994 against 1016, int8
-// 506 against 515; 4096^3: 107.6 against 113.2).
+//
+// The wavefronts of the upper and of the lower rows (one of each per SIMD) run half a step out
+// of phase: while one reads its operands and starts loads, the other's matrix instructions
+// run; two barriers a step.  Against steps in which every wavefront does both, woven together,
+// with one barrier: x W 862 against 906 us, dy W^T 995 against 1017, x^T dy 890 against 926 (8
+// experts, 8192 rows, 4096 x 14336 bf16; 1.12, 0.97 and 1.08 PFLOP/s), int8 504 against 514
+// (1.91 PFLOP/s); 4096^3 bf16: 110, 109 and 108 us.  What is left: the last, partial round of
+// tiles (dy W^T: 2.25 rounds take three), and a tile's first loads and output, 3 to 4 us.
 #include "mm_large.h"
 
 namespace moe {
@@ -22,11 +19,9 @@ using namespace large;
 constexpr int kCS = kT + 8;                   // bf16 per row of the output staging tile
 constexpr size_t kLds = (size_t)kT * kCS * 2; // staging tile; the stages (128 KB) lie inside
 static_assert(kStages * kStage <= (int)kLds, "the stages fit below the staging tile's end");
-template <typename O>
-constexpr bool kApart = !O::kACols && !O::kBCols;
 
-// The steps of one of the two wavefront groups, in step-apart form (below).  Between two
-// barriers one group is in its read phase (R) and the other in its matrix phase (M):
+// The steps of one of the two wavefront groups.  Between two barriers one group is in its read
+// phase (R) and the other in its matrix phase (M):
 //   group 0:  R0 | M0 | R1 | M1 | ... | M(KT-1) | (idle)
 //   group 1: (idle) | R0 | M0 | R1 | ... | R(KT-1) | M(KT-1)
 // R(k) starts the loads of step k + 3 into the stage that held step k - 1, which both groups
@@ -83,8 +78,7 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
     ob.plan(wave * kLoads, lane, t.nj);
 
     // this wavefront's rows, in 16-row blocks: the tile's, split evenly over the two groups
-    // where one group's products wait for the other's
-    const int half = kApart<O> ? min(128, (t.ni + 31) / 32 * 16) : 128, row0 = uni(wm * half);
+    const int half = min(128, (t.ni + 31) / 32 * 16), row0 = uni(wm * half);
     const int nblk = uni(max(0, min(half, t.ni - row0) + 15) / 16);
     typename O::Acc acc[8][4];
 #pragma unroll
@@ -96,36 +90,15 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
     if (KT > 0) {
         const Reader<O::ES, O::kACols, kT> ra(lane);
         const Reader<O::ES, O::kBCols, kT> rb(lane);
-        if constexpr (kApart<O>) {
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                oa.load(lds + s * kStage, wave * kLoads, s);
-                ob.load(lds + s * kStage + kT * 64, wave * kLoads, s);
-            }
-            wait_vmcnt<kVmcnt>();
-            lds_barrier();
-            if (wm == 0) steps<O, 0>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
-            else steps<O, 1>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
-        } else {
-#pragma unroll
-            for (int s = 0; s < kStages; ++s) {
-                oa.load(lds + s * kStage, wave * kLoads, s);
-                ob.load(lds + s * kStage + kT * 64, wave * kLoads, s);
-            }
-            wait_vmcnt<3 * 2 * kLoads>();
-            lds_barrier();
-            u32x4_t a0[8], b0[4], a1[8], b1[4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a0[i] = ra(lds, wm * 8 + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b0[j] = rb(lds + kT * 64, wn * 4 + j);
-            // two steps a turn (an odd last one multiplies the zeros that its loads read)
-            for (int kt = 0; kt < KT; kt += 2) {
-                lds_char *s0 = lds + (kt & 3) * kStage, *s1 = lds + ((kt + 1) & 3) * kStage, *s2 = lds + ((kt + 2) & 3) * kStage;
-                step<O>(s1, s0, kt + 4, nblk, wm, wn, wave, oa, ob, ra, rb, a0, b0, a1, b1, acc);
-                step<O>(s2, s1, kt + 5, nblk, wm, wn, wave, oa, ob, ra, rb, a1, b1, a0, b0, acc);
-            }
+        for (int s = 0; s < 3; ++s) {
+            oa.load(lds + s * kStage, wave * kLoads, s);
+            ob.load(lds + s * kStage + kT * 64, wave * kLoads, s);
         }
+        wait_vmcnt<kVmcnt>();
+        lds_barrier();
+        if (wm == 0) steps<O, 0>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
+        else steps<O, 1>(lds, KT, nblk, row0 / 16, wn, wave, oa, ob, ra, rb, acc);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the last loads (zeros) land before LDS is reused
         __syncthreads();
     }
@@ -192,11 +165,13 @@ hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t
         case 0: return go<Op<0, Elem::bf16>, bf16_t>(a, st);
         case 1: return go<Op<1, Elem::bf16>, bf16_t>(a, st);
         case 2: {
-            // Few rows a group: the time is the writing of the matrices, which many workgroups
-            // at once do better (64 experts, 2048 x 1408: 2 rows a group 85 us here, 94 there;
-            // 32 rows 90 and 95; 64 rows 103 and 96; 256 rows 168 and 151).
-            const int groups = a.rows < a.E ? a.rows : a.E;
-            if (a.rows >= 48ll * groups && a.rows > 0) return launch_mm_stream(out_dtype, a, st);
+            // Groups of middling size go in a stream of tiles.  Smaller ones are a matter of
+            // writing the matrices, which many workgroups at once do better; larger ones of the
+            // steps themselves.  Here and there, in us: 64 experts, 2048 x 1408, rows a group 32:
+            // 85 and 95, 64: 95 and 95, 256: 153 and 150; 8 experts, 4096 x 4096, 64: 76 and 65;
+            // 256 experts, 1024 x 512, 234: 105 and 101; 8 experts, 4096 x 14336, 1024: 890 and 921.
+            const long long groups = a.rows < a.E ? a.rows : a.E;
+            if (a.rows >= 48 * groups && a.rows < 640 * groups) return launch_mm_stream(out_dtype, a, st);
             return f ? go<Op<2, Elem::bf16>, float>(a, st) : go<Op<2, Elem::bf16>, bf16_t>(a, st);
         }
         default: return f ? go<Op<3, Elem::i8>, float>(a, st) : go<Op<3, Elem::i8>, bf16_t>(a, st);

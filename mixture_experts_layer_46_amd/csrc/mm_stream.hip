@@ -1,13 +1,13 @@
-// Weight gradients in large tiles (kind 2 of mm_tile.h, bf16): 256 x 256 on the matrix cores,
-// the steps of mm_large.h.
+// Weight gradients of groups of middling size in large tiles (kind 2 of mm_tile.h, bf16):
+// 256 x 256 on the matrix cores.
 //
+// The contractions, a group's rows, are short, so that what stands between two tiles counts.
 // The grid is persistent and the steps of a workgroup's tiles form one stream: the last four
-// steps of a tile load the first four stages of the next, so that between two tiles stand
-// the output and one table look-up.  It counts because the contractions, a group's rows, are
-// short.  Against one tile per workgroup (mm.hip): 64 experts of 256 rows, 2048 x 1408, 168
-// -> 151 us; of 64 rows, 103 -> 96; 256 experts of 234 rows, 1024 x 512, 114 -> 101; 8
-// experts of 1024 rows, 4096 x 14336, 951 -> 941 (1.02 PFLOP/s).  Kind 0, whose contractions
-// are long, loses 1-4% with it.
+// steps of a tile load the first four stages of the next, and between two tiles stand the
+// output and one table look-up.  Within a step a wavefront multiplies the operands it holds in
+// registers, reads the next step's from LDS and starts the loads of the fourth step after,
+// spread between the matrix instructions; one barrier a step.  (mm.hip's two groups half a
+// step apart are faster step by step, but its tiles share no loads.)
 #include "mm_large.h"
 
 namespace moe {
@@ -19,6 +19,46 @@ using O = Op<2, Elem::bf16>;
 
 constexpr int kCS = kT + 8;                   // bf16 per row of the output piece
 constexpr size_t kLds = (size_t)kStages * kStage + 32 * kCS * 2;      // stages; 32 rows on their way out
+
+// One step: the products of the operands in registers, with the next step's operands read
+// from stage `rd` and a later step's loads started into stage `wr` in between (two reads
+// after each of six row blocks, the loads after the third and the fifth: measured against
+// denser and later placements, 1-4% on the large shapes).  The matrix instruction takes the
+// B operand first, so that a lane's four sums are four columns of one row.
+// The stages are separate __restrict__ arguments: otherwise the compiler takes the
+// transposing reads to touch what is in flight, and waits for every load before them.
+__device__ __attribute__((always_inline)) inline void step(const lds_char* __restrict__ rd, lds_char* __restrict__ wr,
+                                                           int kload, int nblk, int wm, int wn, int wave,
+                                                           const OpA<O>& oa, const OpB<O>& ob,
+                                                           const Reader<O::ES, O::kACols, kT>& ra,
+                                                           const Reader<O::ES, O::kBCols, kT>& rb,
+                                                           const u32x4_t (&af)[8], const u32x4_t (&bf)[4],
+                                                           u32x4_t (&an)[8], u32x4_t (&bn)[4],
+                                                           O::Acc (&acc)[8][4]) {
+    asm volatile("" : "+s"(nblk));    // compared anew at each row block (a scalar compare; kept masks cost vector ones)
+    wait_lds();                       // this step's operands are in registers: their stage is free
+    wait_vmcnt<kVmcnt>();             // this wavefront's loads of the next step have landed
+    lds_barrier();                    // everyone's
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (__builtin_expect(i < nblk, 1)) {                  // a full tile falls through
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mma<O::ELEM>(bf[j], af[i], acc[i][j]);
+        }
+#pragma unroll
+        for (int q = 2 * i; q < 2 * i + 2; ++q) {
+            if (q < 4) bn[q] = rb(rd + kT * 64, wn * 4 + q);
+            else if (q < 12) an[q - 4] = ra(rd, wm * 8 + q - 4);
+        }
+        if (i == 2) oa.load(wr, wave * kLoads, kload);
+        if (i == 4) ob.load(wr + kT * 64, wave * kLoads, kload);
+    }
+    // the sums live in accumulator registers, next to the two sets of operands
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
 
 // A finished tile, one rounding.  Lane l holds row l & 15 and columns 4 (l >> 4) .. + 3 of each
 // 16 x 16 block.  bf16 goes out in whole rows of 512 bytes: 16 rows of the upper and 16 of the
@@ -133,8 +173,8 @@ __global__ __launch_bounds__(512, 1) void k_mm_stream(MmArgs a) {
                 }
             }
             lds_char *s0 = lds + (g & 3) * kStage, *s1 = lds + ((g + 1) & 3) * kStage, *s2 = lds + ((g + 2) & 3) * kStage;
-            step<O>(s1, s0, kload, nblk, wm, wn, wave, oa, ob, ra, rb, a0, b0, a1, b1, acc);
-            step<O>(s2, s1, kload + 1, nblk, wm, wn, wave, oa, ob, ra, rb, a1, b1, a0, b0, acc);
+            step(s1, s0, kload, nblk, wm, wn, wave, oa, ob, ra, rb, a0, b0, a1, b1, acc);
+            step(s2, s1, kload + 1, nblk, wm, wn, wave, oa, ob, ra, rb, a1, b1, a0, b0, acc);
         }
         store_tile<OUT>(a, cur, lds + kStages * kStage, nblk, wm, wn, acc);
         if (next < 0) break;

@@ -6,6 +6,10 @@
 // in LDS stages of its own: no barrier and no other wavefront's loads stand between it and
 // memory.  At the end the wavefronts' sums meet in LDS and are added in wavefront order (so
 // the result does not depend on scheduling), scaled and rounded once.
+//
+// 8 experts of 2 rows, 4096 x 14336 bf16: 140 us, 5.9 TB/s (16-row tiles 147); one row, 4096 x
+// 4096: 10.9 us with 16-row tiles, whose eight wavefronts have twice the steps in flight
+// (32-row 11.3, tiles of 64 19).  Three stages: four and six measured the same.
 #include "mm_tile.h"
 
 namespace moe {

@@ -1,4 +1,5 @@
-// Building blocks of the grouped products' kernels (mm.hip, mm_mid.hip, mm_thin.hip).
+// Building blocks of the grouped products' kernels (mm.hip, mm_stream.hip, mm_mid.hip,
+// mm_thin.hip).
 //
 //   kind 0  y[r, n]     = sum_k x[r, k] w[e, k, n]     (rows r of group e)
 //   kind 1  dx[r, k]    = sum_n dy[r, n] w[e, k, n]
