@@ -1,19 +1,23 @@
 // Grouped products, tiles of 64 and 128: for groups or matrices too small to fill the chip
 // with 256 x 256 tiles, and for fp32 (mm_tile.h has the kinds, layouts and loads).
 //
-// Four wavefronts, 2 x 2 over the tile; S stages of U steps in LDS with the loads S - 1 stages
-// ahead and one barrier per stage: a wavefront that passes a stage's barrier has finished
-// the stage before, which the loads then fill.  Two or more workgroups share a CU and cover
-// each other's waits, where the large kernel needs its two groups.  A workgroup alone on its
-// CU runs at the length of its own chain (barrier, LDS reads, products, addresses: some 400
-// cycles a step, the same with every load out of range); reading a step ahead into a second
-// set of registers did not shorten it.
+// Four wavefronts, 2 x 2 over the tile; S stages of U steps in LDS and one barrier per stage.
+// Two or more workgroups share a CU and cover each other's waits, where the large kernel needs
+// its two groups.
 //
-// fp32 runs the 16x16x4 instruction, at the card's full fp32 rate.  Beside it every vector
-// instruction counts: the two never overlap (matrix and vector cycles together made up 91% of
-// all cycles, whatever else changed), so stages are constants of an unrolled loop, operand
-// resources and row guards scalar.  4096 rows, 2048 x 2048: 292 -> 258 us (dw 306 -> 258); 24
-// groups of 203 rows on average, 1032 x 712: 104 -> 90.
+// 16 and 8 bits: loads S - 1 stages ahead; a wavefront that passes a stage's barrier has
+// finished the stage before, which the loads then fill.  A workgroup alone on its CU runs at
+// the length of its own chain (barrier, LDS reads, products, addresses: some 400 cycles a
+// step, the same with every load out of range); reading a step ahead into a second set of
+// registers lost 2 to 15% with several workgroups a CU and won 5% at best with one.
+//
+// fp32 runs the 16x16x4 instruction, at the card's full fp32 rate, and reads a step ahead (3 to
+// 7% there).  Beside that instruction every vector instruction counts: the two never overlap
+// (matrix and vector cycles together made up 91% of all cycles, whatever else changed), so
+// stages are constants of an unrolled loop, operand resources and row guards scalar.  4096
+// rows, 2048 x 2048: 292 -> 255 us (dw 306 -> 250, 137 TFLOP/s); 24 groups of 203 rows on
+// average, 1032 x 712: 104 -> 92 (dx 94 -> 81, dw 98 -> 87), a single round of tiles, which
+// starts and ends with idle matrix units.
 #include "mm_tile.h"
 
 namespace moe {
@@ -29,6 +33,31 @@ struct Mid {
     static constexpr size_t kOut = (size_t)BM * kCS * 2;
     static constexpr size_t kLds = kOut > (size_t)S * kStage ? kOut : (size_t)S * kStage;
 };
+
+// One fp32 step: the products of the operands in registers, with the next step's read from
+// stage `rd` after the first and a later step's loads started into stage `wr` after the second
+// of the four instructions per pair of blocks (stages as separate arguments: see read_and_load).
+template <typename O, int BM, int BN, int S, typename OA, typename OB, typename RA, typename RB, int FM, int FN>
+__device__ __attribute__((always_inline)) inline void step_f32(const lds_char* __restrict__ rd, lds_char* __restrict__ wr,
+                                                               int kload, int nblk, int ablk, int bblk, int wave,
+                                                               const OA& oa, const OB& ob, const RA& ra, const RB& rb,
+                                                               const u32x4_t (&af)[FM], const u32x4_t (&bf)[FN],
+                                                               u32x4_t (&an)[FM], u32x4_t (&bn)[FN],
+                                                               f32x4_t (&acc)[FM][FN]) {
+    constexpr int NA = BM / 64, NB = BN / 64;
+    wait_lds();                               // this step's operands are in registers: their stage is free
+    wait_vmcnt<(S - 2) * (NA + NB)>();        // this wavefront's loads of the next step have landed
+    lds_barrier();                            // everyone's
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        mma_f32(af, bf, s, acc, nblk);
+        if (s == 0) read_stage<BM>(rd, ablk, bblk, ra, rb, an, bn);
+        if (s == 1) {
+            oa.load(wr, wave * NA, kload);
+            ob.load(wr + BM * 64, wave * NB, kload);
+        }
+    }
+}
 
 template <typename O, int BM, int BN, int S, int U, typename OUT>
 __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
@@ -62,7 +91,31 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
         for (int j = 0; j < L::FN; ++j) acc[i][j] = ACC{0, 0, 0, 0};
 
     const int KT = (t.C + O::kStep - 1) / O::kStep;
-    if (KT > 0) {
+    if constexpr (O::ELEM == Elem::f32) {
+        if (KT > 0) {
+            static_assert(U == 1 && S % 2 == 0, "two sets of operands take turns");
+#pragma unroll
+            for (int q = 0; q < S; ++q) {
+                oa.load(lds + q * L::kStage, wave * L::NA, q);
+                ob.load(lds + q * L::kStage + BM * 64, wave * L::NB, q);
+            }
+            wait_vmcnt<(S - 1) * (L::NA + L::NB)>();
+            lds_barrier();
+            u32x4_t af[2][L::FM], bf[2][L::FN];
+            const int ablk = row0 / 16, bblk = wn * L::FN;
+            read_stage<BM>(lds, ablk, bblk, ra, rb, af[0], bf[0]);
+            for (int kt = 0; kt < KT;) {
+#pragma unroll
+                for (int st = 0; st < S; ++st) {              // stages as constants: no addresses to compute
+                    if (kt >= KT) break;
+                    step_f32<O, BM, BN, S>(lds + (st + 1) % S * L::kStage, lds + st * L::kStage, kt + S, nblk, ablk, bblk, wave,
+                                           oa, ob, ra, rb, af[st % 2], bf[st % 2], af[1 - st % 2], bf[1 - st % 2], acc);
+                    ++kt;
+                }
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+    } else if (KT > 0) {
 #pragma unroll
         for (int q = 0; q < (S - 1) * U; ++q) {
             oa.load(lds + q * L::kSub, wave * L::NA, q);

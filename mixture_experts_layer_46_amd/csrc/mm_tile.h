@@ -174,25 +174,30 @@ __device__ __forceinline__ ACC mma(u32x4_t a, u32x4_t b, ACC c) {
                                                      0, 0);
 }
 
-// One step's products of a wavefront: its first `nblk` row blocks (a full tile falls through
-// the guards).  fp32 takes four instructions per pair of blocks, which follow each other
-// only after every other pair's, so that none waits for the one before it.
+// One fp32 instruction (`s` of the four a step) for each pair of blocks of a wavefront's first
+// `nblk` row blocks.  (The guards, which a full tile falls through, are compared anew each
+// time: scalar compares; masks that are kept cost vector instructions.)
+template <int FM, int FN>
+__device__ __forceinline__ void mma_f32(const u32x4_t (&af)[FM], const u32x4_t (&bf)[FN], int s, f32x4_t (&acc)[FM][FN],
+                                        int nblk) {
+    if (!__builtin_constant_p(nblk)) asm volatile("" : "+s"(nblk));
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        if (__builtin_expect(i < nblk, 1)) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(af[i][s]), __uint_as_float(bf[j][s]),
+                                                                 acc[i][j], 0, 0, 0);
+        }
+}
+
+// One step's products of a wavefront.  fp32 takes four instructions per pair of blocks, which
+// follow each other only after every other pair's, so that none waits for the one before it.
 template <Elem E, typename ACC, int FM, int FN>
 __device__ __forceinline__ void mma_step(const u32x4_t (&af)[FM], const u32x4_t (&bf)[FN], ACC (&acc)[FM][FN], int nblk) {
-    // (compared anew each time: a scalar compare; masks that are kept cost vector instructions)
     if constexpr (E == Elem::f32) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (!__builtin_constant_p(nblk)) asm volatile("" : "+s"(nblk));
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                if (__builtin_expect(i < nblk, 1)) {
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(af[i][s]), __uint_as_float(bf[j][s]),
-                                                                         acc[i][j], 0, 0, 0);
-                }
-        }
+        for (int s = 0; s < 4; ++s) mma_f32(af, bf, s, acc, nblk);
     } else {
         if (!__builtin_constant_p(nblk)) asm volatile("" : "+s"(nblk));
 #pragma unroll
