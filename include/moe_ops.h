@@ -33,8 +33,8 @@ extern "C" {
  * offsets[E] on belong to no group.  Offsets must not decrease; whatever they hold,
  * nothing outside the buffers is read or written.
  * Limits: 0 <= rows < 2^30; 1 <= E <= 256; K and N multiples of 8, at most 2^20; the output's
- * tiles within one launch (2^23 of 256 x 256; fp32 2^24 of 128 x 128, moe_grouped_mm_dw of
- * 64 x 64; MOE_ERR_UNSUPPORTED beyond).  moe_grouped_mm_int8: K a multiple of 16, at most 131056, so that no 32-bit sum
+ * tiles within one launch (2^23 of 256 x 256, fp32 2^24 of 64 x 64; MOE_ERR_UNSUPPORTED
+ * beyond).  moe_grouped_mm_int8: K a multiple of 16, at most 131056, so that no 32-bit sum
  * can overflow. */
 typedef struct {
     int64_t  rows;

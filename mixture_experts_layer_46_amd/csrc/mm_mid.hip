@@ -209,12 +209,11 @@ hipError_t go_16(int kind, bool f, const MmArgs& a, hipStream_t st) {
     }
 }
 
-template <int BM, int BN>
 hipError_t go_32(int kind, const MmArgs& a, hipStream_t st) {
     switch (kind) {
-        case 0: return go<Op<0, Elem::f32>, BM, BN, 4, 1, float>(a, st);
-        case 1: return go<Op<1, Elem::f32>, BM, BN, 4, 1, float>(a, st);
-        default: return go<Op<2, Elem::f32>, 64, 64, 4, 1, float>(a, st);          // the only form of these
+        case 0: return go<Op<0, Elem::f32>, 64, 64, 4, 1, float>(a, st);
+        case 1: return go<Op<1, Elem::f32>, 64, 64, 4, 1, float>(a, st);
+        default: return go<Op<2, Elem::f32>, 64, 64, 4, 1, float>(a, st);
     }
 }
 
@@ -222,9 +221,9 @@ hipError_t go_32(int kind, const MmArgs& a, hipStream_t st) {
 
 // Two steps a barrier for tiles of 64 (16 and 8 bits): 256 rows, 4096 x 4096 transposed 22.8 ->
 // 21.6 us, 512 rows 34.7 -> 32.8, int8 19.0 -> 17.3; tiles of 128 and fp32, whose steps are
-// longer, lose by it (208 rows a group, fp32 weight gradient 89 -> 96).
+// longer, lose by it (208 rows a group, fp32 weight gradient 89 -> 96).  fp32 has tiles of 64 only.
 hipError_t launch_mm_mid(int tile, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
-    if (kind != 3 && dtype == MOE_F32) return tile == 64 ? go_32<64, 64>(kind, a, st) : go_32<128, 128>(kind, a, st);
+    if (kind != 3 && dtype == MOE_F32) return go_32(kind, a, st);
     const bool f = out_dtype == MOE_F32;
     return tile == 64 ? go_16<64, 64, 3, 2>(kind, f, a, st) : go_16<128, 128, 4, 1>(kind, f, a, st);
 }

@@ -7,12 +7,12 @@
 // each step the larger of its latency when a workgroup is alone and of its share of a full
 // CU; the bytes that every form has to move bound the whole from below.
 //
-// The three constants of a form come from some 10000 random calls (1-256 groups, 1-60000 rows,
+// The three constants of a form come from some 12000 random calls (1-256 groups, 1-60000 rows,
 // matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every form.
-// Over those calls the form picked is 2.2% (16- and 8-bit operands), 2.4% (their weight
-// gradient) and 1.6% (fp32) slower than the best one in the geometric mean; the best single
-// form would be 20%, 13% and 32% slower.  An fp32 weight gradient has one form: tiles of 64
-// are 0.6% from the best of two.
+// Over calls that the fit did not see, the form picked is slower than the best one by 1.4% (x W),
+// 2.6% (dy W^T), 1.8% (x^T dy), 1.4% (int8) and 1.1% (fp32) in the geometric mean; the best
+// single form would be 20%, 20%, 13%, 20% and 32% slower.  fp32 has no tiles of 128: they won
+// 0.05% (weight gradients 0.6%) over the other forms.
 #include <algorithm>
 #include <cmath>
 
@@ -39,16 +39,19 @@ constexpr Shape kShape[FORMS] = {{256, 256, 1, 1, 512, 5.0e6}, {128, 128, 2, 1, 
 struct Cost {
     double fixed, step, busy;     // us: per workgroup; per step alone; per step and workgroup of a full CU
 };
-// the forms that do not exist (fp32 LARGE, THIN weight gradients, fp32 MID128 ones) have no cost
-constexpr Cost kRows16[FORMS] = {{3.7, .38, .64}, {2.1, .37, .25}, {2.1, .16, .14}, {2.8, .25, .35}, {2.2, .69, .05}};
-constexpr Cost kWeights16[FORMS] = {{4.0, .52, 1.0}, {2.35, .40, .27}, {1.6, .20, .13}, {}, {}};
-constexpr Cost kRows32[FORMS] = {{}, {2.7, .95, .71}, {1.3, .40, .17}, {3.3, .62, .50}, {3.0, .71, .22}};
-constexpr Cost kWeights32[FORMS] = {{}, {}, {1.0, .34, .23}, {}, {}};
+// the forms that do not exist (fp32 LARGE and MID128, THIN weight gradients) have no cost
+constexpr Cost kY16[FORMS] = {{1.85, .38, .54}, {1.9, .38, .25}, {2.15, .24, .146}, {2.15, .23, .59}, {3.55, .89, .042}};
+constexpr Cost kDx16[FORMS] = {{1.85, .38, .59}, {1.8, .385, .24}, {1.85, .096, .14}, {3.75, .25, .34}, {2.55, .69, .039}};
+constexpr Cost kDw16[FORMS] = {{3.4, .52, 1.0}, {2.1, .34, .28}, {2.0, .20, .116}, {}, {}};
+constexpr Cost kInt8[FORMS] = {{3.0, .33, .68}, {2.0, .44, .24}, {2.2, .21, .118}, {2.25, .25, .48}, {2.5, .69, .05}};
+constexpr Cost kRows32[FORMS] = {{}, {}, {1.05, .52, .10}, {3.95, .545, .45}, {2.15, .96, .187}};
+constexpr Cost kDw32[FORMS] = {{}, {}, {1.0, .34, .23}, {}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
 const Cost* costs(int kind, int dtype) {
-    const bool f32 = kind != 3 && dtype == MOE_F32;
-    return kind == 2 ? (f32 ? kWeights32 : kWeights16) : (f32 ? kRows32 : kRows16);
+    if (kind == 3) return kInt8;
+    if (dtype == MOE_F32) return kind == 2 ? kDw32 : kRows32;
+    return kind == 0 ? kY16 : kind == 1 ? kDx16 : kDw16;
 }
 
 long long blocks_of(int kind, const MmArgs& a, const Shape& s) {
