@@ -237,17 +237,23 @@ def forward(shape: Shape, x, w_gate, bias, w_in, w_up, w_out, out, workspace, st
                                                          _ptr(workspace), nbytes, arr, _stream(stream)))
 
 
-_functions = {}
+operators = {}                        # functions of moe_ops.h that were called before
+
+
+def operator(name: str):
+    fn = operators[name] = getattr(load(), name)
+    return fn
+
+
+def failed(name: str, code: int):
+    raise MoeError(name, code, load().moe_last_error().decode())
 
 
 def call(name: str, *args):
     """One call of an operator of moe_ops.h; raises MoeError on a non-OK status."""
-    fn = _functions.get(name)
-    if fn is None:
-        fn = _functions[name] = getattr(load(), name)
-    code = fn(*args)
+    code = (operators.get(name) or operator(name))(*args)
     if code != 0:
-        raise MoeError(name, code, load().moe_last_error().decode())
+        failed(name, code)
 
 
 NOALLOC_SCRATCH_BYTES = 256 << 20

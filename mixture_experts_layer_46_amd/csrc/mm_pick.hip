@@ -64,7 +64,7 @@ long long blocks_of(int kind, const MmArgs& a, const Shape& s) {
 // A launch holds at most 2^32 threads in a dimension.
 bool fits(int kind, const MmArgs& a, int form) { return blocks_of(kind, a, kShape[form]) * kShape[form].threads < (1ll << 32); }
 
-double estimate(int kind, int dtype, const MmArgs& a, int form) {
+double estimate(int kind, int dtype, const MmArgs& a, int form, int cus) {
     const Shape& s = kShape[form];
     const Cost& c = costs(kind, dtype)[form];
     const int es = kind == 3 ? 1 : dtype == MOE_F32 ? 4 : 2;
@@ -75,7 +75,7 @@ double estimate(int kind, int dtype, const MmArgs& a, int form) {
     if (kind == 2) tiles = E * std::ceil(K / s.bm);
     else if (a.E == 1) tiles = std::ceil(R / s.bm);
     else tiles = mean > .75 * s.bm ? groups * std::max(1., mean / s.bm + .5) : groups;
-    const double per_cu = tiles * std::ceil(J / s.bn) / device_cu_count();
+    const double per_cu = tiles * std::ceil(J / s.bn) / cus;
     const double steps = std::ceil(std::ceil(C * es / 64) / s.split);
     double t;
     if (per_cu <= s.per_cu) {
@@ -97,11 +97,12 @@ bool mm_fits(int kind, int dtype, const MmArgs& a) {
 }
 
 hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
+    const int cus = device_cu_count();
     int best = -1;
     double t_best = 0;
     for (int f = 0; f < FORMS; ++f) {
         if (costs(kind, dtype)[f].fixed == 0 || !fits(kind, a, f)) continue;
-        const double t = estimate(kind, dtype, a, f);
+        const double t = estimate(kind, dtype, a, f, cus);
         if (best < 0 || t < t_best) best = f, t_best = t;
     }
     switch (best) {

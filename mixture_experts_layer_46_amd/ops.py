@@ -75,15 +75,28 @@ def _dense(t, name, dev=None):
     return d
 
 
+def _given(t, name, dtype, shape, dev):
+    """Raises unless t is a dense tensor of that type and shape on device `dev` (one call: the
+    checks' time is the host's).  -1, the CPU, passes here and is refused with the first tensor."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == dev and
+            t.is_contiguous()):
+        _check(t, name, dtype, shape)
+        if dev >= 0:
+            _dense(t, name, dev)
+
+
 def _launch(dev, name, *args):
     """One operator on the current stream of GPU `dev` (the stream's handle alone: a Stream
     object costs microseconds), which need not be the current device."""
+    fn = _lib.operators.get(name) or _lib.operator(name)
     stream = torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch._C._cuda_getDevice():
-        _lib.call(name, *args, stream)
+        code = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _lib.call(name, *args, stream)
+            code = fn(*args, stream)
+    if code != 0:
+        _lib.failed(name, code)
 
 
 def _current(**ts):
@@ -115,19 +128,17 @@ def _mm(x, w, offsets, out, transposed, xname, oname):
     cin, cout = (N, K) if transposed else (K, N)
     R = x.shape[0]
     code = _code(x, xname)
-    _check(x, xname, x.dtype, (R, cin))
-    _check(w, "w", x.dtype, (E, K, N))
-    _check(offsets, "offsets", torch.int32, (E + 1,))
+    dev = x.get_device()
+    if x.shape[1] != cin:
+        _check(x, xname, x.dtype, (R, cin))
+    _given(w, "w", x.dtype, (E, K, N), dev)
+    _given(offsets, "offsets", torch.int32, (E + 1,), dev)
     rest = out is None
     if not rest:
-        _check(out, oname, x.dtype, (R, cout))
-    dev = _dense(x, xname)
-    _dense(w, "w", dev)
-    _dense(offsets, "offsets", dev)
+        _given(out, oname, x.dtype, (R, cout), dev)
+    _dense(x, xname)
     if rest:
         out = x.new_empty((R, cout))
-    else:
-        _dense(out, oname, dev)
     _launch(dev, "moe_grouped_mm_dx" if transposed else "moe_grouped_mm", _mm_shape(R, E, K, N, code, code, rest),
             x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
@@ -177,23 +188,20 @@ def grouped_mm_dw(x, dy, offsets, out=None, dtype=None):
     R, K = x.shape
     N = dy.shape[1]
     code = _code(x, "x")
-    _check(dy, "dy", x.dtype, (R, N))
+    dev = x.get_device()
+    _given(dy, "dy", x.dtype, (R, N), dev)
     _dims(offsets, 1, "offsets")
     E = offsets.shape[0] - 1
-    _check(offsets, "offsets", torch.int32, (E + 1,))
+    _given(offsets, "offsets", torch.int32, (E + 1,), dev)
     if dtype is None:
         dtype = out.dtype if out is not None else x.dtype
     if dtype != x.dtype and dtype != torch.float32:
         raise ValueError(f"dtype must be {x.dtype} or torch.float32, got {dtype}")
     if out is not None:
-        _check(out, "out", dtype, (E, K, N))
-    dev = _dense(x, "x")
-    _dense(dy, "dy", dev)
-    _dense(offsets, "offsets", dev)
+        _given(out, "out", dtype, (E, K, N), dev)
+    _dense(x, "x")
     if out is None:
         out = torch.empty((E, K, N), dtype=dtype, device=x.device)
-    else:
-        _dense(out, "out", dev)
     _launch(dev, "moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
             offsets.data_ptr(), out.data_ptr())
     return out
@@ -238,26 +246,22 @@ def grouped_mm_int8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out
     _dims(wq, 3, "wq")
     R, K = xq.shape
     E, N, _ = wq.shape
-    _check(xq, "xq", torch.int8, (R, K))
-    _check(x_scale, "x_scale", torch.float32, (R,))
-    _check(wq, "wq", torch.int8, (E, N, K))
-    _check(w_scale, "w_scale", torch.float32, (E, N))
-    _check(offsets, "offsets", torch.int32, (E + 1,))
+    dev = xq.get_device()
+    _given(xq, "xq", torch.int8, (R, K), dev)
+    _given(x_scale, "x_scale", torch.float32, (R,), dev)
+    _given(wq, "wq", torch.int8, (E, N, K), dev)
+    _given(w_scale, "w_scale", torch.float32, (E, N), dev)
+    _given(offsets, "offsets", torch.int32, (E + 1,), dev)
     rest = out is None
     if not rest:
         dtype = out.dtype
-        _check(out, "out", dtype, (R, N))
     if dtype not in _CODES:
         raise TypeError(f"unsupported output type {dtype}")
-    dev = _dense(xq, "xq")
-    _dense(x_scale, "x_scale", dev)
-    _dense(wq, "wq", dev)
-    _dense(w_scale, "w_scale", dev)
-    _dense(offsets, "offsets", dev)
+    if not rest:
+        _given(out, "out", dtype, (R, N), dev)
+    _on(xq, "xq", None)
     if rest:
         out = torch.empty((R, N), dtype=dtype, device=xq.device)
-    else:
-        _dense(out, "out", dev)
     _launch(dev, "moe_grouped_mm_int8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
             x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
@@ -279,12 +283,10 @@ def _spec(p, seed, step, dev):
 def _dropout(x, p, seed, step, out):
     code = _code(x, "x")
     if out is not None:
-        _check(out, "out", x.dtype, x.shape)
+        _given(out, "out", x.dtype, x.shape, x.get_device())
     dev = _dense(x, "x")
     if out is None:
         out = torch.empty_like(x)
-    else:
-        _dense(out, "out", dev)
     _launch(dev, "moe_dropout", code, x.numel(), _spec(p, seed, step, dev), x.data_ptr(), out.data_ptr())
     return out
 
@@ -355,8 +357,7 @@ def _gated_act(a, b, p, seed, step, out):
     if out is None:
         out = a.new_empty((R, F))
     else:
-        _check(out, "out", a.dtype, (R, F))
-        _dense(out, "out", dev)
+        _given(out, "out", a.dtype, (R, F), dev)
     _launch(dev, "moe_gated_act", code, R, F, _spec(p, seed, step, dev), a.data_ptr(), lda, bp, ldb, out.data_ptr())
     return out
 
@@ -392,8 +393,7 @@ def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
     tensors to write, which may be halves of one packed gradient."""
     code, dev, lda, ldb, bp = _act_args(a, b)
     R, F = a.shape
-    _check(dh, "dh", a.dtype, (R, F))
-    _dense(dh, "dh", dev)
+    _given(dh, "dh", a.dtype, (R, F), dev)
     lddb, dbp = 0, None
     if out is None:
         da, ldda = a.new_empty((R, F)), F
@@ -430,13 +430,11 @@ def combine_grad(dout, y_perm, row_of_pair, topk_w):
     code = _code(dout, "dout")
     T, H = dout.shape
     R, k = y_perm.shape[0], topk_w.shape[1]
-    _check(y_perm, "y_perm", dout.dtype, (R, H))
-    _check(topk_w, "topk_w", torch.float32, (T, k))
-    _check(row_of_pair, "row_of_pair", torch.int32, (T * k,))
-    dev = _dense(dout, "dout")
-    _dense(y_perm, "y_perm", dev)
-    _dense(row_of_pair, "row_of_pair", dev)
-    _dense(topk_w, "topk_w", dev)
+    dev = dout.get_device()
+    _given(y_perm, "y_perm", dout.dtype, (R, H), dev)
+    _given(topk_w, "topk_w", torch.float32, (T, k), dev)
+    _given(row_of_pair, "row_of_pair", torch.int32, (T * k,), dev)
+    _dense(dout, "dout")
     dy = torch.empty_like(y_perm)
     dw = torch.empty_like(topk_w)
     _launch(dev, "moe_combine_grad", code, T, k, H, R, dout.data_ptr(), y_perm.data_ptr(), row_of_pair.data_ptr(),
