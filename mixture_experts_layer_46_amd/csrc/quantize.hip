@@ -140,7 +140,7 @@ __global__ __launch_bounds__(256) void k_quantize_experts(const T* __restrict__ 
                                                           int8_t* __restrict__ q, float* __restrict__ scale) {
     __shared__ uint32_t mx[64];
     __shared__ float sc[64];
-    __shared__ int8_t tile[64][80];                    // [channel][k], rows of 80 bytes
+    __shared__ alignas(16) int8_t tile[64][80];        // [channel][k], rows of 80 bytes
     const int e = blockIdx.y, n0 = blockIdx.x * 64, tid = threadIdx.x;
     const T* we = w + (long long)e * K * N;
     const int c8 = (tid & 7) * 8, kr = tid >> 3;       // 8 channels of one of 32 rows
