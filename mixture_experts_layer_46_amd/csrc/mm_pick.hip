@@ -10,9 +10,11 @@
 // The three constants of a form come from some 12000 random calls (1-256 groups, 1-60000 rows,
 // matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every form.
 // Over calls that the fit did not see, the form picked is slower than the best one by 1.4% (x W),
-// 2.6% (dy W^T), 1.8% (x^T dy), 1.4% (int8) and 1.1% (fp32) in the geometric mean; the best
-// single form would be 20%, 20%, 13%, 20% and 32% slower.  fp32 has no tiles of 128: they won
-// 0.05% (weight gradients 0.6%) over the other forms.
+// 2.6% (dy W^T), 2.1% (x^T dy), 1.4% (int8) and 1.1% (fp32) in the geometric mean; the best
+// single form would be 20%, 20%, 16%, 20% and 32% slower.  fp32 has no tiles of 128: they won
+// 0.05% (weight gradients 0.6%) over the other forms.  The thin form of a weight gradient
+// wins where one or two groups have small matrices: over such calls 6% (16 bits) and 18%
+// (fp32) in the mean, at most 2.3 times.
 #include <algorithm>
 #include <cmath>
 
@@ -39,13 +41,13 @@ constexpr Shape kShape[FORMS] = {{256, 256, 1, 1, 512, 5.0e6}, {128, 128, 2, 1, 
 struct Cost {
     double fixed, step, busy;     // us: per workgroup; per step alone; per step and workgroup of a full CU
 };
-// the forms that do not exist (fp32 LARGE and MID128, THIN weight gradients) have no cost
+// the forms that do not exist (fp32 LARGE and MID128, weight gradients in THIN16) have no cost
 constexpr Cost kY16[FORMS] = {{1.85, .38, .54}, {1.9, .38, .25}, {2.15, .24, .146}, {2.15, .23, .59}, {3.55, .89, .042}};
 constexpr Cost kDx16[FORMS] = {{1.85, .38, .59}, {1.8, .385, .24}, {1.85, .096, .14}, {3.75, .25, .34}, {2.55, .69, .039}};
-constexpr Cost kDw16[FORMS] = {{3.4, .52, 1.0}, {2.1, .34, .28}, {2.0, .20, .116}, {}, {}};
+constexpr Cost kDw16[FORMS] = {{3.4, .52, 1.0}, {2.1, .34, .28}, {2.0, .20, .116}, {1.5, .20, .55}, {}};
 constexpr Cost kInt8[FORMS] = {{3.0, .33, .68}, {2.0, .44, .24}, {2.2, .21, .118}, {2.25, .25, .48}, {2.5, .69, .05}};
 constexpr Cost kRows32[FORMS] = {{}, {}, {1.05, .52, .10}, {3.95, .545, .45}, {2.15, .96, .187}};
-constexpr Cost kDw32[FORMS] = {{}, {}, {1.0, .34, .23}, {}, {}};
+constexpr Cost kDw32[FORMS] = {{}, {}, {1.5, .68, .30}, {2.95, .44, .57}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
 const Cost* costs(int kind, int dtype) {

@@ -90,10 +90,11 @@ struct Operand {
         for (int i = 0; i < N; ++i) {
             const int j = first + i;
             if constexpr (COLS) {
-                const int pos = j * 1024 + lane * 16, k = pos / kRowB;
-                int c = (pos % kRowB) / 16;
+                const int pos = j * 1024 + lane * 16;
+                int k = pos / kRowB, c = (pos % kRowB) / 16;
+                if constexpr (ES == 4 && T == 32) k ^= (k >> 3) & 1;
                 if constexpr (ES == 2) c ^= 2 * blk_swz<kRowB>(k);
-                else c ^= 4 * ((k >> 2) & 3);
+                else c ^= 4 * ((k >> 2) & (T == 32 ? 1 : 3));
                 off[i] = c * (16 / ES) < valid ? (uint32_t)k * ld + (uint32_t)c * 16 : kOOB;
             } else {
                 const int r = j * 16 + (lane >> 2), q = (lane & 3) ^ swa4(r);
@@ -130,7 +131,7 @@ struct Operand {
 template <int ES, bool COLS, int T>
 struct Reader {
     static constexpr int kRowB = T * ES;
-    int rd, g;
+    int rd, g, up = 0;
     __device__ __forceinline__ explicit Reader(int lane) {
         const int l16 = lane & 15, lq = lane >> 4;
         g = 0;
@@ -138,9 +139,13 @@ struct Reader {
             g = blk_swz<kRowB>(8 * lq + (l16 >> 2));          // the same for the rows of the second read, 4 further
             rd = (8 * lq + (l16 >> 2)) * kRowB + ((l16 & 3) << 3);
         } else if constexpr (COLS) {
-            static_assert(T % 64 == 0, "blocks trade places in fours");
-            g = lq;
+            // One read takes a 64-byte block of four rows 4 apart, on four places of 256 bytes:
+            // blocks trade places in fours, or where a row has two (T = 32), in twos, and the
+            // rows of the upper half with their neighbours.
+            static_assert(T % 64 == 0 || T == 32, "two blocks a row, or fours of them");
+            g = T == 32 ? lq & 1 : lq;
             rd = 4 * lq * kRowB + l16 * 4;
+            up = T == 32 ? (lq >> 1) * kRowB : 0;
         } else {
             rd = l16 * 64 + ((lq ^ swa4(l16)) << 4);
         }
@@ -155,8 +160,13 @@ struct Reader {
             const v8i16_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             return __builtin_bit_cast(u32x4_t, v);
         } else if constexpr (COLS) {
-            const __attribute__((address_space(3))) uint32_t* p =
-                (const __attribute__((address_space(3))) uint32_t*)(stage + rd + ((blk & ~3) | ((blk & 3) ^ g)) * 64);
+            typedef const __attribute__((address_space(3))) uint32_t lds_u32;
+            const lds_char* at = stage + rd + ((blk & ~3) | ((blk & 3) ^ g)) * 64;
+            if constexpr (T == 32) {
+                lds_u32 *even = (lds_u32*)(at + up), *odd = (lds_u32*)(at - up);
+                return u32x4_t{even[0], odd[kRowB / 4], even[2 * (kRowB / 4)], odd[3 * (kRowB / 4)]};
+            }
+            lds_u32* p = (lds_u32*)at;
             return u32x4_t{p[0], p[kRowB / 4], p[2 * (kRowB / 4)], p[3 * (kRowB / 4)]};
         } else {
             return *(const __attribute__((address_space(3))) u32x4_t*)(stage + rd + blk * 1024);

@@ -329,7 +329,9 @@ def test_grouped_mm_int8(M, counts, K, N, out):
 BIG_CASES = [([1000, 257, 0, 2200, 1, 1542], 2064, 2056), ([0, 700, 1, 5, 2294, 0], 1040, 1032), ([1500, 128, 0, 1, 371], 4112, 1032),
              ([0, 1, 0, 12, 2, 0, 7], 4112, 216), ([400, 40, 1, 18, 0, 0], 144, 7336), ([3] * 8 + [0] * 20 + [9] * 36, 304, 440),
              ([60] * 30 + [0] * 4 + [200] * 30, 304, 440), ([45, 0, 33, 64] * 16, 80, 984), ([71], 528, 16184), ([75] * 4, 1872, 2144),
-             ([190, 0, 33, 1, 257, 64, 100, 31, 0, 5, 300, 16, 17, 128, 129, 90, 0, 250, 200, 179], 1040, 1032)]
+             ([190, 0, 33, 1, 257, 64, 100, 31, 0, 5, 300, 16, 17, 128, 129, 90, 0, 250, 200, 179], 1040, 1032),
+             # (a long contraction for few output tiles)
+             ([1654], 328, 440), ([900, 0, 1, 700], 264, 136), ([5003], 40, 8)]
 BIG_IDS = [f"{sum(c)}rows-{len(c)}groups-{k}x{n}" for c, k, n in BIG_CASES]
 
 
