@@ -226,10 +226,12 @@ def grouped_ffn(x_perm, offsets, w_in, w_up, w_out, top_k, T, workspace=None, y_
 
 
 def combine(y_perm, row_of_pair, topk_w, out=None):
-    """out[t] = sum_j topk_w[t, j] * y_perm[row_of_pair[t*k + j]]."""
-    _need_cuda(y_perm, row_of_pair, topk_w, out)
+    """out[t] = sum_j topk_w[t, j] * y_perm[row_of_pair[t*k + j]]; `out` [T, H] in y_perm's type."""
     T, k = topk_w.shape
     H = y_perm.shape[1]
+    if out is not None:
+        _need(out, "out", y_perm.dtype, (T, H))
+    _need_cuda(y_perm, row_of_pair, topk_w, out)
     shape = Shape(T=T, H=H, E=max(k, 1), k=k, F=8, dtype=_dtype_code(y_perm))
     if out is None:
         out = torch.empty((T, H), dtype=y_perm.dtype, device=y_perm.device)
