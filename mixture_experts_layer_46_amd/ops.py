@@ -453,14 +453,34 @@ class QuantizedExperts(NamedTuple):
 def quantize_ffn(w_in, w_up, w_out) -> QuantizedExperts:
     """The experts of forward (w_in, w_up [E, H, F], w_up None for the two-layer SiLU FFN;
     w_out [E, F, H]) as 8-bit matrices, made once.  H and F multiples of 16."""
+    _dims(w_in, 3, "w_in")
+    E, H, F = w_in.shape
+    if w_up is not None:
+        _check(w_up, "w_up", w_in.dtype, (E, H, F))
+    _check(w_out, "w_out", w_in.dtype, (E, F, H))
     return QuantizedExperts(quantize_experts(w_in), None if w_up is None else quantize_experts(w_up),
                             quantize_experts(w_out))
+
+
+def _check_experts(experts, E, H):
+    """Raises unless the 8-bit matrices are those of E experts between rows of H and hidden rows
+    of one width: nothing after this looks at w_out's rows against the layer's."""
+    _dims(experts.w_in[0], 3, "w_in")
+    F = experts.w_in[0].shape[1]
+    for name, pair, shape in (("w_in", experts.w_in, (E, F, H)), ("w_up", experts.w_up, (E, F, H)),
+                              ("w_out", experts.w_out, (E, H, F))):
+        if pair is not None or name != "w_up":
+            _check(pair[0], f"{name}, 8-bit,", torch.int8, shape)
+            _check(pair[1], f"{name}'s scale", torch.float32, shape[:2])
 
 
 def grouped_ffn_int8(x_perm, offsets, experts: QuantizedExperts):
     """The grouped expert FFN on 8-bit experts: the rows x_perm [R, H] and the activated hidden
     rows are quantised per token, both projections run in 8-bit integers.  Returns [R, H] in
     x_perm's type; rows that lie in no group are zeros."""
+    _dims(x_perm, 2, "x_perm")
+    _dims(offsets, 1, "offsets")
+    _check_experts(experts, offsets.shape[0] - 1, x_perm.shape[1])
     q, s = quantize_rows(x_perm)
     a = grouped_mm_int8(q, s, *experts.w_in, offsets, dtype=x_perm.dtype)
     b = None if experts.w_up is None else grouped_mm_int8(q, s, *experts.w_up, offsets, dtype=x_perm.dtype)
@@ -472,6 +492,7 @@ def forward_int8(x, w_gate, experts: QuantizedExperts, top_k, bias=None, flags=0
     """The whole layer (forward) with 8-bit experts (quantize_ffn); the routing stays fp32."""
     import mixture_experts_layer_46_amd as M
     T, H, E, _ = M._check_layer(x, w_gate, bias, out=out, top_k=top_k, experts=False)
+    _check_experts(experts, E, H)
     if out is None:
         out = torch.empty_like(x)
     if T == 0:
