@@ -424,6 +424,11 @@ def combine_grad(dout, y_perm, row_of_pair, topk_w):
     (bf16 or fp32), row_of_pair [T*k] int32 and topk_w [T, k] fp32.  A dropped pair (row -1)
     has dtopk_w 0; rows of dy_perm that no pair names are unset.  No two pairs may name one
     row (permute's never do)."""
+    return _combine_grad(dout, y_perm, row_of_pair, topk_w, torch.empty_like)
+
+
+def _combine_grad(dout, y_perm, row_of_pair, topk_w, like):
+    """combine_grad with dy_perm made by `like` (y_perm)."""
     _dims(dout, 2, "dout")
     _dims(y_perm, 2, "y_perm")
     _dims(topk_w, 2, "topk_w")
@@ -435,7 +440,7 @@ def combine_grad(dout, y_perm, row_of_pair, topk_w):
     _given(topk_w, "topk_w", torch.float32, (T, k), dev)
     _given(row_of_pair, "row_of_pair", torch.int32, (T * k,), dev)
     _dense(dout, "dout")
-    dy = torch.empty_like(y_perm)
+    dy = like(y_perm)
     dw = torch.empty_like(topk_w)
     _launch(dev, "moe_combine_grad", code, T, k, H, R, dout.data_ptr(), y_perm.data_ptr(), row_of_pair.data_ptr(),
             topk_w.data_ptr(), dy.data_ptr(), dw.data_ptr())
@@ -578,17 +583,22 @@ class _Permute(torch.autograd.Function):
 
 
 class _Combine(torch.autograd.Function):
+    """The combine; `whole`: every row has a pair.  Where a capacity left rows without one, their
+    gradient is zeros, written before the others' (combine_grad leaves such rows unset, and
+    nothing unset may pass through autograd)."""
+
     @staticmethod
-    def forward(ctx, y_perm, row_of_pair, topk_w):
+    def forward(ctx, y_perm, row_of_pair, topk_w, whole):
         import mixture_experts_layer_46_amd as M
         ctx.save_for_backward(y_perm, row_of_pair, topk_w)
+        ctx.like = torch.empty_like if whole else torch.zeros_like
         return M.combine(y_perm, row_of_pair, topk_w)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        dy, dw = combine_grad(dout.contiguous(), *ctx.saved_tensors)
-        return dy, None, dw
+        dy, dw = _combine_grad(dout.contiguous(), *ctx.saved_tensors, ctx.like)
+        return dy, None, dw, None
 
 
 def forward_train(x, w_gate, w_in, w_up, w_out, top_k, bias=None, dropout_p=0.0, seed=0, step=0, flags=0,
@@ -608,8 +618,9 @@ def forward_train(x, w_gate, w_in, w_up, w_out, top_k, bias=None, dropout_p=0.0,
         raise ValueError("forward_train needs at least one token")
     with _current(x=x, w_gate=w_gate, bias=bias, w_in=w_in, w_up=w_up, w_out=w_out):
         g, idx, _ = _Route.apply(x, w_gate, bias, top_k, flags)
-        x_perm, offsets, row_of_pair = _Permute.apply(x, idx, E, _lib.capacity_rows(capacity_factor, T, top_k, E))
+        capacity = _lib.capacity_rows(capacity_factor, T, top_k, E)
+        x_perm, offsets, row_of_pair = _Permute.apply(x, idx, E, capacity)
         a = grouped_mm(x_perm, w_in, offsets)
         b = None if w_up is None else grouped_mm(x_perm, w_up, offsets)
         h = gated_act(a, b, dropout_p, seed, step)
-        return _Combine.apply(grouped_mm(h, w_out, offsets), row_of_pair, g)
+        return _Combine.apply(grouped_mm(h, w_out, offsets), row_of_pair, g, capacity == 0)

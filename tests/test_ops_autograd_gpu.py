@@ -1,0 +1,50 @@
+"""The differentiable operators inside larger autograd programs: what the engine hands to their
+backward passes, and what they leave behind for it."""
+import pytest
+import torch
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+bf, f32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def M():
+    import mixture_experts_layer_46_amd as M
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    M._lib.load()
+    return M
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def _layer(dtype, T=64, H=64, E=4, F=64):
+    return dict(x=rand((T, H), dtype, 1), w_gate=rand((H, E), f32, 2, H ** -0.5), w_in=rand((E, H, F), dtype, 3, H ** -0.5),
+                w_up=rand((E, H, F), dtype, 4, H ** -0.5), w_out=rand((E, F, H), dtype, 5, F ** -0.5),
+                bias=rand((E,), f32, 6))
+
+
+def _train(M, d, dout, **kw):
+    g = {n: t.clone().requires_grad_() for n, t in d.items()}
+    out = M.forward_train(g["x"], g["w_gate"], g["w_in"], g["w_up"], g["w_out"], 2, bias=g["bias"], dropout_p=0.1, seed=3,
+                          **kw)
+    return [out.detach(), *torch.autograd.grad(out, list(g.values()), dout)]
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "fp32"])
+def test_dropped_pairs_leave_no_unset_gradients(M, dtype, monkeypatch):
+    """Rows that a capacity left without a pair get a gradient of zeros: torch's anomaly
+    detection, which looks at whole gradients, finds no stray NaN of unwritten memory there."""
+    say(f"anomaly detection, dropped pairs {dtype}")
+    d, dout = _layer(dtype), rand((64, 64), dtype, 7)
+    want = _train(M, d, dout, capacity_factor=0.6)
+    empty_like = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like",
+                        lambda t, **kw: empty_like(t, **kw).fill_(float("nan")) if t.is_floating_point() else empty_like(t, **kw))
+    with torch.autograd.detect_anomaly(check_nan=True):
+        got = _train(M, d, dout, capacity_factor=0.6)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
