@@ -85,6 +85,13 @@ def _given(t, name, dtype, shape, dev):
             _dense(t, name, dev)
 
 
+def _grad(g):
+    """A gradient as autograd hands it over, dense and at an address the kernels take: it may be
+    any view, such as a stack's slice that starts off 16 bytes."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 def _launch(dev, name, *args):
     """One operator on the current stream of GPU `dev` (the stream's handle alone: a Stream
     object costs microseconds), which need not be the current device."""
@@ -154,7 +161,7 @@ class _GroupedMM(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
-        dy = dy.contiguous()
+        dy = _grad(dy)
         dx = grouped_mm_dx(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = grouped_mm_dw(x, dy, offsets) if ctx.needs_input_grad[1] else None
         return dx, dw, None
@@ -300,7 +307,7 @@ class _Dropout(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        return _dropout(dy.contiguous(), ctx.p, ctx.seed, ctx.step, None), None, None, None
+        return _dropout(_grad(dy), ctx.p, ctx.seed, ctx.step, None), None, None, None
 
 
 def _kept_step(step):
@@ -373,7 +380,7 @@ class _GatedAct(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh):
         a, b = ctx.saved_tensors
-        da, db = gated_act_grad(dh.contiguous(), a, b, ctx.p, ctx.seed, ctx.step)
+        da, db = gated_act_grad(_grad(dh), a, b, ctx.p, ctx.seed, ctx.step)
         return da, db, None, None, None
 
 
@@ -579,7 +586,7 @@ class _Permute(torch.autograd.Function):
         (row_of_pair,) = ctx.saved_tensors
         T = row_of_pair.numel() // ctx.k
         ones = torch.ones((T, ctx.k), dtype=torch.float32, device=dx_perm.device)
-        return M.combine(dx_perm.contiguous(), row_of_pair, ones), None, None, None
+        return M.combine(_grad(dx_perm), row_of_pair, ones), None, None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -597,7 +604,7 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        dy, dw = _combine_grad(dout.contiguous(), *ctx.saved_tensors, ctx.like)
+        dy, dw = _combine_grad(_grad(dout), *ctx.saved_tensors, ctx.like)
         return dy, None, dw, None
 
 

@@ -48,3 +48,38 @@ def test_dropped_pairs_leave_no_unset_gradients(M, dtype, monkeypatch):
     with torch.autograd.detect_anomaly(check_nan=True):
         got = _train(M, d, dout, capacity_factor=0.6)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def _shifted(y, dy):
+    """y's gradient dy as the engine hands it over behind a concatenation: a dense view that
+    starts one element into its storage."""
+    flat = torch.cat([torch.zeros(1, dtype=y.dtype, device=y.device), y.reshape(-1)])
+    return flat, torch.cat([torch.zeros(1, dtype=dy.dtype, device=dy.device), dy.reshape(-1)])
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "fp32"])
+def test_gradients_at_any_address(M, dtype):
+    """Gradients that are views off the kernels' 16 bytes (slices of a concatenation's or a
+    stack's gradient) give the same results as aligned ones."""
+    say(f"misaligned gradients {dtype}")
+    R, K, N = 40, 64, 72
+    off = torch.tensor([0, 25, 25, 40], dtype=torch.int32).cuda()
+    x, w, dy = rand((R, K), dtype, 1), rand((3, K, N), dtype, 2, K ** -0.5), rand((R, N), dtype, 3)
+    a, b = rand((R, N), dtype, 4), rand((R, N), dtype, 5)
+    d = _layer(dtype)
+    layer = lambda *t: M.forward_train(*t[:5], 2, bias=t[5], dropout_p=0.1, seed=3)
+    for name, fn, inputs, g in (
+            ("grouped_mm", lambda x, w: M.grouped_mm(x, w, off), (x, w), dy),
+            ("gated_act", lambda a, b: M.gated_act(a, b, 0.1, 5, 6), (a, b), dy),
+            ("dropout", lambda a: M.dropout(a, 0.1, 5, 6), (a,), dy),
+            ("forward_train", layer, tuple(d.values()), rand((64, 64), dtype, 7))):
+        t = [v.clone().requires_grad_() for v in inputs]
+        want = torch.autograd.grad(fn(*t), t, g)
+        flat, gflat = _shifted(fn(*t), g)
+        got = torch.autograd.grad(flat, t, gflat)
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), name
+    # a stack of odd tensors: the second one's gradient starts 35 elements in
+    u, v = rand((5, 7), dtype, 8).requires_grad_(), rand((5, 7), dtype, 9).requires_grad_()
+    g = rand((2, 5, 7), dtype, 10)
+    du, dv = torch.autograd.grad(torch.stack([M.dropout(u, 0.3, 1, 1), M.dropout(v, 0.3, 1, 2)]), (u, v), g)
+    assert torch.equal(du, M.dropout(g[0].clone(), 0.3, 1, 1)) and torch.equal(dv, M.dropout(g[1].clone(), 0.3, 1, 2))
