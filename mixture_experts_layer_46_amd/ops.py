@@ -85,6 +85,14 @@ def _given(t, name, dtype, shape, dev):
             _dense(t, name, dev)
 
 
+def _wrote(*outs):
+    """Counts tensors of the caller's as modified, so that autograd refuses a backward pass over
+    their old contents (tensors of inference mode have no count)."""
+    for t in outs:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _grad(g):
     """A gradient as autograd hands it over, dense and at an address the kernels take: it may be
     any view, such as a stack's slice that starts off 16 bytes."""
@@ -148,6 +156,7 @@ def _mm(x, w, offsets, out, transposed, xname, oname):
         out = x.new_empty((R, cout))
     _launch(dev, "moe_grouped_mm_dx" if transposed else "moe_grouped_mm", _mm_shape(R, E, K, N, code, code, rest),
             x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    _wrote(None if rest else out)
     return out
 
 
@@ -207,11 +216,11 @@ def grouped_mm_dw(x, dy, offsets, out=None, dtype=None):
     if out is not None:
         _given(out, "out", dtype, (E, K, N), dev)
     _dense(x, "x")
-    if out is None:
-        out = torch.empty((E, K, N), dtype=dtype, device=x.device)
+    dw = torch.empty((E, K, N), dtype=dtype, device=x.device) if out is None else out
     _launch(dev, "moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
-            offsets.data_ptr(), out.data_ptr())
-    return out
+            offsets.data_ptr(), dw.data_ptr())
+    _wrote(out)
+    return dw
 
 
 # -------------------------------------------------------------------- 8-bit integers
@@ -271,6 +280,7 @@ def grouped_mm_int8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out
         out = torch.empty((R, N), dtype=dtype, device=xq.device)
     _launch(dev, "moe_grouped_mm_int8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
             x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    _wrote(None if rest else out)
     return out
 
 
@@ -292,10 +302,10 @@ def _dropout(x, p, seed, step, out):
     if out is not None:
         _given(out, "out", x.dtype, x.shape, x.get_device())
     dev = _dense(x, "x")
-    if out is None:
-        out = torch.empty_like(x)
-    _launch(dev, "moe_dropout", code, x.numel(), _spec(p, seed, step, dev), x.data_ptr(), out.data_ptr())
-    return out
+    y = torch.empty_like(x) if out is None else out
+    _launch(dev, "moe_dropout", code, x.numel(), _spec(p, seed, step, dev), x.data_ptr(), y.data_ptr())
+    _wrote(out)
+    return y
 
 
 class _Dropout(torch.autograd.Function):
@@ -361,12 +371,12 @@ def _act_args(a, b):
 def _gated_act(a, b, p, seed, step, out):
     code, dev, lda, ldb, bp = _act_args(a, b)
     R, F = a.shape
-    if out is None:
-        out = a.new_empty((R, F))
-    else:
+    if out is not None:
         _given(out, "out", a.dtype, (R, F), dev)
-    _launch(dev, "moe_gated_act", code, R, F, _spec(p, seed, step, dev), a.data_ptr(), lda, bp, ldb, out.data_ptr())
-    return out
+    h = a.new_empty((R, F)) if out is None else out
+    _launch(dev, "moe_gated_act", code, R, F, _spec(p, seed, step, dev), a.data_ptr(), lda, bp, ldb, h.data_ptr())
+    _wrote(out)
+    return h
 
 
 class _GatedAct(torch.autograd.Function):
@@ -422,6 +432,8 @@ def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
         dbp = db.data_ptr()
     _launch(dev, "moe_gated_act_grad", code, R, F, _spec(p, seed, step, dev), dh.data_ptr(), a.data_ptr(), lda, bp, ldb,
             da.data_ptr(), ldda, dbp, lddb)
+    if out is not None:
+        _wrote(da, db)
     return da, db
 
 
@@ -505,6 +517,7 @@ def forward_int8(x, w_gate, experts: QuantizedExperts, top_k, bias=None, flags=0
     import mixture_experts_layer_46_amd as M
     T, H, E, _ = M._check_layer(x, w_gate, bias, out=out, top_k=top_k, experts=False)
     _check_experts(experts, E, H)
+    given = out
     if out is None:
         out = torch.empty_like(x)
     if T == 0:
@@ -513,7 +526,9 @@ def forward_int8(x, w_gate, experts: QuantizedExperts, top_k, bias=None, flags=0
         _, idx, w = M.route(x, w_gate, top_k, bias=bias, flags=flags)
         g = M.permute(idx, E, x=x, capacity=_lib.capacity_rows(capacity_factor, T, top_k, E))
         y = grouped_ffn_int8(g["x_perm"], g["offsets"], experts)
-        return M.combine(y, g["row_of_pair"], w, out=out)
+        M.combine(y, g["row_of_pair"], w, out=out)
+    _wrote(given)
+    return out
 
 
 # ----------------------------------------------------------------- the layer, trained

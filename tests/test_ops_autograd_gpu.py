@@ -83,3 +83,36 @@ def test_gradients_at_any_address(M, dtype):
     g = rand((2, 5, 7), dtype, 10)
     du, dv = torch.autograd.grad(torch.stack([M.dropout(u, 0.3, 1, 1), M.dropout(v, 0.3, 1, 2)]), (u, v), g)
     assert torch.equal(du, M.dropout(g[0].clone(), 0.3, 1, 1)) and torch.equal(dv, M.dropout(g[1].clone(), 0.3, 1, 2))
+
+
+def test_given_outputs_count_as_written(M):
+    """A tensor written through `out` counts as modified: a backward pass that had kept its old
+    contents raises, as behind any other in-place operation, instead of using the new ones."""
+    say("out and autograd's version counters")
+    a, b = rand((8, 16), bf, 1).requires_grad_(), rand((8, 16), bf, 2)
+    h = M.gated_act(a, b)
+    with torch.no_grad():
+        M.dropout(b, 0.5, 1, 2, out=b)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        h.sum().backward()
+    off = torch.tensor([0, 8], dtype=torch.int32).cuda()
+    x, w, dy = rand((8, 16), bf, 3), rand((1, 16, 24), bf, 4), rand((8, 24), bf, 5)
+    q, s = M.quantize_rows(x)
+    wq, ws = M.quantize_experts(w)
+    gate, experts = rand((16, 2), f32, 6), M.quantize_ffn(rand((2, 16, 32), bf, 7), None, rand((2, 32, 16), bf, 8))
+    e = lambda *shape: torch.empty(*shape, dtype=bf, device="cuda")
+    for call, out in ((lambda o: M.grouped_mm(x, w, off, out=o), e(8, 24)), (lambda o: M.grouped_mm_dx(dy, w, off, out=o), e(8, 16)),
+                      (lambda o: M.grouped_mm_dw(x, dy, off, out=o), e(1, 16, 24)),
+                      (lambda o: M.grouped_mm_int8(q, s, wq, ws, off, out=o), e(8, 24)),
+                      (lambda o: M.dropout(x, 0.1, 1, out=o), e(8, 16)), (lambda o: M.gated_act(x, x, out=o), e(8, 16)),
+                      (lambda o: M.gated_act_grad(x, x, b, out=(o, e(8, 16))), e(8, 16)),
+                      (lambda o: M.gated_act_grad(x, x, b, out=(e(8, 16), o)), e(8, 16)),
+                      (lambda o: M.forward_int8(x, gate, experts, 1, out=o), e(8, 16))):
+        before = out._version
+        call(out)
+        assert out._version > before
+    # tensors of inference mode have no counter; they are written all the same
+    with torch.inference_mode():
+        o = e(8, 16)
+        M.dropout(x, 0.0, 1, out=o)
+        assert torch.equal(o, x)
