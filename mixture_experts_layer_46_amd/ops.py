@@ -19,7 +19,8 @@ and the layers made of them:
     forward_int8(x, w_gate, experts, top_k, ...)              experts = quantize_ffn(w_in, w_up, w_out)
 
 Work is enqueued on the current stream of the tensors' device, which need not be the
-current device.  Tensors that another stream wrote or will use are the caller's to order,
+current device.  An `out` may not overlap an input (dropout's may be its input) and counts as
+modified for autograd.  Tensors that another stream wrote or will use are the caller's to order,
 as everywhere in torch.
 """
 from __future__ import annotations
@@ -83,6 +84,30 @@ def _given(t, name, dtype, shape, dev):
         _check(t, name, dtype, shape)
         if dev >= 0:
             _dense(t, name, dev)
+
+
+def _overlap(a, b):
+    """Whether two tensors share memory.  Halves of one packed tensor, whose rows take turns, do
+    not."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    def end(t):
+        return t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    if end(a) <= b0 or end(b) <= a0:
+        return False
+    if a.shape == b.shape and a.dtype == b.dtype and a.stride() == b.stride() and a.dim() == 2 and a.shape[0] > 1:
+        row, width = a.stride(0) * a.element_size(), a.shape[1] * a.element_size()
+        d = (b0 - a0) % row
+        return d < width or row - d < width
+    return True
+
+
+def _apart(out, oname, **inputs):
+    """Raises where a given output shares memory with an input: a kernel reads while it writes."""
+    for name, t in inputs.items():
+        if t is not None and _overlap(out, t):
+            raise ValueError(f"{oname} overlaps {name}")
 
 
 def _wrote(*outs):
@@ -151,6 +176,7 @@ def _mm(x, w, offsets, out, transposed, xname, oname):
     rest = out is None
     if not rest:
         _given(out, oname, x.dtype, (R, cout), dev)
+        _apart(out, oname, **{xname: x}, w=w, offsets=offsets)
     _dense(x, xname)
     if rest:
         out = x.new_empty((R, cout))
@@ -215,6 +241,7 @@ def grouped_mm_dw(x, dy, offsets, out=None, dtype=None):
         raise ValueError(f"dtype must be {x.dtype} or torch.float32, got {dtype}")
     if out is not None:
         _given(out, "out", dtype, (E, K, N), dev)
+        _apart(out, "out", x=x, dy=dy, offsets=offsets)
     _dense(x, "x")
     dw = torch.empty((E, K, N), dtype=dtype, device=x.device) if out is None else out
     _launch(dev, "moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
@@ -275,6 +302,7 @@ def grouped_mm_int8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out
         raise TypeError(f"unsupported output type {dtype}")
     if not rest:
         _given(out, "out", dtype, (R, N), dev)
+        _apart(out, "out", xq=xq, x_scale=x_scale, wq=wq, w_scale=w_scale, offsets=offsets)
     _on(xq, "xq", None)
     if rest:
         out = torch.empty((R, N), dtype=dtype, device=xq.device)
@@ -301,6 +329,8 @@ def _dropout(x, p, seed, step, out):
     code = _code(x, "x")
     if out is not None:
         _given(out, "out", x.dtype, x.shape, x.get_device())
+        if out.data_ptr() != x.data_ptr():
+            _apart(out, "out", x=x)
     dev = _dense(x, "x")
     y = torch.empty_like(x) if out is None else out
     _launch(dev, "moe_dropout", code, x.numel(), _spec(p, seed, step, dev), x.data_ptr(), y.data_ptr())
@@ -373,6 +403,7 @@ def _gated_act(a, b, p, seed, step, out):
     R, F = a.shape
     if out is not None:
         _given(out, "out", a.dtype, (R, F), dev)
+        _apart(out, "out", a=a, b=b)
     h = a.new_empty((R, F)) if out is None else out
     _launch(dev, "moe_gated_act", code, R, F, _spec(p, seed, step, dev), a.data_ptr(), lda, bp, ldb, h.data_ptr())
     _wrote(out)
@@ -428,6 +459,8 @@ def gated_act_grad(dh, a, b=None, p=0.0, seed=0, step=0, out=None):
             _check(db, "db", a.dtype, (R, F))
             _on(db, "db", dev)
             lddb = _row_stride(db, "db")
+            _apart(db, "db", da=da, dh=dh, a=a, b=b)
+        _apart(da, "da", dh=dh, a=a, b=b)
     if db is not None:
         dbp = db.data_ptr()
     _launch(dev, "moe_gated_act_grad", code, R, F, _spec(p, seed, step, dev), dh.data_ptr(), a.data_ptr(), lda, bp, ldb,

@@ -116,3 +116,21 @@ def test_given_outputs_count_as_written(M):
         o = e(8, 16)
         M.dropout(x, 0.0, 1, out=o)
         assert torch.equal(o, x)
+
+
+def test_activation_outputs_over_inputs_are_refused(M):
+    """Refused on the host, before a launch; halves of one packed tensor are no overlap."""
+    say("gated_act, overlapping outputs")
+    buf = rand((8, 96), bf, 1)
+    a, b, dh = buf[:, :24], buf[:, 24:48], rand((8, 24), bf, 2)
+    flat = buf.view(-1)[:8 * 24].view(8, 24)
+    for call, msg in ((lambda: M.gated_act(a, b, out=flat), "out overlaps a"), (lambda: M.gated_act(dh, b, out=dh), "out overlaps a"),
+                      (lambda: M.gated_act_grad(dh, a, b, out=(buf[:, 48:72], buf[:, 56:80])), "db overlaps da"),
+                      (lambda: M.gated_act_grad(dh, a, b, out=(dh, buf[:, 56:80])), "da overlaps dh"),
+                      (lambda: M.gated_act_grad(dh, a, b, out=(buf[:, 8:32], buf[:, 56:80])), "da overlaps a"),
+                      (lambda: M.gated_act_grad(dh, a, b, out=(buf[:, 56:80], buf[:, 32:56])), "db overlaps b")):
+        with pytest.raises(ValueError, match=msg):
+            call()
+    want = M.gated_act_grad(dh, a, b)
+    M.gated_act_grad(dh, a, b, out=(buf[:, 48:72], buf[:, 72:]))
+    assert torch.equal(buf[:, 48:72], want[0]) and torch.equal(buf[:, 72:], want[1])

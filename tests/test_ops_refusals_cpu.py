@@ -73,3 +73,42 @@ def test_8bit_layer_takes_experts_that_fit():
 def test_quantize_ffn_refuses_matrices_that_do_not_fit(w_in, w_up, w_out, msg):
     with pytest.raises(ValueError, match=msg):
         M.quantize_ffn(w_in, w_up, w_out)
+
+
+OFF = z(3, dtype=i32)
+BUF = z(4096)                                                        # one storage for what overlaps
+
+
+def _part(start, *shape):
+    n = 1
+    for d in shape:
+        n *= d
+    return BUF[start:start + n].view(*shape)
+
+
+@pytest.mark.parametrize("call,msg", [
+    (lambda: M.grouped_mm(_part(0, 6, 16), z(2, 16, 16), OFF, out=_part(0, 6, 16)), "out overlaps x"),
+    (lambda: M.grouped_mm(_part(0, 6, 16), z(2, 16, 16), OFF, out=_part(88, 6, 16)), "out overlaps x"),
+    (lambda: M.grouped_mm(z(6, 16), _part(64, 2, 16, 24), OFF, out=_part(0, 6, 24)), "out overlaps w"),
+    (lambda: M.grouped_mm_dx(_part(0, 6, 24), z(2, 16, 24), OFF, out=_part(136, 6, 16)), "out overlaps dy"),
+    (lambda: M.grouped_mm_dw(z(6, 16), _part(760, 6, 24), OFF, out=_part(0, 2, 16, 24)), "out overlaps dy"),
+    (lambda: M.grouped_mm_int8(z(6, 16, dtype=i8), z(6, dtype=f32), BUF.view(i8)[:768].view(2, 24, 16), z(2, 24, dtype=f32),
+                               OFF, out=_part(376, 6, 24)), "out overlaps wq"),
+    (lambda: M.dropout(_part(0, 5, 7), 0.1, 1, out=_part(8, 5, 7)), "out overlaps x"),
+    # not these: side by side, in place, rows that take turns
+    (lambda: M.grouped_mm(_part(0, 6, 16), z(2, 16, 16), OFF, out=_part(96, 6, 16)), "on the GPU"),
+    (lambda: M.dropout(_part(0, 5, 7), 0.1, 1, out=_part(0, 5, 7)), "on the GPU"),
+])
+def test_outputs_over_inputs_are_refused(call, msg):
+    with pytest.raises(ValueError, match=msg):
+        call()
+
+
+def test_overlap_of_packed_halves():
+    from mixture_experts_layer_46_amd.ops import _overlap
+    p = BUF[:960].view(10, 96)
+    assert not _overlap(p[:, :48], p[:, 48:]) and not _overlap(p[:, 48:], p[:, :48]) and not _overlap(p[:, 16:32], p[:, 64:80])
+    assert _overlap(p[:, :48], p[:, 40:88]) and _overlap(p[:, 40:88], p[:, :48]) and _overlap(p[:, :48], p[:, :48])
+    assert _overlap(p[:5, :48], p[4:9, :48]) and not _overlap(p[:5, :48], p[5:, :48]) and not _overlap(p[:5, :48], p[4:9, 48:])
+    assert not _overlap(p[:1, :48], p[:1, 48:]) and _overlap(p[:1, :48], p[:1, 40:88])
+    assert not _overlap(p[:0], p) and _overlap(p[:, :48], BUF[:480].view(10, 48)) and not _overlap(p, BUF[960:])
