@@ -104,7 +104,10 @@ def _overlap(a, b):
 
 
 def _apart(out, oname, **inputs):
-    """Raises where a given output shares memory with an input: a kernel reads while it writes."""
+    """Raises where a given output shares memory with an input (a kernel reads while it writes), or
+    is part of a recorded graph (which would not learn of the write)."""
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{oname} requires a gradient")
     for name, t in inputs.items():
         if t is not None and _overlap(out, t):
             raise ValueError(f"{oname} overlaps {name}")
@@ -329,8 +332,7 @@ def _dropout(x, p, seed, step, out):
     code = _code(x, "x")
     if out is not None:
         _given(out, "out", x.dtype, x.shape, x.get_device())
-        if out.data_ptr() != x.data_ptr():
-            _apart(out, "out", x=x)
+        _apart(out, "out", x=None if out.data_ptr() == x.data_ptr() else x)
     dev = _dense(x, "x")
     y = torch.empty_like(x) if out is None else out
     _launch(dev, "moe_dropout", code, x.numel(), _spec(p, seed, step, dev), x.data_ptr(), y.data_ptr())

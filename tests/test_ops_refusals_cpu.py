@@ -112,3 +112,17 @@ def test_overlap_of_packed_halves():
     assert _overlap(p[:5, :48], p[4:9, :48]) and not _overlap(p[:5, :48], p[5:, :48]) and not _overlap(p[:5, :48], p[4:9, 48:])
     assert not _overlap(p[:1, :48], p[:1, 48:]) and _overlap(p[:1, :48], p[:1, 40:88])
     assert not _overlap(p[:0], p) and _overlap(p[:, :48], BUF[:480].view(10, 48)) and not _overlap(p, BUF[960:])
+
+
+@pytest.mark.parametrize("call", [
+    lambda o: M.grouped_mm(z(6, 16), z(2, 16, 24), OFF, out=o(6, 24)), lambda o: M.grouped_mm_dx(z(6, 24), z(2, 16, 24), OFF, out=o(6, 16)),
+    lambda o: M.grouped_mm_dw(z(6, 16), z(6, 24), OFF, out=o(2, 16, 24)), lambda o: M.dropout(z(6, 16), 0.1, 1, out=o(6, 16)),
+    lambda o: M.grouped_mm_int8(z(6, 16, dtype=i8), z(6, dtype=f32), z(2, 24, 16, dtype=i8), z(2, 24, dtype=f32), OFF, out=o(6, 24))])
+def test_outputs_inside_a_graph_are_refused(call):
+    """An out that requires a gradient would hide the write from autograd; without recording it
+    is an ordinary tensor."""
+    part = lambda *s: z(*s).requires_grad_()
+    with pytest.raises(ValueError, match="out requires a gradient"):
+        call(part)
+    with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):
+        call(part)
