@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -325,6 +326,7 @@ def _spec(p, seed, step, dev):
         if step.dtype != torch.int64 or step.numel() != 1 or step.get_device() != dev:
             raise ValueError(f"a tensor step must hold one int64 on cuda:{dev}")
         ptr, step = step.data_ptr(), 0
+    seed, step = operator.index(seed), operator.index(step)       # any integer type, numpy's among them
     return ctypes.byref(DropoutSpec(p, seed & 0xFFFFFFFFFFFFFFFF, step & 0xFFFFFFFFFFFFFFFF, ptr))
 
 

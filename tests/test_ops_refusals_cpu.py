@@ -1,5 +1,6 @@
 """Calls that the wrappers refuse on the host, before anything is enqueued (CPU tensors: a call
 that passes every check ends at "on the GPU")."""
+import numpy as np
 import pytest
 import torch
 
@@ -126,3 +127,20 @@ def test_outputs_inside_a_graph_are_refused(call):
         call(part)
     with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):
         call(part)
+
+
+@pytest.mark.parametrize("seed,step,words", [
+    (np.int64(5), np.int32(7), (5, 7)), (np.uint64((1 << 63) + 1), np.int64(-1), ((1 << 63) + 1, (1 << 64) - 1)),
+    (-2, 1 << 64, ((1 << 64) - 2, 0)), (True, np.uint8(255), (1, 255))])
+def test_seed_and_step_of_any_integer_type(seed, step, words):
+    """A seed drawn by numpy is one of its integers, which do not take Python's 64-bit masks."""
+    from mixture_experts_layer_46_amd.ops import _spec
+    d = _spec(0.25, seed, step, 0)._obj
+    assert (d.p, d.seed, d.step, d.step_device) == (0.25, *words, None)
+
+
+@pytest.mark.parametrize("seed,step", [(0.5, 1), (1, 2.0), ("1", 2), (None, 1)])
+def test_seed_and_step_are_integers(seed, step):
+    from mixture_experts_layer_46_amd.ops import _spec
+    with pytest.raises(TypeError):
+        _spec(0.25, seed, step, 0)
