@@ -65,6 +65,14 @@ moe_status moe_grouped_mm_dx(const moe_mm_shape* shape, const void* dy, const vo
 moe_status moe_grouped_mm_dw(const moe_mm_shape* shape, const void* x, const void* dy, const int32_t* offsets,
                              void* dw, hipStream_t stream);
 
+/* The kernel form that a product of these sizes takes on a GPU of `cus` compute units (0: of the
+ * current device): "256x256", "256x256 stream" (weight gradients), "128x128", "64x64", "32x64
+ * thin" or "16x64 thin".  Forms differ in speed and in the order of their sums.  For tests and
+ * for reading traces; enqueues nothing, and with cus > 0 needs no GPU.  NULL where the product
+ * would be refused (the reason in moe_last_error()). */
+typedef enum { MOE_MM_Y = 0, MOE_MM_DX = 1, MOE_MM_DW = 2, MOE_MM_INT8 = 3 } moe_mm_product;
+const char* moe_grouped_mm_form(const moe_mm_shape* shape, int32_t product, int32_t cus);
+
 /* 8-bit rows: scale[r] = max_k |x[r, k]| / 127 in fp32, q[r, k] = x[r, k] / scale[r] to the
  * nearest integer (ties to even), in [-127, 127].  A row of zeros has scale 0 and q 0; a
  * row that holds an infinity or a NaN has scale NaN and q 0.

@@ -26,7 +26,7 @@ EXPORTS = ["moe_workspace_size", "moe_workspace_layout", "moe_capacity_rows", "m
            "moe_forward_noalloc", "moe_router_stats", "moe_status_str", "moe_last_error",
            "moe_peak_mfma_bf16",
            "moe_peak_hbm_read", "moe_peak_hbm_copy",
-           "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw", "moe_grouped_mm_int8",
+           "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw", "moe_grouped_mm_int8", "moe_grouped_mm_form",
            "moe_quantize_rows", "moe_quantize_experts", "moe_dropout", "moe_gated_act",
            "moe_gated_act_grad", "moe_combine_grad"]
 
@@ -121,6 +121,8 @@ def load(path: str = LIB_PATH):
     lib.moe_peak_hbm_copy.restype = ctypes.c_int
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
+    lib.moe_grouped_mm_form.argtypes = [mp, i32, i32]
+    lib.moe_grouped_mm_form.restype = ctypes.c_char_p
     lib.moe_last_error.argtypes = []
     lib.moe_last_error.restype = ctypes.c_char_p
     _lib = lib
@@ -254,6 +256,19 @@ def call(name: str, *args):
     code = (operators.get(name) or operator(name))(*args)
     if code != 0:
         failed(name, code)
+
+
+MM_PRODUCTS = {"y": 0, "dx": 1, "dw": 2, "int8": 3}
+
+
+def grouped_mm_form(product: str, rows: int, E: int, K: int, N: int, dtype: int = MOE_BF16, cus: int = 0) -> str:
+    """The kernel form that a product ("y", "dx", "dw" or "int8") of these sizes takes on a GPU of
+    `cus` compute units (0: the current device); see moe_grouped_mm_form."""
+    s = MmShape(rows, E, K, N, dtype, dtype, 0)
+    form = load().moe_grouped_mm_form(ctypes.byref(s), MM_PRODUCTS[product], cus)
+    if form is None:
+        raise ValueError(load().moe_last_error().decode())
+    return form.decode()
 
 
 NOALLOC_SCRATCH_BYTES = 256 << 20

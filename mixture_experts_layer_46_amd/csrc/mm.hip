@@ -159,21 +159,24 @@ hipError_t go(const MmArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// Groups of middling size go in a stream of tiles.  Smaller ones are a matter of writing the
+// matrices, which many workgroups at once do better; larger ones of the steps themselves.  Here
+// and there, in us: 64 experts, 2048 x 1408, rows a group 32: 85 and 95, 64: 95 and 95, 256: 153
+// and 150; 8 experts, 4096 x 4096, 64: 76 and 65; 256 experts, 1024 x 512, 234: 105 and 101; 8
+// experts, 4096 x 14336, 1024: 890 and 921.
+bool mm_streams(const MmArgs& a) {
+    const long long groups = a.rows < a.E ? a.rows : a.E;
+    return a.rows >= 48 * groups && a.rows < 640 * groups;
+}
+
 hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t st) {
     const bool f = out_dtype == MOE_F32;
     switch (kind) {
         case 0: return go<Op<0, Elem::bf16>, bf16_t>(a, st);
         case 1: return go<Op<1, Elem::bf16>, bf16_t>(a, st);
-        case 2: {
-            // Groups of middling size go in a stream of tiles.  Smaller ones are a matter of
-            // writing the matrices, which many workgroups at once do better; larger ones of the
-            // steps themselves.  Here and there, in us: 64 experts, 2048 x 1408, rows a group 32:
-            // 85 and 95, 64: 95 and 95, 256: 153 and 150; 8 experts, 4096 x 4096, 64: 76 and 65;
-            // 256 experts, 1024 x 512, 234: 105 and 101; 8 experts, 4096 x 14336, 1024: 890 and 921.
-            const long long groups = a.rows < a.E ? a.rows : a.E;
-            if (a.rows >= 48 * groups && a.rows < 640 * groups) return launch_mm_stream(out_dtype, a, st);
+        case 2:
+            if (mm_streams(a)) return launch_mm_stream(out_dtype, a, st);
             return f ? go<Op<2, Elem::bf16>, float>(a, st) : go<Op<2, Elem::bf16>, bf16_t>(a, st);
-        }
         default: return f ? go<Op<3, Elem::i8>, float>(a, st) : go<Op<3, Elem::i8>, bf16_t>(a, st);
     }
 }

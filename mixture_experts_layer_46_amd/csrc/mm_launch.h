@@ -22,8 +22,11 @@ struct MmArgs {
 hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);
 // whether a launch can hold the call's workgroups
 bool mm_fits(int kind, int dtype, const MmArgs& a);
+// the form it takes on a GPU of `cus` compute units, as moe_grouped_mm_form names it (mm_fits)
+const char* mm_form(int kind, int dtype, const MmArgs& a, int cus);
 // the forms: 256 x 256 tiles (bf16, int8); tiles of 64 or 128 (fp32: 64); 16 or 32 rows with the
 // contraction split over 8 or 4 wavefronts (kind 2: 32 rows)
+bool mm_streams(const MmArgs& a);         // whether large weight gradients go in a stream of tiles
 hipError_t launch_mm_stream(int out_dtype, const MmArgs& a, hipStream_t st);              // kind 2 of large
 hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t st);
 hipError_t launch_mm_mid(int tile, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);

@@ -98,8 +98,10 @@ bool mm_fits(int kind, int dtype, const MmArgs& a) {
     return false;
 }
 
-hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
-    const int cus = device_cu_count();
+namespace {
+
+// the form with the shortest estimate, or -1: mm_fits refuses such calls before
+int pick(int kind, int dtype, const MmArgs& a, int cus) {
     int best = -1;
     double t_best = 0;
     for (int f = 0; f < FORMS; ++f) {
@@ -107,14 +109,31 @@ hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStr
         const double t = estimate(kind, dtype, a, f, cus);
         if (best < 0 || t < t_best) best = f, t_best = t;
     }
-    switch (best) {
+    return best;
+}
+
+}  // namespace
+
+const char* mm_form(int kind, int dtype, const MmArgs& a, int cus) {
+    switch (pick(kind, dtype, a, cus)) {
+        case LARGE: return kind == 2 && mm_streams(a) ? "256x256 stream" : "256x256";
+        case MID128: return "128x128";
+        case MID64: return "64x64";
+        case THIN32: return "32x64 thin";
+        case THIN16: return "16x64 thin";
+    }
+    return nullptr;
+}
+
+hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
+    switch (pick(kind, dtype, a, device_cu_count())) {
         case LARGE: return launch_mm_large(kind, out_dtype, a, st);
         case MID128: return launch_mm_mid(128, kind, dtype, out_dtype, a, st);
         case MID64: return launch_mm_mid(64, kind, dtype, out_dtype, a, st);
         case THIN32: return launch_mm_thin(32, kind, dtype, out_dtype, a, st);
         case THIN16: return launch_mm_thin(16, kind, dtype, out_dtype, a, st);
     }
-    return hipErrorInvalidConfiguration;                                  // mm_fits refuses such calls before
+    return hipErrorInvalidConfiguration;
 }
 
 }  // namespace moe

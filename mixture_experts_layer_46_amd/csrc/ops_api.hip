@@ -104,10 +104,14 @@ moe_status check_ld(int64_t ld, int32_t F, const char* name) {
     return MOE_OK;
 }
 
+moe_status too_many(const moe_mm_shape& s, const char* where) {
+    return fail(MOE_ERR_UNSUPPORTED, "%s: too many output tiles for one launch (rows=%lld E=%d K=%d N=%d)", where,
+                (long long)s.rows, s.E, s.K, s.N);
+}
+
+// `kind` is a moe_mm_product, and one of the kinds of mm_tile.h
 moe_status run_mm(int kind, const moe_mm_shape& s, const MmArgs& a, hipStream_t st, const char* where) {
-    if (!mm_fits(kind, s.dtype, a))
-        return fail(MOE_ERR_UNSUPPORTED, "%s: too many output tiles for one launch (rows=%lld E=%d K=%d N=%d)", where,
-                    (long long)s.rows, s.E, s.K, s.N);
+    if (!mm_fits(kind, s.dtype, a)) return too_many(s, where);
     HIPCHK(launch_mm(kind, s.dtype, s.out_dtype, a, st), where);
     return MOE_OK;
 }
@@ -128,7 +132,7 @@ moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, const void* 
     REQ(w, "w");
     REQ(offsets, "offsets");
     REQ(y, "y");
-    return run_mm(0, *shape, mm_args(*shape, x, w, y, offsets), stream, "grouped_mm");
+    return run_mm(MOE_MM_Y, *shape, mm_args(*shape, x, w, y, offsets), stream, "grouped_mm");
 }
 
 moe_status moe_grouped_mm_dx(const moe_mm_shape* shape, const void* dy, const void* w, const int32_t* offsets, void* dx,
@@ -139,7 +143,7 @@ moe_status moe_grouped_mm_dx(const moe_mm_shape* shape, const void* dy, const vo
     REQ(w, "w");
     REQ(offsets, "offsets");
     REQ(dx, "dx");
-    return run_mm(1, *shape, mm_args(*shape, dy, w, dx, offsets), stream, "grouped_mm_dx");
+    return run_mm(MOE_MM_DX, *shape, mm_args(*shape, dy, w, dx, offsets), stream, "grouped_mm_dx");
 }
 
 moe_status moe_grouped_mm_dw(const moe_mm_shape* shape, const void* x, const void* dy, const int32_t* offsets, void* dw,
@@ -151,7 +155,16 @@ moe_status moe_grouped_mm_dw(const moe_mm_shape* shape, const void* x, const voi
     }
     REQ(offsets, "offsets");
     REQ(dw, "dw");
-    return run_mm(2, *shape, mm_args(*shape, x, dy, dw, offsets), stream, "grouped_mm_dw");
+    return run_mm(MOE_MM_DW, *shape, mm_args(*shape, x, dy, dw, offsets), stream, "grouped_mm_dw");
+}
+
+const char* moe_grouped_mm_form(const moe_mm_shape* shape, int32_t product, int32_t cus) {
+    if (product < MOE_MM_Y || product > MOE_MM_INT8) return fail(MOE_ERR_SHAPE, "product %d unknown", product), nullptr;
+    if (cus < 0) return fail(MOE_ERR_SHAPE, "cus = %d < 0", cus), nullptr;
+    if (check_mm(shape, product == MOE_MM_INT8, product == MOE_MM_DW) != MOE_OK) return nullptr;
+    const MmArgs a = mm_args(*shape, nullptr, nullptr, nullptr, nullptr);
+    if (!mm_fits(product, shape->dtype, a)) return too_many(*shape, "grouped_mm_form"), nullptr;
+    return mm_form(product, shape->dtype, a, cus ? cus : device_cu_count());
 }
 
 moe_status moe_quantize_rows(int32_t dtype, int64_t rows, int32_t K, const void* x, int8_t* q, float* scale,
@@ -194,7 +207,7 @@ moe_status moe_grouped_mm_int8(const moe_mm_shape* shape, const int8_t* xq, cons
     MmArgs a = mm_args(*shape, xq, wq, y, offsets);
     a.xs = x_scale;
     a.ws = w_scale;
-    return run_mm(3, *shape, a, stream, "grouped_mm_int8");
+    return run_mm(MOE_MM_INT8, *shape, a, stream, "grouped_mm_int8");
 }
 
 moe_status moe_dropout(int32_t dtype, int64_t n, const moe_dropout_spec* spec, const void* x, void* y,
