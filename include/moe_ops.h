@@ -83,7 +83,7 @@ moe_status moe_quantize_rows(int32_t dtype, int64_t rows, int32_t K, const void*
 
 /* 8-bit experts, made once: w [E, K, N] dtype -> q [E, N, K] int8 (contraction contiguous),
  * scale [E, N] fp32, each output channel of each expert quantised over K as a row above.
- *   K a multiple of 16, N of 8. */
+ *   E <= 256; K a multiple of 16, at most 131056, N of 8, at most 2^20. */
 moe_status moe_quantize_experts(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* w, int8_t* q,
                                 float* scale, hipStream_t stream);
 

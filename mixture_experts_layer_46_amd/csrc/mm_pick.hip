@@ -9,9 +9,9 @@
 //
 // The three constants of a form come from some 12000 random calls (1-256 groups, 1-60000 rows,
 // matrices of 64-8192 by 64-16384, even, Zipf and gapped loads), each timed in every form.
-// Over calls that the fit did not see, the form picked is slower than the best one by 1.4% (x W),
-// 2.6% (dy W^T), 2.1% (x^T dy), 1.4% (int8) and 1.1% (fp32) in the geometric mean; the best
-// single form would be 20%, 20%, 16%, 20% and 32% slower.  fp32 has no tiles of 128: they won
+// Over 11000 further calls the form picked is slower than the best one by 1.4% (x W), 2.0% (dy
+// W^T), 2.9% (x^T dy), 1.7% (int8) and 1.0% (fp32) in the geometric mean; the best single form
+// would be 23%, 20%, 16%, 15% and 24% slower.  fp32 has no tiles of 128: they won
 // 0.05% (weight gradients 0.6%) over the other forms.  The thin form of a weight gradient
 // wins where one or two groups have small matrices: over such calls 6% (16 bits) and 18%
 // (fp32) in the mean, at most 2.3 times.
@@ -30,11 +30,13 @@ enum Form { LARGE, MID128, MID64, THIN32, THIN16, FORMS };
 
 struct Shape {
     int bm, bn;           // tile
-    int per_cu;           // workgroups a CU holds
+    int per_cu;           // workgroups that a CU is taken to hold at once (see below)
     int split;            // wavefronts that share the contraction
     int threads;
     double rate;          // bytes per us that it reaches when weights streamed once are all there is
 };
+// per_cu is the model's, and the constants were fitted with it: what a CU's 160 KB of LDS hold
+// is 1, 2, 3 (fp32: 4), 2 and 1 of these workgroups (135, 67, 51 (35), 75 and 123 KB each).
 constexpr Shape kShape[FORMS] = {{256, 256, 1, 1, 512, 5.0e6}, {128, 128, 2, 1, 256, 5.3e6}, {64, 64, 4, 1, 256, 5.4e6},
                                  {32, 64, 2, 4, 256, 5.6e6},   {16, 64, 1, 8, 512, 4.9e6}};
 

@@ -271,7 +271,8 @@ def quantize_rows(x):
 
 def quantize_experts(w):
     """8-bit expert matrices of w [E, K, N] (bf16 or fp32), made once: (q [E, N, K] int8,
-    scale [E, N] fp32), each output channel quantised over K as quantize_rows does a row."""
+    scale [E, N] fp32), each output channel quantised over K as quantize_rows does a row.  K a
+    multiple of 16, at most 131056, N of 8."""
     _dims(w, 3, "w")
     code = _code(w, "w")
     E, K, N = w.shape
@@ -644,7 +645,7 @@ class _Permute(torch.autograd.Function):
 class _Combine(torch.autograd.Function):
     """The combine; `whole`: every row has a pair.  Where a capacity left rows without one, their
     gradient is zeros, written before the others' (combine_grad leaves such rows unset, and
-    nothing unset may pass through autograd)."""
+    nothing unset may pass through autograd; 8192 tokens of 2, 4096 wide bf16: 49 -> 76 us)."""
 
     @staticmethod
     def forward(ctx, y_perm, row_of_pair, topk_w, whole):
