@@ -87,15 +87,18 @@ def _given(t, name, dtype, shape, dev):
             _dense(t, name, dev)
 
 
+def _end(t):
+    """The address behind a tensor's last element."""
+    if t.is_contiguous():
+        return t.data_ptr() + t.nbytes
+    return t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
 def _overlap(a, b):
     """Whether two tensors share memory.  Halves of one packed tensor, whose rows take turns, do
     not."""
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    def end(t):
-        return t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
     a0, b0 = a.data_ptr(), b.data_ptr()
-    if end(a) <= b0 or end(b) <= a0:
+    if (_end(a) <= b0 if a0 <= b0 else _end(b) <= a0) or a.numel() == 0 or b.numel() == 0:
         return False
     if a.shape == b.shape and a.dtype == b.dtype and a.stride() == b.stride() and a.dim() == 2 and a.shape[0] > 1:
         row, width = a.stride(0) * a.element_size(), a.shape[1] * a.element_size()
@@ -186,7 +189,8 @@ def _mm(x, w, offsets, out, transposed, xname, oname):
         out = x.new_empty((R, cout))
     _launch(dev, "moe_grouped_mm_dx" if transposed else "moe_grouped_mm", _mm_shape(R, E, K, N, code, code, rest),
             x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
-    _wrote(None if rest else out)
+    if not rest:
+        _wrote(out)
     return out
 
 
@@ -250,7 +254,8 @@ def grouped_mm_dw(x, dy, offsets, out=None, dtype=None):
     dw = torch.empty((E, K, N), dtype=dtype, device=x.device) if out is None else out
     _launch(dev, "moe_grouped_mm_dw", _mm_shape(R, E, K, N, code, _CODES[dtype], False), x.data_ptr(), dy.data_ptr(),
             offsets.data_ptr(), dw.data_ptr())
-    _wrote(out)
+    if out is not None:
+        _wrote(out)
     return dw
 
 
@@ -313,7 +318,8 @@ def grouped_mm_int8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out
         out = torch.empty((R, N), dtype=dtype, device=xq.device)
     _launch(dev, "moe_grouped_mm_int8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
             x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
-    _wrote(None if rest else out)
+    if not rest:
+        _wrote(out)
     return out
 
 
@@ -339,7 +345,8 @@ def _dropout(x, p, seed, step, out):
     dev = _dense(x, "x")
     y = torch.empty_like(x) if out is None else out
     _launch(dev, "moe_dropout", code, x.numel(), _spec(p, seed, step, dev), x.data_ptr(), y.data_ptr())
-    _wrote(out)
+    if out is not None:
+        _wrote(out)
     return y
 
 
@@ -411,7 +418,8 @@ def _gated_act(a, b, p, seed, step, out):
         _apart(out, "out", a=a, b=b)
     h = a.new_empty((R, F)) if out is None else out
     _launch(dev, "moe_gated_act", code, R, F, _spec(p, seed, step, dev), a.data_ptr(), lda, bp, ldb, h.data_ptr())
-    _wrote(out)
+    if out is not None:
+        _wrote(out)
     return h
 
 
@@ -565,7 +573,8 @@ def forward_int8(x, w_gate, experts: QuantizedExperts, top_k, bias=None, flags=0
         g = M.permute(idx, E, x=x, capacity=_lib.capacity_rows(capacity_factor, T, top_k, E))
         y = grouped_ffn_int8(g["x_perm"], g["offsets"], experts)
         M.combine(y, g["row_of_pair"], w, out=out)
-    _wrote(given)
+    if given is not None:
+        _wrote(given)
     return out
 
 
