@@ -7,12 +7,15 @@
  *   dropout            counter-based, its mask never stored; alone or with the experts'
  *                      gated activation, and the gradient of that
  *   combine's gradient
+ *   norms              before and after a block, with its gate and residual scale, and the
+ *                      gradients
  *
  * Conventions are those of moe.h: device pointers, 16-byte aligned; dense row-major arrays
  * unless a row stride is given; calls only enqueue on `stream`; nothing is allocated or
  * kept; arguments are checked on the host before anything is enqueued (moe_status, the
- * detail in moe_last_error()).  None of these calls needs a workspace, so any number of
- * them may run at the same time, captured or not, on buffers of their own.  Outputs must
+ * detail in moe_last_error()).  None of these calls needs a workspace (but
+ * moe_residual_norm_grad, which says so), so any number of them may run at the same time,
+ * captured or not, on buffers of their own.  Outputs must
  * not overlap inputs, except that moe_dropout may work in place.
  *
  * Results are deterministic: every output is written by one workgroup, sums run in a fixed
@@ -141,6 +144,42 @@ moe_status moe_gated_act_grad(int32_t dtype, int64_t rows, int32_t F, const moe_
 moe_status moe_combine_grad(int32_t dtype, int64_t T, int32_t k, int32_t H, int64_t rows, const void* dout,
                             const void* y_perm, const int32_t* row_of_pair, const float* topk_w, void* dy_perm,
                             float* dtopk_w, hipStream_t stream);
+
+/* The norms before and after a block, with the block's gate and residual scale:
+ *
+ *   v = z r(z) w_post    y = scale x + gate v    u = y r(y) w_next    r(t) = 1 / sqrt(mean t^2 + eps)
+ *
+ * x is the stream that runs past the block, z the block's output, y the stream behind it and u
+ * the next block's input.  Everything between inputs and outputs is fp32; u is made from the
+ * unrounded y.  A row whose mean square lies outside fp32's range is not supported. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_norm_gate;
+typedef struct {
+    int64_t T;           /* rows, < 2^31 */
+    int64_t ldx, ldz;    /* elements from one row of x / z to the next (multiples of 8, at least H) */
+    int32_t H;           /* a multiple of 8, at most 16384 */
+    int32_t dtype;       /* MOE_F32 or MOE_BF16: x, z, y, u and their gradients */
+    int32_t gate;        /* moe_norm_gate: what gate and dgate hold, [H] or [T] */
+    float   scale, eps;  /* eps > 0 */
+} moe_norm_shape;
+
+/* x, z [T, H]; w_post, w_next [H], gate [H] or [T] fp32; y, u [T, H] dense out.
+ *   w_post NULL: v = z.  gate NULL exactly with MOE_GATE_NONE: y = scale x + v.  w_next and u
+ *   NULL together: no u.  z NULL: u = x r(x) w_next, the norm alone; w_post, gate and y are then
+ *   NULL and w_next is not.  T == 0 returns MOE_OK and enqueues nothing. */
+moe_status moe_residual_norm(const moe_norm_shape* shape, const void* x, const void* z, const float* w_post,
+                             const float* gate, const float* w_next, void* y, void* u, hipStream_t stream);
+
+/* Bytes of workspace that the gradient needs: partial sums over rows (host only). */
+moe_status moe_residual_norm_grad_workspace(const moe_norm_shape* shape, size_t* bytes);
+
+/* Its gradient, from the inputs alone.  dy, du [T, H] dense: the gradients of y (NULL: zeros) and u
+ * (NULL exactly when w_next is).  Out: dx, dz [T, H] dense (dz NULL exactly when z is), dw_post,
+ * dw_next [H] and dgate [H] or [T] fp32, each NULL exactly when its parameter is; they are fully
+ * overwritten, also when T == 0.  Two calls may not use one workspace at the same time. */
+moe_status moe_residual_norm_grad(const moe_norm_shape* shape, const void* dy, const void* du, const void* x,
+                                  const void* z, const float* w_post, const float* gate, const float* w_next,
+                                  void* dx, void* dz, float* dw_post, float* dgate, float* dw_next, void* workspace,
+                                  size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -28,7 +28,8 @@ EXPORTS = ["moe_workspace_size", "moe_workspace_layout", "moe_capacity_rows", "m
            "moe_peak_hbm_read", "moe_peak_hbm_copy",
            "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw", "moe_grouped_mm_int8", "moe_grouped_mm_form",
            "moe_quantize_rows", "moe_quantize_experts", "moe_dropout", "moe_gated_act",
-           "moe_gated_act_grad", "moe_combine_grad"]
+           "moe_gated_act_grad", "moe_combine_grad",
+           "moe_residual_norm", "moe_residual_norm_grad_workspace", "moe_residual_norm_grad"]
 
 MOE_MM_ZERO_REST = 0x1
 
@@ -57,6 +58,11 @@ class MmShape(ctypes.Structure):
 class DropoutSpec(ctypes.Structure):
     _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("step", ctypes.c_uint64),
                 ("step_device", ctypes.c_void_p)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldz", ctypes.c_int64), ("H", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -95,7 +101,8 @@ def load(path: str = LIB_PATH):
         "moe_forward_noalloc": [sp, vp, f32p, f32p, vp, vp, vp, vp, st],
         "moe_router_stats": [sp, f32p, f32p, i32p, i32p, f32p, st],
     }
-    mp, dp = ctypes.POINTER(MmShape), ctypes.POINTER(DropoutSpec)
+    mp, dp, np = ctypes.POINTER(MmShape), ctypes.POINTER(DropoutSpec), ctypes.POINTER(NormShape)
+    sz = ctypes.c_size_t
     i32, i64 = ctypes.c_int32, ctypes.c_int64
     sig.update({
         "moe_grouped_mm": [mp, vp, vp, i32p, vp, st],
@@ -108,6 +115,9 @@ def load(path: str = LIB_PATH):
         "moe_gated_act": [i32, i64, i32, dp, vp, i64, vp, i64, vp, st],
         "moe_gated_act_grad": [i32, i64, i32, dp, vp, vp, i64, vp, i64, vp, i64, vp, i64, st],
         "moe_combine_grad": [i32, i64, i32, i32, i64, vp, vp, i32p, f32p, vp, f32p, st],
+        "moe_residual_norm": [np, vp, vp, f32p, f32p, f32p, vp, vp, st],
+        "moe_residual_norm_grad_workspace": [np, ctypes.POINTER(sz)],
+        "moe_residual_norm_grad": [np, vp, vp, vp, vp, f32p, f32p, f32p, vp, vp, f32p, f32p, f32p, vp, sz, st],
     })
     for name, args in sig.items():
         fn = getattr(lib, name)

@@ -69,4 +69,23 @@ hipError_t launch_combine_grad(const void* dout, const void* y_perm, const int32
                                void* dy_perm, float* dw, long long T, int k, int H, int dtype, long long rows,
                                hipStream_t st);
 
+struct NormArgs {                 // moe_residual_norm
+    const void *x, *z;            // z NULL: u = norm(x)
+    const float *w_post, *gate, *w_next;
+    void *y, *u;
+    long long T, ldx, ldz;
+    int H, gate_kind;             // a moe_norm_gate
+    float scale, eps;
+};
+struct NormGradArgs {             // moe_residual_norm_grad; f.y and f.u unused
+    NormArgs f;
+    const void *dy, *du;
+    void *dx, *dz;
+    float *dw_post, *dgate, *dw_next;
+    float* parts;                 // [norm_grad_parts][3][H]
+};
+int norm_grad_parts(long long T, int H);
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t st);
+hipError_t launch_norm_grad(const NormGradArgs& g, int dtype, hipStream_t st);
+
 }  // namespace moe

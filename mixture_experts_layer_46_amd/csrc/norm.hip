@@ -1,0 +1,410 @@
+// The norms before and after a block, fused with the block's gate and residual scale, and
+// their gradient (formulas: include/moe_ops.h).
+//
+//   v = z r(z) w_post    y = scale x + gate v    u = y r(y) w_next    r(t) = 1 / sqrt(mean t^2 + eps)
+//
+// Everything between the inputs and the rounded outputs is fp32, u from the unrounded y.  The
+// gradient needs nothing but the inputs: with t = du w_next, and yh = y r(y), zh = z r(z),
+//
+//   g  = dy + r(y) (t - yh mean(t yh))                      the gradient of y
+//   dx = scale g      p = g gate w_post      dz = r(z) (p - zh mean(p zh))
+//   dw_next = sum du yh   dw_post = sum g gate zh   dgate = sum g w_post zh   (over rows, or columns)
+//
+// so a row costs one read of each input and one write of each output, with two (three)
+// reductions over the row in between.  Memory bounds both kernels: the row stays in registers,
+// P threads a row (a wavefront up to a workgroup of 512), the next row's loads start before
+// this row's reductions, and a thread's columns do not change, so that the parameters are read
+// once and the sums over rows stay in registers until the end.  These are added up over
+// workgroups by a second kernel, from partial sums in the caller's workspace, in a fixed order.
+#include "common.h"
+#include "launch.h"
+#include "mm_launch.h"
+
+namespace moe {
+
+namespace {
+
+template <typename T>
+struct Chunk;                                 // 8 elements as they lie in memory
+template <>
+struct Chunk<bf16_t> {
+    uint4 d;
+    __device__ __forceinline__ void get(const bf16_t* p) { d = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void clear() { d = uint4{0u, 0u, 0u, 0u}; }
+    __device__ __forceinline__ void open(float (&v)[8]) const {
+        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[2 * q] = bf16lo_to_f32(w[q]), v[2 * q + 1] = bf16hi_to_f32(w[q]);
+    }
+    static __device__ __forceinline__ void put(bf16_t* p, const float (&v)[8]) {
+        *reinterpret_cast<uint4*>(p) = uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                             pack_bf16x2(v[6], v[7])};
+    }
+};
+template <>
+struct Chunk<float> {
+    float4 a, b;
+    __device__ __forceinline__ void get(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void open(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    static __device__ __forceinline__ void put(float* p, const float (&v)[8]) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+
+// Sums over lanes, without LDS: over each 16 lanes (in all of them), and over a wavefront.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float sum16(float x) {
+    x = dpp_add<0xB1, 0xf>(x);                // lane ^ 1
+    x = dpp_add<0x4E, 0xf>(x);                // lane ^ 2
+    x = dpp_add<0x141, 0xf>(x);               // mirrored in 8 lanes
+    return dpp_add<0x140, 0xf>(x);            // mirrored in 16
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    x = sum16(x);
+    x = dpp_add<0x142, 0xa>(x);               // lane 15 of rows 0 and 2 to the rows after them
+    x = dpp_add<0x143, 0xc>(x);               // lane 31 to the upper half
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+// A row's threads: a wavefront (RPW = 4 rows in a workgroup of 256) or the workgroup (RPW = 1,
+// as many wavefronts as the row needs), with C chunks of 8 columns each.
+template <int RPW>
+__device__ __forceinline__ int row_threads() { return RPW > 1 ? 64 : (int)blockDim.x; }
+template <int RPW>
+__device__ __forceinline__ int row_thread() { return RPW > 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x; }
+
+// Sums of two numbers over the threads of a row.  `slot` alternates from call to call: a
+// wavefront writes a slot again only after the barrier behind which all have read it.  red[.]
+// of wavefronts that the workgroup lacks are zeros.
+template <int RPW>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*red)[16], int& slot) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (RPW == 1) {
+        if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = float2{a, b};
+        __syncthreads();
+        const float2 r = red[slot][threadIdx.x & 15];
+        a = sum16(r.x);
+        b = sum16(r.y);
+        slot ^= 1;
+    }
+    return float2{a, b};
+}
+__device__ __forceinline__ void clear_red(float2 (*red)[16]) {
+    if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = float2{0.f, 0.f};
+    __syncthreads();
+}
+
+// This thread's columns of a vector of H parameters (1 where there is none).
+template <int C>
+__device__ __forceinline__ void get_params(const float* __restrict__ w, int P, int t, int H, float (&v)[C][8]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c * P + t) * 8;
+        Chunk<float> k;
+        k.a = k.b = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (w && col < H) k.get(w + col);
+        k.open(v[c]);
+    }
+}
+template <int C, typename T>
+__device__ __forceinline__ void get_row(const T* __restrict__ row, bool live, int P, int t, int H, Chunk<T> (&v)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c * P + t) * 8;
+        v[c].clear();
+        if (live && col < H) v[c].get(row + col);
+    }
+}
+
+template <typename T, int RPW, int C>
+__global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm(NormArgs a) {
+    __shared__ float2 red[2][16];
+    if constexpr (RPW == 1) clear_red(red);
+    int slot = 0;
+    const int P = row_threads<RPW>(), t = row_thread<RPW>(), sub = RPW > 1 ? (int)(threadIdx.x >> 6) : 0, H = a.H;
+    const long long first = (long long)blockIdx.x * RPW + sub, step = (long long)gridDim.x * RPW;
+    const float over = 1.f / (float)H;
+    const T *x = (const T*)a.x, *z = (const T*)a.z;
+    float w1[C][8], gc[C][8], w2[C][8];
+    get_params<C>(a.w_post, P, t, H, w1);
+    get_params<C>(a.gate_kind == 1 ? a.gate : nullptr, P, t, H, gc);
+    get_params<C>(a.w_next, P, t, H, w2);
+    Chunk<T> xn[C], zn[C];
+    get_row<C>(x + first * a.ldx, first < a.T, P, t, H, xn);
+    get_row<C>(z + first * a.ldz, z && first < a.T, P, t, H, zn);
+    // every row of threads runs the same number of rounds, so that the barriers match
+    for (long long r0 = (long long)blockIdx.x * RPW; r0 < a.T; r0 += step) {
+        const long long r = r0 + sub;
+        const bool live = r < a.T;
+        float y[C][8], v[C][8];
+#pragma unroll
+        for (int c = 0; c < C; ++c) xn[c].open(y[c]), zn[c].open(v[c]);
+        const float gt = a.gate_kind == 2 && live ? a.gate[r] : 1.f;
+        const bool more = r + step < a.T;
+        get_row<C>(x + (r + step) * a.ldx, more, P, t, H, xn);
+        get_row<C>(z + (r + step) * a.ldz, z && more, P, t, H, zn);
+        if (z) {
+            float rz = 1.f;
+            if (a.w_post) {
+                float s = 0.f;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s = fmaf(v[c][j], v[c][j], s);
+                rz = rsqrtf(row_sum<RPW>(s, 0.f, red, slot).x * over + a.eps);
+            }
+            const float f = rz * gt;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[c][j] = fmaf(a.scale, y[c][j], v[c][j] * f * (w1[c][j] * gc[c][j]));
+                const int col = (c * P + t) * 8;
+                if (live && col < H) Chunk<T>::put((T*)a.y + r * H + col, y[c]);
+            }
+        }
+        if (a.w_next) {
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(y[c][j], y[c][j], s);
+            const float ry = rsqrtf(row_sum<RPW>(s, 0.f, red, slot).x * over + a.eps);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[c][j] *= ry * w2[c][j];
+                const int col = (c * P + t) * 8;
+                if (live && col < H) Chunk<T>::put((T*)a.u + r * H + col, y[c]);
+            }
+        }
+    }
+}
+
+// HOLD: the parameters stay in registers; otherwise (rows above 8192) they are read again for
+// each row, since the sums over rows take the registers.
+template <typename T, int RPW, int C, bool HOLD>
+__global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm_grad(NormGradArgs g) {
+    const NormArgs& a = g.f;
+    __shared__ float2 red[2][16];
+    __shared__ float sums[RPW > 1 ? 64 * C * 8 : 1];
+    if constexpr (RPW == 1) clear_red(red);
+    int slot = 0;
+    const int P = row_threads<RPW>(), t = row_thread<RPW>(), sub = RPW > 1 ? (int)(threadIdx.x >> 6) : 0, H = a.H;
+    const long long first = (long long)blockIdx.x * RPW + sub, step = (long long)gridDim.x * RPW;
+    const float over = 1.f / (float)H;
+    const T *x = (const T*)a.x, *z = (const T*)a.z, *dy = (const T*)g.dy, *du = (const T*)g.du;
+    const bool need_z = z && (a.w_post || a.w_next || a.gate_kind), channel = a.gate_kind == 1;
+    const float* gate_c = channel ? a.gate : nullptr;
+    float w1[C][8], gc[C][8], w2[C][8];
+    float s1[C][8] = {}, sg[C][8] = {}, s2[C][8] = {};
+    if constexpr (HOLD) {
+        get_params<C>(a.w_post, P, t, H, w1);
+        get_params<C>(gate_c, P, t, H, gc);
+        get_params<C>(a.w_next, P, t, H, w2);
+    }
+    Chunk<T> xn[C], zn[C], dyn[C], dun[C];
+    auto start = [&](long long r) {
+        const bool live = r < a.T;
+        get_row<C>(x + r * a.ldx, live && a.w_next, P, t, H, xn);
+        get_row<C>(z + r * a.ldz, live && need_z, P, t, H, zn);
+        get_row<C>(dy + r * H, live && dy, P, t, H, dyn);
+        get_row<C>(du + r * H, live && a.w_next, P, t, H, dun);
+    };
+    start(first);
+    for (long long r0 = (long long)blockIdx.x * RPW; r0 < a.T; r0 += step) {
+        const long long r = r0 + sub;
+        const bool live = r < a.T;
+        if constexpr (!HOLD) {
+            get_params<C>(a.w_post, P, t, H, w1);
+            get_params<C>(gate_c, P, t, H, gc);
+            get_params<C>(a.w_next, P, t, H, w2);
+        }
+        float xv[C][8], zv[C][8], gv[C][8], uv[C][8];
+#pragma unroll
+        for (int c = 0; c < C; ++c) xn[c].open(xv[c]), zn[c].open(zv[c]), dyn[c].open(gv[c]), dun[c].open(uv[c]);
+        const float gt = a.gate_kind == 2 && live ? a.gate[r] : 1.f;
+        start(r + step);
+        float rz = 1.f;
+        if (a.w_post) {
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(zv[c][j], zv[c][j], s);
+            rz = rsqrtf(row_sum<RPW>(s, 0.f, red, slot).x * over + a.eps);
+        }
+        if (a.w_next) {
+            float sy = 0.f, st = 0.f;
+            if (z) {
+                const float f = rz * gt;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) xv[c][j] = fmaf(a.scale, xv[c][j], zv[c][j] * f * (w1[c][j] * gc[c][j]));
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sy = fmaf(xv[c][j], xv[c][j], sy);
+                    st = fmaf(uv[c][j] * w2[c][j], xv[c][j], st);
+                }
+            const float2 s = row_sum<RPW>(sy, st, red, slot);
+            const float ry = rsqrtf(s.x * over + a.eps), k = ry * ry * (s.y * over);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    gv[c][j] += ry * (uv[c][j] * w2[c][j] - xv[c][j] * k);
+                    s2[c][j] = fmaf(uv[c][j], xv[c][j] * ry, s2[c][j]);
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c * P + t) * 8;
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = a.scale * gv[c][j];
+            if (live && col < H) Chunk<T>::put((T*)g.dx + r * H + col, o);
+        }
+        if (z) {
+            float k = 0.f;
+            if (a.w_post || a.gate_kind == 2) {
+                float s = 0.f;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s = fmaf(gv[c][j] * (w1[c][j] * gc[c][j]), zv[c][j], s);
+                s = row_sum<RPW>(s, 0.f, red, slot).x;
+                if (a.gate_kind == 2 && live && t == 0) g.dgate[r] = s * rz;
+                if (a.w_post) k = s * rz * rz * over;
+            }
+            const float f = rz * gt;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int col = (c * P + t) * 8;
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float q = gv[c][j] * (zv[c][j] * f);
+                    s1[c][j] = fmaf(q, gc[c][j], s1[c][j]);
+                    sg[c][j] = fmaf(q, w1[c][j], sg[c][j]);
+                    o[j] = f * (gv[c][j] * (w1[c][j] * gc[c][j]) - zv[c][j] * k);
+                }
+                if (live && col < H) Chunk<T>::put((T*)g.dz + r * H + col, o);
+            }
+        }
+    }
+    // this workgroup's sums: [3][H] of the workspace, those of its rows of threads added in order
+    float* part = g.parts + (size_t)blockIdx.x * 3 * H;
+    auto put = [&](int which, float (&s)[C][8]) {
+        if constexpr (RPW == 1) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int col = (c * P + t) * 8;
+                if (col < H) Chunk<float>::put(part + (size_t)which * H + col, s[c]);
+            }
+        } else {
+            for (int k = 0; k < RPW; ++k) {
+                __syncthreads();
+                if (sub == k)
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float* p = sums + (c * P + t) * 8 + j;
+                            *p = k ? *p + s[c][j] : s[c][j];
+                        }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < H; i += 64 * RPW) part[(size_t)which * H + i] = sums[i];
+        }
+    };
+    if (a.w_post) put(0, s1);
+    if (channel) put(1, sg);
+    if (a.w_next) put(2, s2);
+}
+
+// Adds the workgroups' sums: 64 columns per workgroup, its 16 wavefronts over the partial sums.
+__global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ parts, int n, int H, float* d0, float* d1,
+                                                      float* d2) {
+    __shared__ float sums[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, which = blockIdx.y, col = blockIdx.x * 64 + lane;
+    float* d = which == 0 ? d0 : which == 1 ? d1 : d2;
+    if (!d) return;
+    float s = 0.f;
+    if (col < H)
+        for (int i = wave; i < n; i += 16) s += parts[((size_t)i * 3 + which) * H + col];
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < H) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += sums[i][lane];
+        d[col] = s;
+    }
+}
+
+// Rows up to 512: a wavefront each, four to a workgroup.  Longer ones: a workgroup each, a chunk
+// a thread up to 8192, then two.
+bool short_rows(int H) { return H <= 512; }
+int threads_for(int H) { return short_rows(H) ? 256 : ((H <= 8192 ? H / 8 : (H + 15) / 16) + 63) / 64 * 64; }
+
+template <typename T>
+hipError_t go(const NormArgs& a, hipStream_t st) {
+    const int NT = threads_for(a.H), rpw = short_rows(a.H) ? 4 : 1;
+    const long long want = (a.T + rpw - 1) / rpw, most = (long long)(1024 / NT < 1 ? 1 : 1024 / NT) * device_cu_count();
+    const dim3 grid((unsigned)(want < most ? want : most));
+    if (short_rows(a.H)) hipLaunchKernelGGL((k_norm<T, 4, 1>), grid, dim3(NT), 0, st, a);
+    else if (a.H <= 8192) hipLaunchKernelGGL((k_norm<T, 1, 1>), grid, dim3(NT), 0, st, a);
+    else hipLaunchKernelGGL((k_norm<T, 1, 2>), grid, dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t go_grad(const NormGradArgs& g, hipStream_t st) {
+    const dim3 grid((unsigned)norm_grad_parts(g.f.T, g.f.H));
+    const int H = g.f.H, NT = threads_for(H);
+    if (short_rows(H)) hipLaunchKernelGGL((k_norm_grad<T, 4, 1, true>), grid, dim3(NT), 0, st, g);
+    else if (H <= 8192) hipLaunchKernelGGL((k_norm_grad<T, 1, 1, true>), grid, dim3(NT), 0, st, g);
+    else hipLaunchKernelGGL((k_norm_grad<T, 1, 2, false>), grid, dim3(NT), 0, st, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// As many workgroups as 256 CUs hold at 1024 threads each, or as there are rows.
+int norm_grad_parts(long long T, int H) {
+    const int NT = threads_for(H), rpw = short_rows(H) ? 4 : 1, most = 256 * (1024 / NT < 1 ? 1 : 1024 / NT);
+    const long long want = (T + rpw - 1) / rpw;
+    return (int)(want < most ? want : most);
+}
+
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t st) {
+    return dtype == MOE_F32 ? go<float>(a, st) : go<bf16_t>(a, st);
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& g, int dtype, hipStream_t st) {
+    if (g.f.T > 0) {
+        const hipError_t e = dtype == MOE_F32 ? go_grad<float>(g, st) : go_grad<bf16_t>(g, st);
+        if (e != hipSuccess) return e;
+    }
+    float* dgate = g.f.gate_kind == 1 ? g.dgate : nullptr;
+    if (!g.dw_post && !dgate && !g.dw_next) return hipSuccess;
+    hipLaunchKernelGGL(k_norm_reduce, dim3((unsigned)((g.f.H + 63) / 64), 3), dim3(1024), 0, st, g.parts,
+                       norm_grad_parts(g.f.T, g.f.H), g.f.H, g.dw_post, dgate, g.dw_next);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -45,6 +45,7 @@ constexpr int kMaxDim = 1 << 20;          // K, N: 256 rows of fp32 stay below 2
 constexpr int kMaxInt8K = 131056;         // 128 * 128 * K < 2^31
 constexpr int64_t kMaxGrid = 1 << 24;     // workgroups of 256 threads: 2^32 work items a launch
 constexpr int64_t kMaxElems = 1ll << 34;
+constexpr int kMaxNorm = 16384;           // a row stays in a workgroup's registers
 
 moe_status check_dtype(int32_t dtype) {
     if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "dtype %d unknown", dtype);
@@ -114,6 +115,35 @@ moe_status run_mm(int kind, const moe_mm_shape& s, const MmArgs& a, hipStream_t 
     if (!mm_fits(kind, s.dtype, a)) return too_many(s, where);
     HIPCHK(launch_mm(kind, s.dtype, s.out_dtype, a, st), where);
     return MOE_OK;
+}
+
+moe_status check_norm(const moe_norm_shape* s, const void* z, const float* w_post, const float* gate,
+                      const float* w_next) {
+    if (!s) return fail(MOE_ERR_NULL, "shape is NULL");
+    CHECK(check_dtype(s->dtype));
+    if (s->T < 0) return fail(MOE_ERR_SHAPE, "T = %lld < 0", (long long)s->T);
+    if (s->T >= (1ll << 31)) return fail(MOE_ERR_UNSUPPORTED, "T = %lld >= 2^31", (long long)s->T);
+    if (s->H <= 0) return fail(MOE_ERR_SHAPE, "H = %d must be positive", s->H);
+    if (s->H % 8 || s->H > kMaxNorm)
+        return fail(MOE_ERR_UNSUPPORTED, "H = %d must be a multiple of 8, at most %d", s->H, kMaxNorm);
+    if (!(s->eps > 0.f && s->eps < INFINITY)) return fail(MOE_ERR_SHAPE, "eps = %g must be positive", (double)s->eps);
+    if (!std::isfinite(s->scale)) return fail(MOE_ERR_SHAPE, "scale = %g must be finite", (double)s->scale);
+    CHECK(check_ld(s->ldx, s->H, "ldx"));
+    if (s->gate < MOE_GATE_NONE || s->gate > MOE_GATE_TOKEN)
+        return fail(MOE_ERR_UNSUPPORTED, "gate kind %d unknown", s->gate);
+    if (s->T > 0 && (gate != nullptr) != (s->gate != MOE_GATE_NONE))
+        return fail(MOE_ERR_NULL, "gate and its kind (%d) do not match", s->gate);
+    if (z) {
+        CHECK(check_ld(s->ldz, s->H, "ldz"));
+    } else if (s->T > 0) {
+        if (w_post || gate) return fail(MOE_ERR_NULL, "w_post and gate need z");
+        if (!w_next) return fail(MOE_ERR_NULL, "w_next is NULL");
+    }
+    return MOE_OK;
+}
+NormArgs norm_args(const moe_norm_shape& s, const void* x, const void* z, const float* w_post, const float* gate,
+                   const float* w_next, void* y, void* u) {
+    return NormArgs{x, z, w_post, gate, w_next, y, u, (long long)s.T, (long long)s.ldx, (long long)s.ldz, s.H, s.gate, s.scale, s.eps};
 }
 
 }  // namespace
@@ -283,6 +313,74 @@ moe_status moe_combine_grad(int32_t dtype, int64_t T, int32_t k, int32_t H, int6
     REQ(dtopk_w, "dtopk_w");
     HIPCHK(launch_combine_grad(dout, y_perm, row_of_pair, topk_w, dy_perm, dtopk_w, T, k, H, dtype, rows, stream),
            "combine_grad");
+    return MOE_OK;
+}
+
+moe_status moe_residual_norm(const moe_norm_shape* shape, const void* x, const void* z, const float* w_post,
+                             const float* gate, const float* w_next, void* y, void* u, hipStream_t stream) {
+    CHECK(check_norm(shape, z, w_post, gate, w_next));
+    if (shape->T == 0) return MOE_OK;
+    REQ(x, "x");
+    if (z) {
+        REQ(z, "z");
+        REQ(y, "y");
+    } else if (y) {
+        return fail(MOE_ERR_NULL, "y needs z");
+    }
+    if ((u != nullptr) != (w_next != nullptr)) return fail(MOE_ERR_NULL, "w_next and u must be given together");
+    if (w_post) REQ(w_post, "w_post");
+    if (gate) REQ(gate, "gate");
+    if (w_next) REQ(w_next, "w_next");
+    if (u) REQ(u, "u");
+    HIPCHK(launch_norm(norm_args(*shape, x, z, w_post, gate, w_next, y, u), shape->dtype, stream), "residual_norm");
+    return MOE_OK;
+}
+
+moe_status moe_residual_norm_grad_workspace(const moe_norm_shape* shape, size_t* bytes) {
+    if (!shape) return fail(MOE_ERR_NULL, "shape is NULL");
+    if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+    if (shape->T < 0 || shape->T >= (1ll << 31) || shape->H <= 0 || shape->H % 8 || shape->H > kMaxNorm)
+        return fail(MOE_ERR_SHAPE, "T = %lld or H = %d out of range", (long long)shape->T, shape->H);
+    *bytes = (size_t)norm_grad_parts(shape->T, shape->H) * 3 * shape->H * sizeof(float);
+    return MOE_OK;
+}
+
+moe_status moe_residual_norm_grad(const moe_norm_shape* shape, const void* dy, const void* du, const void* x,
+                                  const void* z, const float* w_post, const float* gate, const float* w_next, void* dx,
+                                  void* dz, float* dw_post, float* dgate, float* dw_next, void* workspace,
+                                  size_t ws_bytes, hipStream_t stream) {
+    CHECK(check_norm(shape, z, w_post, gate, w_next));
+    if ((dw_post != nullptr) != (w_post != nullptr)) return fail(MOE_ERR_NULL, "w_post and dw_post must be given together");
+    if ((dw_next != nullptr) != (w_next != nullptr)) return fail(MOE_ERR_NULL, "w_next and dw_next must be given together");
+    if ((dgate != nullptr) != (gate != nullptr)) return fail(MOE_ERR_NULL, "gate and dgate must be given together");
+    if (shape->T > 0) {
+        REQ(x, "x");
+        REQ(dx, "dx");
+        if ((dz != nullptr) != (z != nullptr)) return fail(MOE_ERR_NULL, "z and dz must be given together");
+        if (z) {
+            REQ(z, "z");
+            REQ(dz, "dz");
+        } else if (dy) {
+            return fail(MOE_ERR_NULL, "dy needs z");
+        }
+        if (dy) REQ(dy, "dy");
+        if ((du != nullptr) != (w_next != nullptr)) return fail(MOE_ERR_NULL, "w_next and du must be given together");
+        if (du) REQ(du, "du");
+        if (w_post) REQ(w_post, "w_post");
+        if (gate) REQ(gate, "gate");
+        if (w_next) REQ(w_next, "w_next");
+    }
+    if (dw_post) REQ(dw_post, "dw_post");
+    if (dgate) REQ(dgate, "dgate");
+    if (dw_next) REQ(dw_next, "dw_next");
+    const size_t need = (size_t)norm_grad_parts(shape->T, shape->H) * 3 * shape->H * sizeof(float);
+    if (need) {
+        REQ(workspace, "workspace");
+        if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+    }
+    const NormGradArgs g{norm_args(*shape, x, z, w_post, gate, w_next, nullptr, nullptr), dy, du, dx, dz, dw_post, dgate,
+                         dw_next, (float*)workspace};
+    HIPCHK(launch_norm_grad(g, shape->dtype, stream), "residual_norm_grad");
     return MOE_OK;
 }
 
