@@ -4,6 +4,7 @@
  *
  *   grouped products   y = x W_e over ragged row groups, and both gradients
  *   8-bit integers     per-token and per-channel quantisation, and the grouped product
+ *   8-bit floats       quantisation with a scale for each block of 128, and the grouped product
  *   dropout            counter-based, its mask never stored; alone or with the experts'
  *                      gated activation, and the gradient of that
  *   combine's gradient
@@ -98,6 +99,36 @@ moe_status moe_quantize_experts(int32_t dtype, int32_t E, int32_t K, int32_t N, 
 moe_status moe_grouped_mm_int8(const moe_mm_shape* shape, const int8_t* xq, const float* x_scale,
                                const int8_t* wq, const float* w_scale, const int32_t* offsets, void* y,
                                hipStream_t stream);
+
+/* 8-bit floating point (e4m3, no infinities) with a power-of-two scale for each block of 128: of
+ * consecutive elements of a row, or of 128 x 128 elements of an expert matrix; blocks at the
+ * ends may be smaller.  A block's scale is 2^e with the least e >= -127 for which its largest
+ * magnitude is at most 448 2^e, held as the byte e + 127 (E8M0); q is x 2^-e to the nearest
+ * e4m3 number, ties to even.  A block that holds an infinity or a NaN has the byte 255 (NaN)
+ * and q 0.  Rows of scales are padded to MOE_FP8_SCALES(K) = 4 ceil(K / 512) bytes; padding
+ * written here is 127 and never read.
+ *
+ * Rows: x [rows, K] dtype -> q [rows, K], scale [rows, MOE_FP8_SCALES(K)]; K a multiple of 16, at
+ * most 2^20; rows < 2^24. */
+#define MOE_FP8_SCALES(K) (((K) + 511) / 512 * 4)
+moe_status moe_quantize_rows_fp8(int32_t dtype, int64_t rows, int32_t K, const void* x, uint8_t* q, uint8_t* scale,
+                                 hipStream_t stream);
+
+/* Experts, made once: w [E, K, N] dtype -> q [E, N, K] (contraction contiguous), scale
+ * [E, ceil(N / 128), MOE_FP8_SCALES(K)].  E <= 256; K a multiple of 16, N of 8, at most 2^20. */
+moe_status moe_quantize_experts_fp8(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* w, uint8_t* q,
+                                    uint8_t* scale, hipStream_t stream);
+
+/* y[r, n] = sum over blocks B of the contraction of x_scale[r, B] w_scale[e, n div 128, B]
+ * sum_{k in B} xq[r, k] wq[e, n, k], summed in fp32, one rounding to out_dtype (MOE_BF16 or
+ * MOE_F32; shape->dtype is ignored).
+ *   xq [rows, K], x_scale [rows, MOE_FP8_SCALES(K)], wq [E, N, K], w_scale [E, ceil(N / 128),
+ *   MOE_FP8_SCALES(K)], y [rows, N] out.  Limits as moe_grouped_mm; K a multiple of 16. */
+moe_status moe_grouped_mm_fp8(const moe_mm_shape* shape, const uint8_t* xq, const uint8_t* x_scale, const uint8_t* wq,
+                              const uint8_t* w_scale, const int32_t* offsets, void* y, hipStream_t stream);
+
+/* The kernel form that it takes (see moe_grouped_mm_form). */
+const char* moe_grouped_mm_fp8_form(const moe_mm_shape* shape, int32_t cus);
 
 /* Counter-based dropout.  t = round(65536 p), c = 65536 / (65536 - t); element i of the
  * row-major tensor is kept where u(i) >= t and then multiplied by c, else it is 0 (also

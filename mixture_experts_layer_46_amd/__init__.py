@@ -21,13 +21,15 @@ from ._lib import (MOE_BF16, MOE_F32, MOE_FFN_SILU2, MOE_FFN_SWIGLU, MOE_FLAG_BI
                    MOE_FLAG_NO_RENORM, MoeError, Shape, capacity_rows)
 from . import ops
 from .ops import *  # noqa: F401,F403  (ops.__all__)
-from . import norms
+from . import fp8, gated, norms
+from .fp8 import *  # noqa: F401,F403
+from .gated import *  # noqa: F401,F403
 from .norms import *  # noqa: F401,F403
 
 __all__ = ["forward", "route", "route_from_logits", "permute", "grouped_ffn", "combine",
            "router_stats", "make_shape", "Workspace", "Shape", "MoeError", "forward_intermediates",
            "MOE_FLAG_BIAS_SELECT_ONLY", "MOE_FLAG_NO_RENORM", "capacity_rows"]
-__all__ += ops.__all__ + norms.__all__
+__all__ += ops.__all__ + fp8.__all__ + gated.__all__ + norms.__all__
 
 
 def _dtype_code(t: torch.Tensor) -> int:

@@ -20,7 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "grouped_gemm.hip", "combine.hip", "peaks.hip",
            "ops_api.hip", "mm.hip", "mm_stream.hip", "mm_mid.hip", "mm_thin.hip", "mm_pick.hip",
-           "quantize.hip", "dropout.hip", "combine_grad.hip", "norm.hip"]
+           "quantize.hip", "dropout.hip", "combine_grad.hip", "norm.hip",
+           "mm_fp8.hip", "mm_fp8_thin.hip", "quantize_fp8.hip"]
 ARCH = "gfx950"
 
 

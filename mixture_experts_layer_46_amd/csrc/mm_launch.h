@@ -69,6 +69,22 @@ hipError_t launch_combine_grad(const void* dout, const void* y_perm, const int32
                                void* dy_perm, float* dw, long long T, int k, int H, int dtype, long long rows,
                                hipStream_t st);
 
+struct Fp8Args {
+    MmArgs m;                     // as an 8-bit integer product; xs, ws unused
+    const uint8_t *xs, *ws;       // exponents of the blocks' scales, biased by 127
+};
+bool mm_fp8_fits(int out_dtype, const MmArgs& a);
+const char* mm_fp8_form(int out_dtype, const MmArgs& a, int cus);
+hipError_t launch_mm_fp8(int out_dtype, const Fp8Args& a, hipStream_t st);
+hipError_t launch_fp8_large(const Fp8Args& a, hipStream_t st);                // bf16 output
+hipError_t launch_fp8_mid(int tile, const Fp8Args& a, hipStream_t st);
+hipError_t launch_fp8_exact(const Fp8Args& a, hipStream_t st);                // fp32 output, tiles of 64
+hipError_t launch_fp8_thin(int rows, int out_dtype, const Fp8Args& a, hipStream_t st);
+hipError_t launch_quantize_rows_fp8(const void* x, int dtype, long long rows, int K, uint8_t* q, uint8_t* scale,
+                                    hipStream_t st);
+hipError_t launch_quantize_experts_fp8(const void* w, int dtype, int E, int K, int N, uint8_t* q, uint8_t* scale,
+                                       hipStream_t st);
+
 struct NormArgs {                 // moe_residual_norm
     const void *x, *z;            // z NULL: u = norm(x)
     const float *w_post, *gate, *w_next;

@@ -52,7 +52,13 @@ constexpr Cost kRows32[FORMS] = {{}, {}, {1.05, .52, .10}, {3.95, .545, .45}, {2
 constexpr Cost kDw32[FORMS] = {{}, {}, {1.5, .68, .30}, {2.95, .44, .57}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
+// kinds beyond mm_tile.h's: 8-bit floating point with bf16 and with fp32 output
+enum { FP8 = 4, FP8_F32 = 5 };
+constexpr Cost kFp8F32[FORMS] = {{}, {}, {2.2, .21, .118}, {2.25, .25, .48}, {2.5, .69, .05}};
+
 const Cost* costs(int kind, int dtype) {
+    if (kind == FP8) return kInt8;
+    if (kind == FP8_F32) return kFp8F32;
     if (kind == 3) return kInt8;
     if (dtype == MOE_F32) return kind == 2 ? kDw32 : kRows32;
     return kind == 0 ? kY16 : kind == 1 ? kDx16 : kDw16;
@@ -71,7 +77,7 @@ bool fits(int kind, const MmArgs& a, int form) { return blocks_of(kind, a, kShap
 double estimate(int kind, int dtype, const MmArgs& a, int form, int cus) {
     const Shape& s = kShape[form];
     const Cost& c = costs(kind, dtype)[form];
-    const int es = kind == 3 ? 1 : dtype == MOE_F32 ? 4 : 2;
+    const int es = kind >= 3 ? 1 : dtype == MOE_F32 ? 4 : 2;
     const double E = a.E, K = a.K, N = a.N, R = std::max(a.rows, 1);
     const double groups = std::min(E, R), mean = R / groups;             // groups that can have rows
     const double J = kind == 1 ? K : N, C = kind == 1 ? N : kind == 2 ? mean : K;
@@ -93,6 +99,8 @@ double estimate(int kind, int dtype, const MmArgs& a, int form, int cus) {
 }
 
 }  // namespace
+
+bool mm_fp8_fits(int out_dtype, const MmArgs& a) { return mm_fits(out_dtype == MOE_F32 ? FP8_F32 : FP8, MOE_BF16, a); }
 
 bool mm_fits(int kind, int dtype, const MmArgs& a) {
     for (int f = 0; f < FORMS; ++f)
@@ -116,6 +124,10 @@ int pick(int kind, int dtype, const MmArgs& a, int cus) {
 
 }  // namespace
 
+const char* mm_fp8_form(int out_dtype, const MmArgs& a, int cus) {
+    return mm_form(out_dtype == MOE_F32 ? FP8_F32 : FP8, MOE_BF16, a, cus);
+}
+
 const char* mm_form(int kind, int dtype, const MmArgs& a, int cus) {
     switch (pick(kind, dtype, a, cus)) {
         case LARGE: return kind == 2 && mm_streams(a) ? "256x256 stream" : "256x256";
@@ -125,6 +137,18 @@ const char* mm_form(int kind, int dtype, const MmArgs& a, int cus) {
         case THIN16: return "16x64 thin";
     }
     return nullptr;
+}
+
+hipError_t launch_mm_fp8(int out_dtype, const Fp8Args& a, hipStream_t st) {
+    const int kind = out_dtype == MOE_F32 ? FP8_F32 : FP8;
+    switch (pick(kind, MOE_BF16, a.m, device_cu_count())) {
+        case LARGE: return launch_fp8_large(a, st);
+        case MID128: return launch_fp8_mid(128, a, st);
+        case MID64: return kind == FP8 ? launch_fp8_mid(64, a, st) : launch_fp8_exact(a, st);
+        case THIN32: return launch_fp8_thin(32, out_dtype, a, st);
+        case THIN16: return launch_fp8_thin(16, out_dtype, a, st);
+    }
+    return hipErrorInvalidConfiguration;
 }
 
 hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {

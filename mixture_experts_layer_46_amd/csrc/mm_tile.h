@@ -71,9 +71,15 @@ __device__ __forceinline__ int blk_swz(int k) {
     else return 0;
 }
 
+// Swizzle of `rows` operands read 32 indexes at a time (mm_fp8.hip): the 16 lanes that one LDS
+// cycle of a ds_read_b128 serves (see swa4) have four indexes each of every m mod 4, whose m / 4
+// differ modulo 4.
+__device__ __forceinline__ int swa32(int m) { return (m >> 2) & 3; }
+
 // One operand of a tile of T indexes: what a wavefront needs to start the loads of a step.
-// N loads of 1 KB each are this wavefront's (of the T / 16 that fill a step's stage).
-template <int ES, bool COLS, int T, int N>
+// N loads of 1 KB each are this wavefront's (of the T / 16 that fill a step's stage).  R32: laid
+// out for reads of 32 indexes.
+template <int ES, bool COLS, int T, int N, bool R32 = false>
 struct Operand {
     static constexpr int kRowB = T * ES;          // columns: bytes of a stage's row
     static constexpr int kStep = 64 / ES;
@@ -97,8 +103,8 @@ struct Operand {
                 else c ^= 4 * ((k >> 2) & (T == 32 ? 1 : 3));
                 off[i] = c * (16 / ES) < valid ? (uint32_t)k * ld + (uint32_t)c * 16 : kOOB;
             } else {
-                const int r = j * 16 + (lane >> 2), q = (lane & 3) ^ swa4(r);
-                kq = (uint32_t)q * 16;            // the same for every load: swa4 has period 8
+                const int r = j * 16 + (lane >> 2), q = (lane & 3) ^ (R32 ? swa32(r) : swa4(r));
+                kq = (uint32_t)q * 16;            // the same for every load: the swizzles' periods divide 16
                 off[i] = r < valid ? (uint32_t)r * ld + kq : kOOB;
             }
         }
@@ -326,18 +332,18 @@ __device__ __forceinline__ void tile_of_item(const MmArgs& a, const Groups& g, i
     t.nj = min(BN, J - t.j0);
 }
 
-template <typename O, int T, int N>
-__device__ __forceinline__ Operand<O::ES, O::kACols, T, N> operand_a(const MmArgs& a, const Tile2& t) {
-    Operand<O::ES, O::kACols, T, N> o;
+template <typename O, int T, int N, bool R32 = false>
+__device__ __forceinline__ Operand<O::ES, O::kACols, T, N, R32> operand_a(const MmArgs& a, const Tile2& t) {
+    Operand<O::ES, O::kACols, T, N, R32> o;
     o.base = t.abase;
     o.ld = (O::KIND == 2 ? a.K : t.C) * O::ES;
     o.n = O::kACols ? t.C : t.ni;
     o.cbytes = t.C * O::ES;
     return o;
 }
-template <typename O, int T, int N>
-__device__ __forceinline__ Operand<O::ES, O::kBCols, T, N> operand_b(const MmArgs& a, const Tile2& t) {
-    Operand<O::ES, O::kBCols, T, N> o;
+template <typename O, int T, int N, bool R32 = false>
+__device__ __forceinline__ Operand<O::ES, O::kBCols, T, N, R32> operand_b(const MmArgs& a, const Tile2& t) {
+    Operand<O::ES, O::kBCols, T, N, R32> o;
     o.base = t.bbase;
     o.ld = (O::kBCols ? a.N : t.C) * O::ES;
     o.n = O::kBCols ? t.C : t.nj;

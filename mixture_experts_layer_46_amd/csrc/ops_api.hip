@@ -77,6 +77,14 @@ moe_status check_mm(const moe_mm_shape* s, bool int8, bool dw) {
     return MOE_OK;
 }
 
+moe_status check_fp8(const moe_mm_shape* s) {
+    moe_mm_shape t = s ? *s : moe_mm_shape{};
+    t.dtype = t.out_dtype;                    // the operands' type is no choice
+    CHECK(check_mm(s ? &t : nullptr, false, false));
+    if (s->K % 16) return fail(MOE_ERR_UNSUPPORTED, "fp8: K must be a multiple of 16 (K=%d)", s->K);
+    return MOE_OK;
+}
+
 MmArgs mm_args(const moe_mm_shape& s, const void* a, const void* b, void* c, const int32_t* offsets) {
     return MmArgs{a, b, c, offsets, nullptr, nullptr, (int)s.rows, s.E, s.K, s.N, (s.flags & MOE_MM_ZERO_REST) ? 1 : 0};
 }
@@ -238,6 +246,60 @@ moe_status moe_grouped_mm_int8(const moe_mm_shape* shape, const int8_t* xq, cons
     a.xs = x_scale;
     a.ws = w_scale;
     return run_mm(MOE_MM_INT8, *shape, a, stream, "grouped_mm_int8");
+}
+
+moe_status moe_quantize_rows_fp8(int32_t dtype, int64_t rows, int32_t K, const void* x, uint8_t* q, uint8_t* scale,
+                                 hipStream_t stream) {
+    CHECK(check_dtype(dtype));
+    if (rows < 0) return fail(MOE_ERR_SHAPE, "rows = %lld < 0", (long long)rows);
+    if (K <= 0) return fail(MOE_ERR_SHAPE, "K = %d must be positive", K);
+    if (K % 16 || K > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "K = %d must be a multiple of 16, at most 2^20", K);
+    if (rows >= kMaxGrid) return fail(MOE_ERR_UNSUPPORTED, "rows = %lld >= 2^24", (long long)rows);
+    if (rows == 0) return MOE_OK;
+    REQ(x, "x");
+    REQ(q, "q");
+    REQ(scale, "scale");
+    HIPCHK(launch_quantize_rows_fp8(x, dtype, rows, K, q, scale, stream), "quantize_rows_fp8");
+    return MOE_OK;
+}
+
+moe_status moe_quantize_experts_fp8(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* w, uint8_t* q,
+                                    uint8_t* scale, hipStream_t stream) {
+    CHECK(check_dtype(dtype));
+    const moe_mm_shape s{0, E, K, N, dtype, dtype, 0};
+    CHECK(check_fp8(&s));
+    const long long blocks = (long long)E * ((K + 127) / 128) * ((N + 127) / 128);
+    if (blocks >= kMaxGrid)
+        return fail(MOE_ERR_UNSUPPORTED, "quantize_experts_fp8: %lld blocks, at most 2^24 (E=%d K=%d N=%d)", blocks, E, K, N);
+    REQ(w, "w");
+    REQ(q, "q");
+    REQ(scale, "scale");
+    HIPCHK(launch_quantize_experts_fp8(w, dtype, E, K, N, q, scale, stream), "quantize_experts_fp8");
+    return MOE_OK;
+}
+
+moe_status moe_grouped_mm_fp8(const moe_mm_shape* shape, const uint8_t* xq, const uint8_t* x_scale, const uint8_t* wq,
+                              const uint8_t* w_scale, const int32_t* offsets, void* y, hipStream_t stream) {
+    CHECK(check_fp8(shape));
+    if (shape->rows == 0) return MOE_OK;
+    REQ(xq, "xq");
+    REQ(x_scale, "x_scale");
+    REQ(wq, "wq");
+    REQ(w_scale, "w_scale");
+    REQ(offsets, "offsets");
+    REQ(y, "y");
+    const Fp8Args a{mm_args(*shape, xq, wq, y, offsets), x_scale, w_scale};
+    if (!mm_fp8_fits(shape->out_dtype, a.m)) return too_many(*shape, "grouped_mm_fp8");
+    HIPCHK(launch_mm_fp8(shape->out_dtype, a, stream), "grouped_mm_fp8");
+    return MOE_OK;
+}
+
+const char* moe_grouped_mm_fp8_form(const moe_mm_shape* shape, int32_t cus) {
+    if (cus < 0) return fail(MOE_ERR_SHAPE, "cus = %d < 0", cus), nullptr;
+    if (check_fp8(shape) != MOE_OK) return nullptr;
+    const MmArgs a = mm_args(*shape, nullptr, nullptr, nullptr, nullptr);
+    if (!mm_fp8_fits(shape->out_dtype, a)) return too_many(*shape, "grouped_mm_fp8_form"), nullptr;
+    return mm_fp8_form(shape->out_dtype, a, cus ? cus : device_cu_count());
 }
 
 moe_status moe_dropout(int32_t dtype, int64_t n, const moe_dropout_spec* spec, const void* x, void* y,
