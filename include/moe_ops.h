@@ -3,6 +3,7 @@
  * the layer and serving it with 8-bit experts need.
  *
  *   grouped products   y = x W_e over ragged row groups, and both gradients
+ *   gated products     h = SiLU(x W_in) * (x W_up) in one kernel, and the gradient by x
  *   8-bit integers     per-token and per-channel quantisation, and the grouped product
  *   8-bit floats       quantisation with a scale for each block of 128, and the grouped product
  *   dropout            counter-based, its mask never stored; alone or with the experts'
@@ -76,6 +77,25 @@ moe_status moe_grouped_mm_dw(const moe_mm_shape* shape, const void* x, const voi
  * would be refused (the reason in moe_last_error()). */
 typedef enum { MOE_MM_Y = 0, MOE_MM_DX = 1, MOE_MM_DW = 2, MOE_MM_INT8 = 3 } moe_mm_product;
 const char* moe_grouped_mm_form(const moe_mm_shape* shape, int32_t product, int32_t cus);
+
+/* The gated half of the experts' feed-forward, in one kernel:
+ * h[r] = SiLU(x[r] W_in_e) * (x[r] W_up_e) for the rows r of every group e.
+ *   x [rows, K], w_in and w_up [E, K, N], h [rows, N] out.  Sums and activation in fp32, one
+ *   rounding.  a, b [rows, N] out, both or neither (NULL): the two projections, each rounded
+ *   once, as the gradient wants them.  MOE_MM_ZERO_REST covers h, a and b.
+ *   rows == 0 returns MOE_OK and enqueues nothing. */
+moe_status moe_gated_mm(const moe_mm_shape* shape, const void* x, const void* w_in, const void* w_up,
+                        const int32_t* offsets, void* h, void* a, void* b, hipStream_t stream);
+
+/* The gradient of its two projections by x, in one product: dx[r] = da[r] W_in_e^T + db[r] W_up_e^T.
+ *   da, db [rows, N], w_in and w_up [E, K, N], dx [rows, K] out.  (da and db are those of
+ *   moe_gated_act_grad with the kept a and b; the matrices' gradients moe_grouped_mm_dw of x with
+ *   each.) */
+moe_status moe_gated_mm_dx(const moe_mm_shape* shape, const void* da, const void* db, const void* w_in, const void* w_up,
+                           const int32_t* offsets, void* dx, hipStream_t stream);
+
+/* The kernel forms that they take (see moe_grouped_mm_form); dx: that of moe_gated_mm_dx. */
+const char* moe_gated_mm_form(const moe_mm_shape* shape, int32_t dx, int32_t cus);
 
 /* 8-bit rows: scale[r] = max_k |x[r, k]| / 127 in fp32, q[r, k] = x[r, k] / scale[r] to the
  * nearest integer (ties to even), in [-127, 127].  A row of zeros has scale 0 and q 0; a

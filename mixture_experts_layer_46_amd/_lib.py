@@ -31,6 +31,7 @@ EXPORTS = ["moe_workspace_size", "moe_workspace_layout", "moe_capacity_rows", "m
            "moe_gated_act_grad", "moe_combine_grad",
            "moe_quantize_rows_fp8", "moe_quantize_experts_fp8", "moe_grouped_mm_fp8",
            "moe_grouped_mm_fp8_form",
+           "moe_gated_mm", "moe_gated_mm_dx", "moe_gated_mm_form",
            "moe_residual_norm", "moe_residual_norm_grad_workspace", "moe_residual_norm_grad"]
 
 MOE_MM_ZERO_REST = 0x1
@@ -120,6 +121,8 @@ def load(path: str = LIB_PATH):
         "moe_quantize_rows_fp8": [i32, i64, i32, vp, vp, vp, st],
         "moe_quantize_experts_fp8": [i32, i32, i32, i32, vp, vp, vp, st],
         "moe_grouped_mm_fp8": [mp, vp, vp, vp, vp, i32p, vp, st],
+        "moe_gated_mm": [mp, vp, vp, vp, i32p, vp, vp, vp, st],
+        "moe_gated_mm_dx": [mp, vp, vp, vp, vp, i32p, vp, st],
         "moe_residual_norm": [np, vp, vp, f32p, f32p, f32p, vp, vp, st],
         "moe_residual_norm_grad_workspace": [np, ctypes.POINTER(sz)],
         "moe_residual_norm_grad": [np, vp, vp, vp, vp, f32p, f32p, f32p, vp, vp, f32p, f32p, f32p, vp, sz, st],
@@ -140,6 +143,8 @@ def load(path: str = LIB_PATH):
     lib.moe_grouped_mm_form.restype = ctypes.c_char_p
     lib.moe_grouped_mm_fp8_form.argtypes = [mp, i32]
     lib.moe_grouped_mm_fp8_form.restype = ctypes.c_char_p
+    lib.moe_gated_mm_form.argtypes = [mp, i32, i32]
+    lib.moe_gated_mm_form.restype = ctypes.c_char_p
     lib.moe_last_error.argtypes = []
     lib.moe_last_error.restype = ctypes.c_char_p
     _lib = lib
@@ -279,11 +284,13 @@ MM_PRODUCTS = {"y": 0, "dx": 1, "dw": 2, "int8": 3}
 
 
 def grouped_mm_form(product: str, rows: int, E: int, K: int, N: int, dtype: int = MOE_BF16, cus: int = 0) -> str:
-    """The kernel form that a product ("y", "dx", "dw", "int8" or "fp8") of these sizes takes on a GPU of
-    `cus` compute units (0: the current device); see moe_grouped_mm_form."""
+    """The kernel form that a product ("y", "dx", "dw", "int8", "fp8", "gated" or "gated dx") of these
+    sizes takes on a GPU of `cus` compute units (0: the current device); see moe_grouped_mm_form."""
     s = MmShape(rows, E, K, N, dtype, dtype, 0)
     if product == "fp8":
         form = load().moe_grouped_mm_fp8_form(ctypes.byref(s), cus)
+    elif product in ("gated", "gated dx"):
+        form = load().moe_gated_mm_form(ctypes.byref(s), product == "gated dx", cus)
     else:
         form = load().moe_grouped_mm_form(ctypes.byref(s), MM_PRODUCTS[product], cus)
     if form is None:

@@ -24,6 +24,7 @@
 // (some 60 integer instructions a block) under the loads.  8192 x 14336 bf16, h from a packed
 // pair: 121 us, 5.8 TB/s; its kind of gradient over 65536 x 2048: 232 us, 5.8 TB/s; 256 x
 // 4096, plain: 3.0 us, the launch.
+#include "act.h"
 #include "common.h"
 #include "launch.h"
 #include "mm_launch.h"
@@ -81,27 +82,6 @@ __device__ __forceinline__ float get1(const float* p) { return *p; }
 __device__ __forceinline__ float get1(const bf16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put1(bf16_t* p, float v) { *p = f32_to_bf16(v); }
-
-// exp(x) for x <= 0 by the hardware's base-2 exponential, which flushes subnormal results:
-// below 2^-126 it is taken 2^64 higher and scaled back.
-__device__ __forceinline__ float fast_exp(float x) {
-    const float y = x * 1.44269504f;
-    const bool tiny = y < -126.f;
-    const float r = __builtin_amdgcn_exp2f(tiny ? y + 64.f : y);
-    return tiny ? r * 0x1p-64f : r;
-}
-
-// s = 1 / (1 + exp(-a)) and 1 - s, both without cancellation or overflow.  bf16 results
-// take the hardware's exponential and reciprocal.  The fp32 product a log2(e) puts up to
-// 1.25 |a| 2^-24 on the exponential's relative error (2^-17 where it reaches the least normal
-// value), beside a few 2^-23 of the two instructions: far below the results' own 2^-9.
-template <bool FAST>
-__device__ __forceinline__ void sigmoid(float a, float& s, float& ns) {
-    const float t = FAST ? fast_exp(-fabsf(a)) : expf(-fabsf(a));
-    const float big = FAST ? __builtin_amdgcn_rcpf(1.f + t) : 1.f / (1.f + t), small = t * big;
-    s = a >= 0.f ? big : small;
-    ns = a >= 0.f ? small : big;
-}
 
 // The step of this launch: the caller's, plus a device word where one is given (a captured
 // launch then draws a new mask at each replay).

@@ -32,7 +32,7 @@ template <typename O, int GROUP>
 __device__ __attribute__((always_inline)) inline void steps(lds_char* lds, int KT, int nblk, int ablk, int wn, int wave,
                                                             const OpA<O>& oa, const OpB<O>& ob,
                                                             const Reader<O::ES, O::kACols, kT>& ra,
-                                                            const Reader<O::ES, O::kBCols, kT>& rb,
+                                                            const ReaderB<O, kT, 4>& rb,
                                                             typename O::Acc (&acc)[8][4]) {
     u32x4_t af[8], bf[4];
     if constexpr (GROUP == 1) lds_barrier();
@@ -69,9 +69,10 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
     const int l16 = lane & 15, lq = lane >> 4;
 
     const int w = item_of_block(blockIdx.x, gridDim.x);
-    if (w >= count_items<O, kT, kT, OUT>(a, groups)) return;
+    constexpr int kCols = tile_cols<O>(kT);
+    if (w >= count_items<O, kT, kCols, OUT>(a, groups)) return;
     Tile2 t;
-    tile_of_item<O, kT, kT>(a, groups, w, t);
+    tile_of_item<O, kT, kCols>(a, groups, w, t);
     auto oa = operand_a<O, kT, kLoads>(a, t);
     auto ob = operand_b<O, kT, kLoads>(a, t);
     oa.plan(wave * kLoads, lane, t.ni);
@@ -86,10 +87,10 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = typename O::Acc{0, 0, 0, 0};
 
-    const int KT = (t.C + O::kStep - 1) / O::kStep;
+    const int KT = t.template steps<O>();
     if (KT > 0) {
         const Reader<O::ES, O::kACols, kT> ra(lane);
-        const Reader<O::ES, O::kBCols, kT> rb(lane);
+        const ReaderB<O, kT, 4> rb(lane);
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
             oa.load(lds + s * kStage, wave * kLoads, s);
@@ -108,6 +109,35 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
     const int J = O::KIND == 1 ? a.K : a.N;
     typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
     typedef __attribute__((address_space(3))) u32x2_t lds_u2;
+    if constexpr (O::kGated) {
+        // h, then the projections where they are kept; each through LDS as whole rows
+        for (int which = 0; which < (a.ca ? 3 : 1); ++which) {
+            if (which) __syncthreads();                       // the tensor before has been read
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i >= nblk) break;
+                const int r = row0 + 16 * i + l16;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f32x4_t x = which == 1 ? acc[i][j] : acc[i][2 + j];
+                    if (which == 0)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) x[v] = gated<O::ELEM>(acc[i][j][v], acc[i][2 + j][v]);
+                    *(lds_u2*)(lds + (r * kCS + wn * 32 + 16 * j + 4 * lq) * 2) =
+                        u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+                }
+            }
+            __syncthreads();
+            bf16_t* out = (bf16_t*)(which == 0 ? a.c : which == 1 ? a.ca : a.cb);
+            for (int c = tid; c < t.ni * 16; c += 512) {
+                const int r = c >> 4, cc = (c & 15) * 8;
+                if (cc < t.nj)
+                    __builtin_nontemporal_store(*(const __attribute__((address_space(3))) u32x4_t*)(lds + (r * kCS + cc) * 2),
+                                                reinterpret_cast<u32x4_t*>(out + (t.crow + r) * J + t.j0 + cc));
+            }
+        }
+        return;
+    }
     f32x4_t wsc[4];
     if constexpr (O::ELEM == Elem::i8)
 #pragma unroll
@@ -153,7 +183,7 @@ template <typename O, typename OUT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
     hipError_t e = allow_lds<k_mm<O, OUT>>(kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mm<O, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, kT, kT)), dim3(512), kLds, st, a);
+    hipLaunchKernelGGL((k_mm<O, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, kT, tile_cols<O>(kT))), dim3(512), kLds, st, a);
     return hipGetLastError();
 }
 
@@ -177,6 +207,8 @@ hipError_t launch_mm_large(int kind, int out_dtype, const MmArgs& a, hipStream_t
         case 2:
             if (mm_streams(a)) return launch_mm_stream(out_dtype, a, st);
             return f ? go<Op<2, Elem::bf16>, float>(a, st) : go<Op<2, Elem::bf16>, bf16_t>(a, st);
+        case MM_GATED: return go<Op<0, Elem::bf16, Var::gated>, bf16_t>(a, st);
+        case MM_DX_TWO: return go<Op<1, Elem::bf16, Var::two>, bf16_t>(a, st);
         default: return f ? go<Op<3, Elem::i8>, float>(a, st) : go<Op<3, Elem::i8>, bf16_t>(a, st);
     }
 }

@@ -15,9 +15,9 @@ constexpr int kLoads = 2;                     // loads of one operand per wavefr
 constexpr int kVmcnt = 4 * kLoads;            // loads of the two steps after the awaited one
 
 template <typename O>
-using OpA = Operand<O::ES, O::kACols, kT, kLoads>;
+using OpA = OperandA<O, kT, kLoads>;
 template <typename O>
-using OpB = Operand<O::ES, O::kBCols, kT, kLoads>;
+using OpB = OperandB<O, kT, kLoads>;
 
 }  // namespace large
 }  // namespace moe

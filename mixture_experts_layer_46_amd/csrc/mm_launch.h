@@ -16,7 +16,13 @@ struct MmArgs {
     const float *xs, *ws;         // int8: row and column scales
     int rows, E, K, N;
     int zero_rest;
+    const void *a2 = nullptr, *b2 = nullptr;      // MM_GATED: w_up; MM_DX_TWO: db and w_up
+    void *ca = nullptr, *cb = nullptr;            // MM_GATED: where the projections are kept, or NULL
 };
+
+// kinds beyond mm_tile.h's: h = SiLU(x W_in) * (x W_up), dx = da W_in^T + db W_up^T, and 8-bit
+// floating point with bf16 and with fp32 output
+enum { MM_FP8 = 4, MM_FP8_F32 = 5, MM_GATED = 6, MM_DX_TWO = 7 };
 
 // kind: 0 y = x W, 1 dx = dy W^T, 2 dW = x^T dy, 3 int8; in the form that suits the sizes
 hipError_t launch_mm(int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st);

@@ -29,7 +29,8 @@ struct Mid {
     static constexpr int FM = BM / 32, FN = BN / 32;          // 16-index blocks of a wavefront
     static constexpr int NA = BM / 64, NB = BN / 64;          // loads per wavefront and step
     static constexpr int kSub = (BM + BN) * 64, kStage = U * kSub;      // bytes of one step; of a stage
-    static constexpr int kCS = BN + 8;                        // bf16 per row of the staging tile
+    static constexpr int kCols = tile_cols<O>(BN);            // columns of C
+    static constexpr int kCS = kCols + 8;                     // bf16 per row of the staging tile
     static constexpr size_t kOut = (size_t)BM * kCS * 2;
     static constexpr size_t kLds = kOut > (size_t)S * kStage ? kOut : (size_t)S * kStage;
 };
@@ -72,14 +73,14 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
 
     Tile2 t;
     const int w = item_of_block(blockIdx.x, gridDim.x);
-    if (w >= count_items<O, BM, BN, OUT>(a, groups)) return;
-    tile_of_item<O, BM, BN>(a, groups, w, t);
+    if (w >= count_items<O, BM, L::kCols, OUT>(a, groups)) return;
+    tile_of_item<O, BM, L::kCols>(a, groups, w, t);
     auto oa = operand_a<O, BM, L::NA>(a, t);
     auto ob = operand_b<O, BN, L::NB>(a, t);
     oa.plan(wave * L::NA, lane, t.ni);
     ob.plan(wave * L::NB, lane, t.nj);
     const Reader<O::ES, O::kACols, BM> ra(lane);
-    const Reader<O::ES, O::kBCols, BN> rb(lane);
+    const ReaderB<O, BN, L::FN> rb(lane);
 
     // rows split evenly over the two wavefront rows, in 16-row blocks
     const int half = min(BM / 2, (t.ni + 31) / 32 * 16), row0 = uni(wm * half);
@@ -90,7 +91,7 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
 #pragma unroll
         for (int j = 0; j < L::FN; ++j) acc[i][j] = ACC{0, 0, 0, 0};
 
-    const int KT = (t.C + O::kStep - 1) / O::kStep;
+    const int KT = t.template steps<O>();
     if constexpr (O::ELEM == Elem::f32) {
         if (KT > 0) {
             static_assert(U == 1 && S % 2 == 0, "two sets of operands take turns");
@@ -144,6 +145,46 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
     }
 
     const int J = O::KIND == 1 ? a.K : a.N;
+    typedef __attribute__((address_space(3))) bf16_t lds_bf16;
+    lds_bf16* sC = reinterpret_cast<lds_bf16*>(lds);
+    if constexpr (O::kGated) {
+        // h, then the projections where they are kept; bf16 through LDS as whole rows
+        for (int which = 0; which < (a.ca ? 3 : 1); ++which) {
+            if (which) __syncthreads();                       // the tensor before has been read
+            OUT* out = (OUT*)(which == 0 ? a.c : which == 1 ? a.ca : a.cb);
+#pragma unroll
+            for (int i = 0; i < L::FM; ++i) {
+                if (i >= nblk) break;
+                const int r = row0 + 16 * i + 4 * lq;
+#pragma unroll
+                for (int j = 0; j < L::FN / 2; ++j) {
+                    const int col = wn * (L::kCols / 2) + 16 * j + l16;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float p = acc[i][j][v], q = acc[i][L::FN / 2 + j][v];
+                        const float val = which == 0 ? gated<O::ELEM>(p, q) : which == 1 ? p : q;
+                        if constexpr (sizeof(OUT) == 2) {
+                            sC[(r + v) * L::kCS + col] = f32_to_bf16(val);
+                        } else {
+                            if (r + v < t.ni && col < t.nj) out[(t.crow + r + v) * J + t.j0 + col] = val;
+                        }
+                    }
+                }
+            }
+            if constexpr (sizeof(OUT) == 2) {
+                __syncthreads();
+                constexpr int CPR = L::kCols / 8;
+                for (int c = tid; c < t.ni * CPR; c += 256) {
+                    const int r = c / CPR, cc = (c % CPR) * 8;
+                    if (cc < t.nj)
+                        __builtin_nontemporal_store(
+                            *reinterpret_cast<const __attribute__((address_space(3))) u32x4_t*>(sC + r * L::kCS + cc),
+                            reinterpret_cast<u32x4_t*>(out + (t.crow + r) * J + t.j0 + cc));
+                }
+            }
+        }
+        return;
+    }
     float wsc[L::FN];
     if constexpr (O::ELEM == Elem::i8)
 #pragma unroll
@@ -151,8 +192,6 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
             const int col = wn * (BN / 2) + 16 * j + l16;
             wsc[j] = col < t.nj ? a.ws[(long long)t.e * a.N + t.j0 + col] : 0.f;
         }
-    typedef __attribute__((address_space(3))) bf16_t lds_bf16;
-    lds_bf16* sC = reinterpret_cast<lds_bf16*>(lds);
 #pragma unroll
     for (int i = 0; i < L::FM; ++i) {
         if (i >= nblk) break;
@@ -195,7 +234,7 @@ hipError_t go(const MmArgs& a, hipStream_t st) {
     constexpr size_t lds = Mid<O, BM, BN, S, U>::kLds;
     hipError_t e = allow_lds<k_mm_mid<O, BM, BN, S, U, OUT>>(lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mm_mid<O, BM, BN, S, U, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, BM, BN)), dim3(256), lds, st, a);
+    hipLaunchKernelGGL((k_mm_mid<O, BM, BN, S, U, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, BM, tile_cols<O>(BN))), dim3(256), lds, st, a);
     return hipGetLastError();
 }
 
@@ -204,6 +243,7 @@ hipError_t go_16(int kind, bool f, const MmArgs& a, hipStream_t st) {
     switch (kind) {
         case 0: return go<Op<0, Elem::bf16>, BM, BN, S, U, bf16_t>(a, st);
         case 1: return go<Op<1, Elem::bf16>, BM, BN, S, U, bf16_t>(a, st);
+        case MM_DX_TWO: return go<Op<1, Elem::bf16, Var::two>, BM, BN, S, U, bf16_t>(a, st);
         case 2: return f ? go<Op<2, Elem::bf16>, BM, BN, S, U, float>(a, st) : go<Op<2, Elem::bf16>, BM, BN, S, U, bf16_t>(a, st);
         default: return f ? go<Op<3, Elem::i8>, BM, BN, S, U, float>(a, st) : go<Op<3, Elem::i8>, BM, BN, S, U, bf16_t>(a, st);
     }
@@ -213,6 +253,8 @@ hipError_t go_32(int kind, const MmArgs& a, hipStream_t st) {
     switch (kind) {
         case 0: return go<Op<0, Elem::f32>, 64, 64, 4, 1, float>(a, st);
         case 1: return go<Op<1, Elem::f32>, 64, 64, 4, 1, float>(a, st);
+        case MM_GATED: return go<Op<0, Elem::f32, Var::gated>, 64, 128, 4, 1, float>(a, st);
+        case MM_DX_TWO: return go<Op<1, Elem::f32, Var::two>, 64, 64, 4, 1, float>(a, st);
         default: return go<Op<2, Elem::f32>, 64, 64, 4, 1, float>(a, st);
     }
 }
@@ -225,6 +267,9 @@ hipError_t go_32(int kind, const MmArgs& a, hipStream_t st) {
 hipError_t launch_mm_mid(int tile, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
     if (kind != 3 && dtype == MOE_F32) return go_32(kind, a, st);
     const bool f = out_dtype == MOE_F32;
+    if (kind == MM_GATED)                                     // 64 columns of h either way
+        return tile == 64 ? go<Op<0, Elem::bf16, Var::gated>, 64, 128, 4, 1, bf16_t>(a, st)
+                          : go<Op<0, Elem::bf16, Var::gated>, 128, 128, 4, 1, bf16_t>(a, st);
     return tile == 64 ? go_16<64, 64, 3, 2>(kind, f, a, st) : go_16<128, 128, 4, 1>(kind, f, a, st);
 }
 

@@ -52,35 +52,45 @@ constexpr Cost kRows32[FORMS] = {{}, {}, {1.05, .52, .10}, {3.95, .545, .45}, {2
 constexpr Cost kDw32[FORMS] = {{}, {}, {1.5, .68, .30}, {2.95, .44, .57}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
-// kinds beyond mm_tile.h's: 8-bit floating point with bf16 and with fp32 output
-enum { FP8 = 4, FP8_F32 = 5 };
+// gated tiles: columns of h
+constexpr Shape kGatedShape[FORMS] = {{256, 128, 1, 1, 512, 5.0e6}, {128, 64, 2, 1, 256, 5.3e6}, {64, 64, 3, 1, 256, 5.4e6},
+                                      {32, 64, 1, 4, 256, 5.6e6}, {16, 64, 1, 4, 256, 4.9e6}};
+const Shape& shape_of(int kind, int form) { return kind == MM_GATED ? kGatedShape[form] : kShape[form]; }
+
+constexpr Cost kGated16[FORMS] = {{1.85, .38, .54}, {1.9, .38, .25}, {2.15, .24, .19}, {2.15, .40, .59}, {3.55, .60, .3}};
+constexpr Cost kGated32[FORMS] = {{}, {}, {1.05, .52, .20}, {3.95, .70, .9}, {2.15, .9, .45}};
 constexpr Cost kFp8F32[FORMS] = {{}, {}, {2.2, .21, .118}, {2.25, .25, .48}, {2.5, .69, .05}};
 
 const Cost* costs(int kind, int dtype) {
-    if (kind == FP8) return kInt8;
-    if (kind == FP8_F32) return kFp8F32;
+    if (kind == MM_FP8) return kInt8;
+    if (kind == MM_FP8_F32) return kFp8F32;
+    if (kind == MM_GATED) return dtype == MOE_F32 ? kGated32 : kGated16;
+    if (kind == MM_DX_TWO) return dtype == MOE_F32 ? kRows32 : kDx16;
     if (kind == 3) return kInt8;
     if (dtype == MOE_F32) return kind == 2 ? kDw32 : kRows32;
     return kind == 0 ? kY16 : kind == 1 ? kDx16 : kDw16;
 }
 
 long long blocks_of(int kind, const MmArgs& a, const Shape& s) {
-    const long long J = kind == 1 ? a.K : a.N;
+    const long long J = kind == 1 || kind == MM_DX_TWO ? a.K : a.N;
     const long long ni = kind == 2 ? (long long)a.E * ((a.K + s.bm - 1) / s.bm)
                                    : ((long long)a.rows + s.bm - 1) / s.bm + std::min(a.rows, a.E);
     return ni * ((J + s.bn - 1) / s.bn);
 }
 
 // A launch holds at most 2^32 threads in a dimension.
-bool fits(int kind, const MmArgs& a, int form) { return blocks_of(kind, a, kShape[form]) * kShape[form].threads < (1ll << 32); }
+bool fits(int kind, const MmArgs& a, int form) {
+    return blocks_of(kind, a, shape_of(kind, form)) * shape_of(kind, form).threads < (1ll << 32);
+}
 
 double estimate(int kind, int dtype, const MmArgs& a, int form, int cus) {
-    const Shape& s = kShape[form];
+    const Shape& s = shape_of(kind, form);
     const Cost& c = costs(kind, dtype)[form];
-    const int es = kind >= 3 ? 1 : dtype == MOE_F32 ? 4 : 2;
+    const bool dx = kind == 1 || kind == MM_DX_TWO;
+    const int es = kind == 3 || kind == MM_FP8 || kind == MM_FP8_F32 ? 1 : dtype == MOE_F32 ? 4 : 2;
     const double E = a.E, K = a.K, N = a.N, R = std::max(a.rows, 1);
     const double groups = std::min(E, R), mean = R / groups;             // groups that can have rows
-    const double J = kind == 1 ? K : N, C = kind == 1 ? N : kind == 2 ? mean : K;
+    const double J = dx ? K : N, C = kind == MM_DX_TWO ? 2 * N : dx ? N : kind == 2 ? mean : K;
     double tiles;                                                        // expected row tiles
     if (kind == 2) tiles = E * std::ceil(K / s.bm);
     else if (a.E == 1) tiles = std::ceil(R / s.bm);
@@ -94,13 +104,14 @@ double estimate(int kind, int dtype, const MmArgs& a, int form, int cus) {
         const double r = per_cu / s.per_cu;
         t = (r < 2 ? 2 : r + .4) * (c.fixed + steps * std::max(c.step, s.per_cu * c.busy));
     }
-    const double bytes = (R * K + R * N) * es + (kind == 2 ? E : groups) * K * N * es, m = bytes / (kind == 2 ? kWriteRate : s.rate);
+    const double mats = kind == 2 ? E : kind == MM_GATED || kind == MM_DX_TWO ? 2 * groups : groups;
+    const double bytes = (R * K + R * N * (kind == MM_DX_TWO ? 2 : 1)) * es + mats * K * N * es, m = bytes / (kind == 2 ? kWriteRate : s.rate);
     return std::max(t, m) + .2 * std::min(t, m);
 }
 
 }  // namespace
 
-bool mm_fp8_fits(int out_dtype, const MmArgs& a) { return mm_fits(out_dtype == MOE_F32 ? FP8_F32 : FP8, MOE_BF16, a); }
+bool mm_fp8_fits(int out_dtype, const MmArgs& a) { return mm_fits(out_dtype == MOE_F32 ? MM_FP8_F32 : MM_FP8, MOE_BF16, a); }
 
 bool mm_fits(int kind, int dtype, const MmArgs& a) {
     for (int f = 0; f < FORMS; ++f)
@@ -125,7 +136,7 @@ int pick(int kind, int dtype, const MmArgs& a, int cus) {
 }  // namespace
 
 const char* mm_fp8_form(int out_dtype, const MmArgs& a, int cus) {
-    return mm_form(out_dtype == MOE_F32 ? FP8_F32 : FP8, MOE_BF16, a, cus);
+    return mm_form(out_dtype == MOE_F32 ? MM_FP8_F32 : MM_FP8, MOE_BF16, a, cus);
 }
 
 const char* mm_form(int kind, int dtype, const MmArgs& a, int cus) {
@@ -140,11 +151,11 @@ const char* mm_form(int kind, int dtype, const MmArgs& a, int cus) {
 }
 
 hipError_t launch_mm_fp8(int out_dtype, const Fp8Args& a, hipStream_t st) {
-    const int kind = out_dtype == MOE_F32 ? FP8_F32 : FP8;
+    const int kind = out_dtype == MOE_F32 ? MM_FP8_F32 : MM_FP8;
     switch (pick(kind, MOE_BF16, a.m, device_cu_count())) {
         case LARGE: return launch_fp8_large(a, st);
         case MID128: return launch_fp8_mid(128, a, st);
-        case MID64: return kind == FP8 ? launch_fp8_mid(64, a, st) : launch_fp8_exact(a, st);
+        case MID64: return kind == MM_FP8 ? launch_fp8_mid(64, a, st) : launch_fp8_exact(a, st);
         case THIN32: return launch_fp8_thin(32, out_dtype, a, st);
         case THIN16: return launch_fp8_thin(16, out_dtype, a, st);
     }

@@ -21,11 +21,12 @@ namespace {
 
 constexpr int kBN = 64;
 
-template <int RB, int W, int S>
+template <typename O, int RB, int W, int S>
 struct Thin {
-    static constexpr int BM = 16 * RB, NA = RB, NB = kBN / 16;
-    static constexpr int kA = BM * 64, kStage = (BM + kBN) * 64;
-    static constexpr size_t kRing = (size_t)W * S * kStage, kSums = (size_t)W * BM * kBN * 4;
+    static constexpr int BT = O::kGated ? 2 * kBN : kBN;      // columns of a stage
+    static constexpr int BM = 16 * RB, NA = RB, NB = BT / 16, FN = BT / 16;
+    static constexpr int kA = BM * 64, kStage = (BM + BT) * 64;
+    static constexpr size_t kRing = (size_t)W * S * kStage, kSums = (size_t)W * BM * BT * 4;
     static constexpr size_t kLds = kRing > kSums ? kRing : kSums;
 };
 
@@ -37,24 +38,35 @@ template <typename O, int RB, int W, int S, typename OA, typename OB, typename R
 __device__ __attribute__((always_inline)) inline void load_and_read(const lds_char* __restrict__ rd,
                                                                     lds_char* __restrict__ wr, int kt, const OA& oa,
                                                                     const OB& ob, const RA& ra, const RBt& rb,
-                                                                    u32x4_t (&af)[RB], u32x4_t (&bf)[4]) {
-    using L = Thin<RB, W, S>;
+                                                                    u32x4_t (&af)[RB], u32x4_t (&bf)[Thin<O, RB, W, S>::FN]) {
+    using L = Thin<O, RB, W, S>;
     oa.load(wr, 0, kt);
     ob.load(wr + L::kA, 0, kt);
     wait_vmcnt<(S - 1) * (L::NA + L::NB)>();
 #pragma unroll
     for (int i = 0; i < RB; ++i) af[i] = ra(rd, i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) bf[j] = rb(rd + L::kA, j);
+    for (int j = 0; j < L::FN; ++j) bf[j] = rb(rd + L::kA, j);
     __builtin_amdgcn_sched_barrier(0);
     wait_lds();                                               // read: the next step may refill this stage
     __builtin_amdgcn_sched_barrier(0);
 }
 
+template <typename OUT>
+__device__ __forceinline__ void put8(OUT* p, const float (&o)[8]) {
+    if constexpr (sizeof(OUT) == 2) {
+        *reinterpret_cast<uint4*>(p) = uint4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                             pack_bf16x2(o[6], o[7])};
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
+    }
+}
+
 template <typename O, int RB, int W, int S, typename OUT>
 __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__          // the host pass needs the signature only
-    using L = Thin<RB, W, S>;
+    using L = Thin<O, RB, W, S>;
     using ACC = typename O::Acc;
     extern __shared__ uint4 smem[];
     __shared__ Groups groups;
@@ -66,18 +78,18 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
     if (w >= count_items<O, L::BM, kBN, OUT>(a, groups)) return;
     tile_of_item<O, L::BM, kBN>(a, groups, w, t);
     auto oa = operand_a<O, L::BM, L::NA>(a, t);
-    auto ob = operand_b<O, kBN, L::NB>(a, t);
+    auto ob = operand_b<O, L::BT, L::NB>(a, t);
     oa.plan(0, lane, t.ni);
     ob.plan(0, lane, t.nj);
     const Reader<O::ES, O::kACols, L::BM> ra(lane);
-    const Reader<O::ES, O::kBCols, kBN> rb(lane);
-    ACC acc[RB][4];
+    const ReaderB<O, L::BT, L::FN> rb(lane);
+    ACC acc[RB][L::FN];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = ACC{0, 0, 0, 0};
+        for (int j = 0; j < L::FN; ++j) acc[i][j] = ACC{0, 0, 0, 0};
 
-    const int KT = (t.C + O::kStep - 1) / O::kStep;
+    const int KT = t.template steps<O>();
     lds_char* ring = lds + wave * (S * L::kStage);
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) {
@@ -86,7 +98,7 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
     }
     int st = 0, nx = S - 1;                                   // stage of this step, and of the loads it starts
     for (int kt = wave; kt < KT; kt += W) {
-        u32x4_t af[RB], bf[4];
+        u32x4_t af[RB], bf[L::FN];
         load_and_read<O, RB, W, S>(ring + st * L::kStage, ring + nx * L::kStage, kt + (S - 1) * W, oa, ob, ra, rb, af, bf);
         mma_step<O::ELEM>(af, bf, acc, RB);
         st = st + 1 == S ? 0 : st + 1;
@@ -101,14 +113,14 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < L::FN; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const auto x = acc[i][j][v];
                 int bits;
                 if constexpr (O::ELEM == Elem::i8) bits = x;
                 else bits = __float_as_int(x);
-                sums[(wave * L::BM + 16 * i + 4 * lq + v) * kBN + 16 * j + l16] = bits;
+                sums[(wave * L::BM + 16 * i + 4 * lq + v) * L::BT + 16 * j + l16] = bits;
             }
     __syncthreads();
     const int J = O::KIND == 1 ? a.K : a.N;
@@ -117,7 +129,21 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
         const int r = c / (kBN / 8), cc = (c % (kBN / 8)) * 8;
         if (cc >= t.nj) continue;
         float o[8];
-        if constexpr (O::ELEM == Elem::i8) {
+        if constexpr (O::kGated) {
+            float p[8] = {}, u[8] = {};
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    p[q] += __int_as_float(sums[(w * L::BM + r) * L::BT + cc + q]);
+                    u[q] += __int_as_float(sums[(w * L::BM + r) * L::BT + kBN + cc + q]);
+                }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = gated<O::ELEM>(p[q], u[q]);
+            if (a.ca) {
+                put8((OUT*)a.ca + (t.crow + r) * J + t.j0 + cc, p);
+                put8((OUT*)a.cb + (t.crow + r) * J + t.j0 + cc, u);
+            }
+        } else if constexpr (O::ELEM == Elem::i8) {
             int s[8] = {};
             for (int w = 0; w < W; ++w)
 #pragma unroll
@@ -133,21 +159,14 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) o[q] += __int_as_float(sums[(w * L::BM + r) * kBN + cc + q]);
         }
-        OUT* p = (OUT*)a.c + (t.crow + r) * J + t.j0 + cc;
-        if constexpr (sizeof(OUT) == 2) {
-            *reinterpret_cast<uint4*>(p) = uint4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                                 pack_bf16x2(o[6], o[7])};
-        } else {
-            reinterpret_cast<float4*>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
-        }
+        put8((OUT*)a.c + (t.crow + r) * J + t.j0 + cc, o);
     }
 #endif
 }
 
 template <typename O, int RB, int W, int S, typename OUT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
-    constexpr size_t lds = Thin<RB, W, S>::kLds;
+    constexpr size_t lds = Thin<O, RB, W, S>::kLds;
     hipError_t e = allow_lds<k_mm_thin<O, RB, W, S, OUT>>(lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_mm_thin<O, RB, W, S, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, 16 * RB, kBN)), dim3(W * 64), lds, st, a);
@@ -165,6 +184,9 @@ hipError_t go_kind(int kind, int dtype, int out_dtype, const MmArgs& a, hipStrea
             return out_dtype == MOE_F32 ? go<Op<2, Elem::bf16>, RB, W, S, float>(a, st)
                                         : go<Op<2, Elem::bf16>, RB, W, S, bf16_t>(a, st);
         }
+    if (kind == MM_DX_TWO)
+        return dtype == MOE_F32 ? go<Op<1, Elem::f32, Var::two>, RB, W, S, float>(a, st)
+                                : go<Op<1, Elem::bf16, Var::two>, RB, W, S, bf16_t>(a, st);
     if (dtype == MOE_F32)
         return kind == 0 ? go<Op<0, Elem::f32>, RB, W, S, float>(a, st) : go<Op<1, Elem::f32>, RB, W, S, float>(a, st);
     return kind == 0 ? go<Op<0, Elem::bf16>, RB, W, S, bf16_t>(a, st) : go<Op<1, Elem::bf16>, RB, W, S, bf16_t>(a, st);
@@ -176,6 +198,13 @@ hipError_t go_kind(int kind, int dtype, int out_dtype, const MmArgs& a, hipStrea
 // CU.  Three stages each.  Measured against 16 rows with four wavefronts and 64 rows with
 // four or eight, which no rule on the sizes made pay.
 hipError_t launch_mm_thin(int rows, int kind, int dtype, int out_dtype, const MmArgs& a, hipStream_t st) {
+    if (kind == MM_GATED) {                                   // stages are nearly twice as large: four wavefronts
+        if (dtype == MOE_F32)
+            return rows == 16 ? go<Op<0, Elem::f32, Var::gated>, 1, 4, 4, float>(a, st)
+                              : go<Op<0, Elem::f32, Var::gated>, 2, 4, 3, float>(a, st);
+        return rows == 16 ? go<Op<0, Elem::bf16, Var::gated>, 1, 4, 4, bf16_t>(a, st)
+                          : go<Op<0, Elem::bf16, Var::gated>, 2, 4, 3, bf16_t>(a, st);
+    }
     return rows == 16 ? go_kind<1, 8, 3>(kind, dtype, out_dtype, a, st) : go_kind<2, 4, 3>(kind, dtype, out_dtype, a, st);
 }
 

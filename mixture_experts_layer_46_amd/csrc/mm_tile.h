@@ -6,6 +6,14 @@
 //   kind 2  dw[e, k, n] = sum_r x[r, k] dy[r, n]       (r over the rows of group e)
 //   kind 3  y[r, n]     = (sum_k xq[r, k] wq[e, n, k]) xs[r] ws[e, n]     (int8)
 //
+// and two variants for the experts' gated projections:
+//
+//   kind 0, gated    h[r, f]  = SiLU(sum_k x[r, k] w_in[e, k, f]) sum_k x[r, k] w_up[e, k, f]: a tile's B
+//                    operand is half as many columns of each matrix, side by side in LDS, and
+//                    a wavefront holds the same columns of both products
+//   kind 1, two      dx[r, k] = sum_f da[r, f] w_in[e, k, f] + db[r, f] w_up[e, k, f]: one contraction, whose
+//                    steps run through the first pair of operands, then through the second
+//
 // All are C[i, j] = sum_c A[i, c] B[c, j] on tiles of C, in steps of the contraction that
 // take 64 bytes of each index (32 bf16, 64 int8, 16 fp32).  An operand lies in memory in
 // one of two layouts:
@@ -29,6 +37,7 @@
 
 #include <type_traits>
 
+#include "act.h"
 #include "common.h"
 #include "launch.h"
 #include "mm_common.h"
@@ -42,8 +51,12 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 enum class Elem { bf16, i8, f32 };
 
-template <int KIND_, Elem E_>
+enum class Var { plain, gated, two };
+
+template <int KIND_, Elem E_, Var V_ = Var::plain>
 struct Op {
+    static constexpr bool kGated = V_ == Var::gated, kTwo = V_ == Var::two;
+    static_assert(!(kGated && KIND_ != 0) && !(kTwo && KIND_ != 1), "the variants of kinds 0 and 1");
     static constexpr int KIND = KIND_;
     static constexpr Elem ELEM = E_;
     static constexpr bool kACols = KIND == 2, kBCols = KIND == 0 || KIND == 2;
@@ -133,6 +146,35 @@ struct Operand {
     }
 };
 
+// The B operand of a gated tile: T / 2 columns of one matrix, then of the other; N loads in all.
+template <int ES, int T, int N>
+struct GatedOperand {
+    Operand<ES, true, T / 2, N / 2> in, up;
+    __device__ __forceinline__ void plan(int first, int lane, int valid) {
+        in.plan(first / 2, lane, valid);
+        up.plan(first / 2, lane, valid);
+    }
+    __device__ __forceinline__ void load(lds_char* stage, int first, int kt) const {
+        in.load(stage, first / 2, kt);
+        up.load(stage + T / 2 * 64, first / 2, kt);
+    }
+};
+
+// An operand whose steps run through one tensor and then, from step `half` on, through another
+// of the same layout.
+template <int ES, int T, int N>
+struct TwoOperand {
+    Operand<ES, false, T, N> o;
+    uint64_t base2;
+    int half;
+    __device__ __forceinline__ void plan(int first, int lane, int valid) { o.plan(first, lane, valid); }
+    __device__ __forceinline__ void load(lds_char* stage, int first, int kt) const {
+        Operand<ES, false, T, N> p = o;
+        if (kt >= half) p.base = base2;
+        p.load(stage, first, kt >= half ? kt - half : kt);
+    }
+};
+
 // 16-index block `blk` of an operand's stage as a matrix operand.
 template <int ES, bool COLS, int T>
 struct Reader {
@@ -179,6 +221,26 @@ struct Reader {
         }
     }
 };
+
+// Of a gated tile of T columns in all, FN blocks a wavefront: its block j < FN / 2 is of the first
+// matrix, j >= FN / 2 of the second.
+template <int ES, int T, int FN>
+struct GatedReader {
+    Reader<ES, true, T / 2> r;
+    __device__ __forceinline__ explicit GatedReader(int lane) : r(lane) {}
+    __device__ __forceinline__ u32x4_t operator()(const lds_char* stage, int blk) const {
+        const int w = blk / FN, j = blk % FN;
+        return r(stage + j / (FN / 2) * (T / 2 * 64), w * (FN / 2) + j % (FN / 2));
+    }
+};
+
+template <typename O, int T, int N, bool R32 = false>
+using OperandA = std::conditional_t<O::kTwo, TwoOperand<O::ES, T, N>, Operand<O::ES, O::kACols, T, N, R32>>;
+template <typename O, int T, int N, bool R32 = false>
+using OperandB = std::conditional_t<O::kTwo, TwoOperand<O::ES, T, N>,
+                                    std::conditional_t<O::kGated, GatedOperand<O::ES, T, N>, Operand<O::ES, O::kBCols, T, N, R32>>>;
+template <typename O, int T, int FN>
+using ReaderB = std::conditional_t<O::kGated, GatedReader<O::ES, T, FN>, Reader<O::ES, O::kBCols, T>>;
 
 template <Elem E, typename ACC>
 __device__ __forceinline__ ACC mma(u32x4_t a, u32x4_t b, ACC c) {
@@ -272,7 +334,14 @@ struct Tile2 {
     int C;                        // contraction length
     long long crow;               // first row within C
     uint64_t abase, bbase;        // first bytes of the operands
+    uint64_t abase2, bbase2;      // of the second ones, where the variant has any
+    // steps of the contraction
+    template <typename O>
+    __device__ __forceinline__ int steps() const { return (C + O::kStep - 1) / O::kStep * (O::kTwo ? 2 : 1); }
 };
+// columns of C in a tile whose B operand fills BN columns of a stage
+template <typename O>
+constexpr int tile_cols(int BN) { return O::kGated ? BN / 2 : BN; }
 
 // Work items of a launch (all its tiles); fills `g` and, if asked, zeros the rows of no group.
 // Call with all threads.
@@ -283,7 +352,14 @@ __device__ __forceinline__ int count_items(const MmArgs& a, Groups& g) {
         return a.E * ((a.K + BM - 1) / BM) * NJ;             // the tiles of every expert's matrix, rows or not
     } else {
         load_groups(a.offsets, a.E, a.rows, BM, g);
-        if (a.zero_rest) zero_rest(a.offsets, a.E, a.rows, a.c, (long long)J * sizeof(OUT), blockIdx.x, gridDim.x);
+        if (a.zero_rest) {
+            zero_rest(a.offsets, a.E, a.rows, a.c, (long long)J * sizeof(OUT), blockIdx.x, gridDim.x);
+            if constexpr (O::kGated)
+                if (a.ca) {
+                    zero_rest(a.offsets, a.E, a.rows, a.ca, (long long)J * sizeof(OUT), blockIdx.x, gridDim.x);
+                    zero_rest(a.offsets, a.E, a.rows, a.cb, (long long)J * sizeof(OUT), blockIdx.x, gridDim.x);
+                }
+        }
         return uni(g.pre[a.E]) * NJ;
     }
 }
@@ -327,28 +403,48 @@ __device__ __forceinline__ void tile_of_item(const MmArgs& a, const Groups& g, i
         const uint64_t mat = (uint64_t)a.b + (uint64_t)t.e * a.K * a.N * O::ES;
         t.bbase = mat + (O::kBCols ? (uint64_t)t.j0 : (uint64_t)t.j0 * t.C) * O::ES;
     }
+    if constexpr (O::kTwo) t.abase2 = uni(t.abase - (uint64_t)a.a + (uint64_t)a.a2);
+    if constexpr (O::kTwo || O::kGated) t.bbase2 = uni(t.bbase - (uint64_t)a.b + (uint64_t)a.b2);
     t.abase = uni(t.abase);
     t.bbase = uni(t.bbase);
     t.nj = min(BN, J - t.j0);
 }
 
 template <typename O, int T, int N, bool R32 = false>
-__device__ __forceinline__ Operand<O::ES, O::kACols, T, N, R32> operand_a(const MmArgs& a, const Tile2& t) {
+__device__ __forceinline__ OperandA<O, T, N, R32> operand_a(const MmArgs& a, const Tile2& t) {
     Operand<O::ES, O::kACols, T, N, R32> o;
     o.base = t.abase;
     o.ld = (O::KIND == 2 ? a.K : t.C) * O::ES;
     o.n = O::kACols ? t.C : t.ni;
     o.cbytes = t.C * O::ES;
-    return o;
+    if constexpr (O::kTwo) return {o, t.abase2, (t.C + O::kStep - 1) / O::kStep};
+    else return o;
 }
 template <typename O, int T, int N, bool R32 = false>
-__device__ __forceinline__ Operand<O::ES, O::kBCols, T, N, R32> operand_b(const MmArgs& a, const Tile2& t) {
-    Operand<O::ES, O::kBCols, T, N, R32> o;
+__device__ __forceinline__ OperandB<O, T, N, R32> operand_b(const MmArgs& a, const Tile2& t) {
+    constexpr int TB = O::kGated ? T / 2 : T, NB = O::kGated ? N / 2 : N;      // of one matrix
+    Operand<O::ES, O::kBCols, TB, NB, R32> o;
     o.base = t.bbase;
     o.ld = (O::kBCols ? a.N : t.C) * O::ES;
     o.n = O::kBCols ? t.C : t.nj;
     o.cbytes = t.C * O::ES;
-    return o;
+    if constexpr (O::kTwo) {
+        return {o, t.bbase2, (t.C + O::kStep - 1) / O::kStep};
+    } else if constexpr (O::kGated) {
+        auto up = o;
+        up.base = t.bbase2;
+        return {o, up};
+    } else {
+        return o;
+    }
+}
+
+// SiLU(a) b, in fp32 (rounded to bf16 or not at all).
+template <Elem E>
+__device__ __forceinline__ float gated(float a, float b) {
+    float s, ns;
+    sigmoid<E == Elem::bf16>(a, s, ns);
+    return a * s * b;
 }
 
 // Workgroups for the tiles of a launch (row tiles are bounded from the row count: the group

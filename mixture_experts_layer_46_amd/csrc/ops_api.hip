@@ -118,7 +118,7 @@ moe_status too_many(const moe_mm_shape& s, const char* where) {
                 (long long)s.rows, s.E, s.K, s.N);
 }
 
-// `kind` is a moe_mm_product, and one of the kinds of mm_tile.h
+// `kind` is a moe_mm_product, and one of the kinds of mm_tile.h, or one of mm_launch.h's
 moe_status run_mm(int kind, const moe_mm_shape& s, const MmArgs& a, hipStream_t st, const char* where) {
     if (!mm_fits(kind, s.dtype, a)) return too_many(s, where);
     HIPCHK(launch_mm(kind, s.dtype, s.out_dtype, a, st), where);
@@ -203,6 +203,52 @@ const char* moe_grouped_mm_form(const moe_mm_shape* shape, int32_t product, int3
     const MmArgs a = mm_args(*shape, nullptr, nullptr, nullptr, nullptr);
     if (!mm_fits(product, shape->dtype, a)) return too_many(*shape, "grouped_mm_form"), nullptr;
     return mm_form(product, shape->dtype, a, cus ? cus : device_cu_count());
+}
+
+moe_status moe_gated_mm(const moe_mm_shape* shape, const void* x, const void* w_in, const void* w_up, const int32_t* offsets,
+                        void* h, void* a, void* b, hipStream_t stream) {
+    CHECK(check_mm(shape, false, false));
+    if (shape->rows == 0) return MOE_OK;
+    REQ(x, "x");
+    REQ(w_in, "w_in");
+    REQ(w_up, "w_up");
+    REQ(offsets, "offsets");
+    REQ(h, "h");
+    if ((a != nullptr) != (b != nullptr)) return fail(MOE_ERR_NULL, "a and b must be given together");
+    if (a) {
+        REQ(a, "a");
+        REQ(b, "b");
+    }
+    MmArgs m = mm_args(*shape, x, w_in, h, offsets);
+    m.b2 = w_up;
+    m.ca = a;
+    m.cb = b;
+    return run_mm(MM_GATED, *shape, m, stream, "gated_mm");
+}
+
+moe_status moe_gated_mm_dx(const moe_mm_shape* shape, const void* da, const void* db, const void* w_in, const void* w_up,
+                           const int32_t* offsets, void* dx, hipStream_t stream) {
+    CHECK(check_mm(shape, false, false));
+    if (shape->rows == 0) return MOE_OK;
+    REQ(da, "da");
+    REQ(db, "db");
+    REQ(w_in, "w_in");
+    REQ(w_up, "w_up");
+    REQ(offsets, "offsets");
+    REQ(dx, "dx");
+    MmArgs m = mm_args(*shape, da, w_in, dx, offsets);
+    m.a2 = db;
+    m.b2 = w_up;
+    return run_mm(MM_DX_TWO, *shape, m, stream, "gated_mm_dx");
+}
+
+const char* moe_gated_mm_form(const moe_mm_shape* shape, int32_t dx, int32_t cus) {
+    if (cus < 0) return fail(MOE_ERR_SHAPE, "cus = %d < 0", cus), nullptr;
+    if (check_mm(shape, false, false) != MOE_OK) return nullptr;
+    const MmArgs a = mm_args(*shape, nullptr, nullptr, nullptr, nullptr);
+    const int kind = dx ? MM_DX_TWO : MM_GATED;
+    if (!mm_fits(kind, shape->dtype, a)) return too_many(*shape, "gated_mm_form"), nullptr;
+    return mm_form(kind, shape->dtype, a, cus ? cus : device_cu_count());
 }
 
 moe_status moe_quantize_rows(int32_t dtype, int64_t rows, int32_t K, const void* x, int8_t* q, float* scale,

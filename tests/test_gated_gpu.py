@@ -1,0 +1,296 @@
+"""The gated projections and their gradients against 64 bits.
+
+Tolerances: a sum of n products kept in fp32 is off by at most n 2^-23 sum |a||b|; SiLU's slope
+is below 1.1; the sigmoid and the few products around it are off by 2^-20 of their magnitudes
+(bf16: the hardware's exponential and reciprocal; fp32 less).  The projections' gradients are
+rounded to the operands' type before the products, eps / 2 of each, and every output once.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+bf, f32, f64 = torch.bfloat16, torch.float32, torch.float64
+ACT = 2.0 ** -20
+
+
+@pytest.fixture(scope="module", autouse=True)
+def M():
+    import mixture_experts_layer_46_amd as M
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    M._lib.load()
+    return M
+
+
+def half_eps(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype)
+
+
+def offs(counts, start=0):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]) + start, dtype=torch.int32)
+
+
+def check(got, ref, acc, what):
+    """|got - ref| <= acc + eps/2 (|ref| + acc), and NaN exactly where the reference has it."""
+    got = got.detach().cpu()
+    assert got.shape == ref.shape, what
+    tol = acc + half_eps(got.dtype) * (ref.abs() + acc) + 1e-38
+    err = (got.to(f64) - ref).abs()
+    bad = ~(err <= tol)
+    if bool(bad.any()):
+        i = int(torch.nonzero(bad.flatten())[0])
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, first at flat {i}: "
+                             f"{got.flatten()[i].item()} for {ref.flatten()[i].item()} (tolerance {tol.flatten()[i].item():.3g})")
+
+
+def mm(a, b):
+    """a @ b in 64 bits on the GPU, operands dense."""
+    return (a.cuda() @ b.cuda().contiguous()).cpu()
+
+
+def forward_ref(x, w_in, w_up, off):
+    """{h, a, b: (value, tolerance before the last rounding)}"""
+    R, K = x.shape
+    E, _, N = w_in.shape
+    x, w_in, w_up = (t.to(f64) for t in (x, w_in, w_up))
+    z = lambda: torch.zeros(R, N, dtype=f64)
+    a, da, b, db = z(), z(), z(), z()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        for w, v, d in ((w_in, a, da), (w_up, b, db)):
+            v[r] = mm(x[r], w[e])
+            d[r] = K * 2.0 ** -23 * mm(x[r].abs(), w[e].abs())
+    s = a * torch.sigmoid(a)
+    h = s * b
+    return {"a": (a, da), "b": (b, db), "h": (h, 1.1 * da * (b.abs() + db) + s.abs() * db + ACT * (1 + a.abs() / 8) * h.abs())}
+
+
+def grad_ref(dh, x, w_in, w_up, a, b, off):
+    """(dx, dw_in, dw_up), each (value, tolerance before the last rounding)"""
+    R, K = x.shape
+    E, _, N = w_in.shape
+    rnd = half_eps(x.dtype) + ACT
+    dh, x, w_in, w_up, a, b = (t.to(f64) for t in (dh, x, w_in, w_up, a, b))
+    s = torch.sigmoid(a)
+    da, db = dh * b * s * (1 + a * (1 - s)), dh * a * s
+    ma, mb = (dh * b * s).abs() * (1 + a.abs() * (1 - s)), db.abs()
+    dx, tx = torch.zeros(R, K, dtype=f64), torch.zeros(R, K, dtype=f64)
+    dw = [torch.zeros(E, K, N, dtype=f64) for _ in range(4)]
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        n = r.stop - r.start
+        dx[r] = mm(da[r], w_in[e].T) + mm(db[r], w_up[e].T)
+        tx[r] = (2 * N * 2.0 ** -23 + rnd) * (mm(ma[r], w_in[e].abs().T) + mm(mb[r], w_up[e].abs().T))
+        for i, (d, m) in enumerate(((da, ma), (db, mb))):
+            dw[2 * i][e] = mm(x[r].T, d[r])
+            dw[2 * i + 1][e] = (n * 2.0 ** -23 + rnd) * mm(x[r].abs().T, m[r])
+    return (dx, tx), (dw[0], dw[1]), (dw[2], dw[3])
+
+
+def operands(R, E, K, N, dtype):
+    return (rand((R, K), dtype, R + K), rand((E, K, N), dtype, K + N, K ** -0.5), rand((E, K, N), dtype, K + N + 1, K ** -0.5))
+
+
+def kept(M, x, w_in, w_up, off):
+    """(h, a, b) as a training pass keeps them."""
+    return M.gated._gated(x, w_in, w_up, off, None, True)
+
+
+# counts, K, N: one row, empty groups first, last and between, rows around every tile height, odd sizes
+CASES = [([1], 8, 8), ([1], 264, 520), ([0, 1, 0], 32, 64), ([3, 0, 0, 5, 2], 40, 72), ([15, 16, 17, 31, 32, 33], 64, 136),
+         ([63, 64, 65, 1], 136, 264), ([0, 127, 128, 129], 256, 256), ([255, 256, 257, 0], 96, 512), ([320, 2, 511], 520, 264),
+         ([1300], 1032, 328), ([2] * 100 + [0] * 56 + [5] * 100, 48, 40), ([0, 0, 0], 24, 16)]
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("counts,K,N", CASES)
+def test_gated_mm(M, counts, K, N, dtype):
+    say("gated_mm", counts, K, N, dtype)
+    R, E = sum(counts), len(counts)
+    x, w_in, w_up = operands(R, E, K, N, dtype)
+    off = offs(counts)
+    ref = forward_ref(x, w_in, w_up, off)
+    c = [t.cuda() for t in (x, w_in, w_up, off)]
+    h, a, b = kept(M, *c)
+    for name, t in (("a", a), ("b", b), ("h", h)):
+        check(t, *ref[name], name)
+    assert torch.equal(M.gated_mm(*c), h)
+    dh = rand((R, N), dtype, 7)
+    grads = M.gated_mm_grad(dh.cuda(), *c[:3], a, b, c[3])
+    for name, t, r in zip(("dx", "dw_in", "dw_up"), grads, grad_ref(dh, x, w_in, w_up, a.cpu(), b.cpu(), off)):
+        check(t, *r, name)
+
+
+# product, type, form, rows, groups, K, N: a remainder on every side
+FORMS = [("gated", bf, "256x256", 1266, 1, 40, 3488), ("gated", bf, "256x256", 4490, 2, 40, 1128),
+         ("gated", bf, "128x128", 979, 1, 40, 1072), ("gated", bf, "128x128", 8, 5, 56, 3576),
+         ("gated", bf, "64x64", 3, 1, 40, 216), ("gated", bf, "64x64", 1, 5, 40, 72),
+         ("gated", bf, "32x64 thin", 1, 1, 72, 128), ("gated", bf, "32x64 thin", 2, 5, 104, 40),
+         ("gated", f32, "64x64", 3, 1, 40, 272), ("gated", f32, "64x64", 3, 3, 72, 40),
+         ("gated", f32, "32x64 thin", 332, 1, 184, 784), ("gated", f32, "32x64 thin", 6, 5, 504, 3104),
+         ("gated", f32, "16x64 thin", 1, 1, 392, 40), ("gated", f32, "16x64 thin", 1, 5, 104, 40),
+         ("gated dx", bf, "256x256", 5774, 1, 2200, 56), ("gated dx", bf, "256x256", 4639, 3, 1928, 40),
+         ("gated dx", bf, "128x128", 1952, 1, 1096, 40), ("gated dx", bf, "128x128", 879, 5, 2136, 40),
+         ("gated dx", bf, "64x64", 2, 1, 56, 216), ("gated dx", bf, "64x64", 5, 2, 40, 40),
+         ("gated dx", bf, "32x64 thin", 4462, 1, 40, 664), ("gated dx", bf, "32x64 thin", 7, 5, 2376, 976),
+         ("gated dx", bf, "16x64 thin", 1, 1, 40, 576), ("gated dx", bf, "16x64 thin", 1, 3, 56, 384),
+         ("gated dx", f32, "64x64", 181, 1, 1608, 48), ("gated dx", f32, "64x64", 165, 2, 1560, 40),
+         ("gated dx", f32, "32x64 thin", 554, 1, 680, 72), ("gated dx", f32, "32x64 thin", 117, 3, 1944, 64),
+         ("gated dx", f32, "16x64 thin", 1, 1, 40, 128), ("gated dx", f32, "16x64 thin", 1, 2, 40, 104)]
+NAMES = {bf: "bf16", f32: "fp32"}
+each_form = pytest.mark.parametrize("product,dtype,form,R,E,K,N", FORMS,
+                                    ids=lambda v: NAMES.get(v, str(v).replace(" ", "-")))
+
+
+def groups_of(R, E):
+    """(offsets, rows of no group at either end): ragged groups, where there are enough one without
+    rows and one of a single row."""
+    rest = 3 if R > 100 else 0
+    n = R - 2 * rest
+    counts = np.full(E, n // E)
+    if E > 2:
+        counts[1], counts[2] = 0, 1
+    counts[0] += n - counts.sum()
+    return offs(counts, rest), rest
+
+
+@each_form
+def test_forms(M, product, dtype, form, R, E, K, N):
+    say(product, form, R, E, K, N, dtype)
+    code = M._lib.MOE_F32 if dtype == f32 else M._lib.MOE_BF16
+    assert M._lib.grouped_mm_form(product, R, E, K, N, dtype=code, cus=256) == form
+    x, w_in, w_up = operands(R, E, K, N, dtype)
+    off, rest = groups_of(R, E)
+    c = [t.cuda() for t in (x, w_in, w_up, off)]
+    if product == "gated":
+        ref = forward_ref(x, w_in, w_up, off)
+        h, a, b = kept(M, *c)
+        for name, t in (("a", a), ("b", b), ("h", h)):
+            check(t, *ref[name], name)
+            assert not bool(t[:rest].any() or t[R - rest:].any()), "rows of no group"
+        out = torch.full_like(h, 7)
+        M.gated_mm(*c, out=out)
+        assert torch.equal(out[rest:R - rest], h[rest:R - rest])
+        assert bool((out[:rest] == 7).all() and (out[R - rest:] == 7).all())
+    else:
+        a, b, dh = (rand((R, N), dtype, s) for s in (11, 12, 13))
+        ref = grad_ref(dh, x, w_in, w_up, a, b, off)[0]
+        dx = M.gated_mm_grad(dh.cuda(), *c[:3], a.cuda(), b.cuda(), c[3])[0]
+        check(dx, *ref, "dx")
+        assert not bool(dx[:rest].any() or dx[R - rest:].any()), "rows of no group"
+
+
+@each_form
+def test_not_finite_stays(M, product, dtype, form, R, E, K, N):
+    """A NaN of a row stays in it; nothing passes to the next group."""
+    x, w_in, w_up = (t.cuda() for t in operands(R, E, K, N, dtype))
+    off, rest = groups_of(R, E)
+    off = off.cuda()
+    r = R - rest - 1
+    if product == "gated":
+        run = lambda v: M.gated_mm(v, w_in, w_up, off)
+        v = x
+    else:
+        b, dh = rand((R, N), dtype, 12).cuda(), rand((R, N), dtype, 13).cuda()
+        v = rand((R, N), dtype, 11).cuda()
+        run = lambda v: M.gated_mm_grad(dh, x, w_in, w_up, v, b, off)[0]
+    clean = run(v)
+    v[r, v.shape[1] - 1] = float("nan")
+    got = run(v)
+    assert bool(torch.isnan(got[r]).all())
+    keep = torch.arange(R, device="cuda") != r
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("off", [[5, 3, 9], [-4, 2, 100], [0, 100, 2], [9, 9, 9], [100, 100, 100], [-1, -1, -1]])
+@pytest.mark.parametrize("dtype,R,K,N", [(bf, 9, 136, 136), (f32, 9, 136, 136), (bf, 2815, 136, 1128), (f32, 1343, 136, 488)],
+                         ids=str)
+def test_malformed_offsets_stay_inside(M, off, dtype, R, K, N):
+    x, w_in, w_up = (t.cuda() for t in operands(R, 2, K, N, dtype))
+    buf = torch.full((R + 64, N), 3.0, device="cuda", dtype=dtype)
+    M.gated_mm(x, w_in, w_up, torch.tensor([v * R // 9 for v in off], dtype=torch.int32, device="cuda"), out=buf[32:32 + R])
+    assert bool((buf[:32] == 3).all() and (buf[32 + R:] == 3).all())
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "fp32"])
+def test_autograd(M, dtype):
+    """Through autograd, all leaves and single ones, with a gradient at an odd address."""
+    counts, K, N = [40, 0, 25, 1], 72, 104
+    R = sum(counts)
+    x, w_in, w_up = operands(R, 4, K, N, dtype)
+    off = offs(counts).cuda()
+    c = [t.cuda().requires_grad_() for t in (x, w_in, w_up)]
+    h = M.gated_mm(*c, off)
+    _, a, b = kept(M, *(t.detach() for t in c), off)
+    dh = rand((R, N), dtype, 5)
+    odd = torch.zeros(R * N + 1, device="cuda", dtype=dtype)[1:].view(R, N).copy_(dh)
+    ref = grad_ref(dh, x, w_in, w_up, a.cpu(), b.cpu(), off.cpu())
+    grads = torch.autograd.grad(h, c, odd)
+    for name, t, r in zip(("dx", "dw_in", "dw_up"), grads, ref):
+        check(t, *r, name)
+    for i in range(3):
+        only = [t.detach().requires_grad_(j == i) for j, t in enumerate(c)]
+        (g,) = torch.autograd.grad(M.gated_mm(*only, off), only[i], dh.cuda())
+        assert torch.equal(g, grads[i])
+
+
+def test_gradient_against_differences(M):
+    """Differences of the fp32 forward along a direction: the step's third derivative leaves
+    O(h^2), the forward's rounding 2^-20 of the loss's terms over h."""
+    counts, K, N = [30, 0, 17], 64, 72
+    R = sum(counts)
+    x, w_in, w_up = (t.cuda() for t in operands(R, 3, K, N, f32))
+    off, dh = offs(counts).cuda(), rand((R, N), f32, 5).cuda()
+    _, a, b = kept(M, x, w_in, w_up, off)
+    leaves = [x, w_in, w_up]
+    for i, grad in enumerate(M.gated_mm_grad(dh, x, w_in, w_up, a, b, off)):
+        way, h = rand(leaves[i].shape, f32, 20 + i).cuda(), 2.0 ** -8
+        loss = []
+        for sign in (1, -1):
+            v = list(leaves)
+            v[i] = leaves[i] + sign * h * way
+            t = M.gated_mm(*v, off).double() * dh
+            loss.append(t.sum())
+        slope, want = float((loss[0] - loss[1]) / (2 * h)), float((grad.double() * way).sum())
+        bound = 2.0 ** -20 * float(t.abs().sum()) / h + 100 * h * h * float((grad.double() * way).abs().sum())
+        assert abs(slope - want) <= bound, (i, slope, want, bound)
+
+
+def test_captured(M):
+    """A captured pass and its gradient, replayed on new inputs."""
+    counts, K, N = [100, 0, 200], 264, 520
+    R = sum(counts)
+    x, w_in, w_up = (t.cuda() for t in operands(R, 3, K, N, bf))
+    off, dh = offs(counts).cuda(), rand((R, N), bf, 5).cuda()
+
+    def run():
+        h, a, b = kept(M, x, w_in, w_up, off)
+        return (h, *M.gated_mm_grad(dh, x, w_in, w_up, a, b, off))
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in range(3):
+        x.copy_(rand((R, K), bf, 40 + i))
+        want = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+def test_no_rows(M):
+    w = torch.zeros(2, 48, 24, device="cuda")
+    x, off = torch.zeros(0, 48, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    h = M.gated_mm(x, w, w, off)
+    assert h.shape == (0, 24)
+    dx, d1, d2 = M.gated_mm_grad(h, x, w, w, h, h, off)
+    assert dx.shape == (0, 48) and d1.shape == d2.shape == w.shape and not bool(d1.any() or d2.any())
