@@ -10,7 +10,9 @@ x [T, H] (bf16 or fp32), w_gate [H, E] fp32, w_in / w_up [E, H, F], w_out [E, F,
 (w_up None for the two-layer SiLU FFN), bias [E] fp32 or None.
 
 ops.py holds the operators that training the layer (forward_train) and serving it with
-8-bit experts (forward_int8) need, exported here too.
+8-bit experts (forward_int8) need; fp8.py those of experts in 8-bit floating point
+(forward_fp8), gated.py the gated projections in one kernel, norms.py the norms around the
+layer, block.py the layer between them (forward_block).  All are exported here too.
 """
 from __future__ import annotations
 
@@ -21,7 +23,8 @@ from ._lib import (MOE_BF16, MOE_F32, MOE_FFN_SILU2, MOE_FFN_SWIGLU, MOE_FLAG_BI
                    MOE_FLAG_NO_RENORM, MoeError, Shape, capacity_rows)
 from . import ops
 from .ops import *  # noqa: F401,F403  (ops.__all__)
-from . import fp8, gated, norms
+from . import block, fp8, gated, norms
+from .block import *  # noqa: F401,F403
 from .fp8 import *  # noqa: F401,F403
 from .gated import *  # noqa: F401,F403
 from .norms import *  # noqa: F401,F403
@@ -29,7 +32,7 @@ from .norms import *  # noqa: F401,F403
 __all__ = ["forward", "route", "route_from_logits", "permute", "grouped_ffn", "combine",
            "router_stats", "make_shape", "Workspace", "Shape", "MoeError", "forward_intermediates",
            "MOE_FLAG_BIAS_SELECT_ONLY", "MOE_FLAG_NO_RENORM", "capacity_rows"]
-__all__ += ops.__all__ + fp8.__all__ + gated.__all__ + norms.__all__
+__all__ += ops.__all__ + block.__all__ + fp8.__all__ + gated.__all__ + norms.__all__
 
 
 def _dtype_code(t: torch.Tensor) -> int:

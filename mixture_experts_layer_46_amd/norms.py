@@ -61,8 +61,7 @@ def _args(x, z, w_post, gate, scale, w_next, eps):
         _given(w_next, "w_next", torch.float32, (H,), dev)
     kind = _gate_kind(gate, T, H, dev)
     ldx = _row_stride(x, "x")
-    _on(x, "x", None)
-    if z is not None:
+    if z is not None and z.get_device() != dev:
         _on(z, "z", dev)
     s, ws = _shape(T, ldx, ldz, H, code, kind, scale, eps)
     return T, H, dev, s, ws
@@ -76,6 +75,7 @@ def _forward(x, z, w_post, gate, scale, w_next, eps, out):
     T, H, dev, s, _ = _args(x, z, w_post, gate, scale, w_next, eps)
     y = u = None
     if out is None:
+        _on(x, "x", None)
         y = None if z is None else x.new_empty((T, H))
         u = None if w_next is None else x.new_empty((T, H))
     else:
@@ -87,6 +87,7 @@ def _forward(x, z, w_post, gate, scale, w_next, eps, out):
                 continue
             _given(o, name, x.dtype, (T, H), dev)
             _apart(o, name, x=x, z=z, w_post=w_post, gate=gate, w_next=w_next, u=u if o is y else None)
+        _on(x, "x", None)
     if T > 0:
         _launch(dev, "moe_residual_norm", s, x.data_ptr(), _ptr(z), _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(y), _ptr(u))
     if out is not None:
@@ -102,6 +103,7 @@ def _backward(dy, du, x, z, w_post, gate, scale, w_next, eps):
         _given(du, "du", x.dtype, (T, H), dev)
     elif du is not None:
         raise ValueError("du needs w_next")
+    _on(x, "x", None)
     dx = x.new_empty((T, H))
     dz = None if z is None else x.new_empty((T, H))
     dw_post, dgate, dw_next = (None if t is None else torch.empty_like(t) for t in (w_post, gate, w_next))

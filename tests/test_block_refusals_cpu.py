@@ -1,0 +1,243 @@
+"""What the operators around the block refuse on the host: the Python wrappers (CPU tensors: a call
+that passes every check ends at "on the GPU") and the C ABI (addresses never dereferenced)."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import mixture_experts_layer_46_amd as M
+from mixture_experts_layer_46_amd import _lib
+
+FAKE = 1 << 40
+MIS = FAKE + 8
+bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+E4, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.fail("libmoe.so is not built: run python -m mixture_experts_layer_46_amd.build")
+    return _lib.load()
+
+
+def z(*shape, dtype=bf):
+    return torch.zeros(*shape, dtype=torch.uint8).view(dtype) if dtype in (E4, E8) else torch.zeros(*shape, dtype=dtype)
+
+
+W = z(16, dtype=f32)
+OFF = z(5, dtype=i32)
+X8, XS, W8, WS = z(6, 32, dtype=E4), z(6, 4, dtype=E8), z(4, 24, 32, dtype=E4), z(4, 1, 4, dtype=E8)
+
+
+@pytest.mark.parametrize("call,msg", [
+    (lambda: M.norm(z(6, 16), None), "w is required"),
+    (lambda: M.norm(z(6, 16), W), "on the GPU"),
+    (lambda: M.norm(z(16), W), "x must be a tensor of 2"),
+    (lambda: M.norm(z(6, 16, dtype=torch.float16), W), "unsupported element type"),
+    (lambda: M.norm(z(6, 16), z(16)), "w_next must be torch.float32"),
+    (lambda: M.norm(z(6, 16), z(8, dtype=f32)), "w_next must have shape"),
+    (lambda: M.norm(z(6, 32)[:, ::2], W), "contiguous along its last"),
+    (lambda: M.norm(z(6, 16).requires_grad_(), W, out=z(6, 16)), "out cannot be given"),
+    (lambda: M.norm(z(6, 16), W, out=z(6, 8)), "u must have shape"),
+    (lambda: M.norm_grad(z(6, 8), z(6, 16), W), "du must have shape"),
+    (lambda: M.norm_grad(z(6, 16), z(6, 16), None), "w is required"),
+    (lambda: M.residual_norm(z(6, 16), None), "z is required"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 8)), "z must be"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16, dtype=f32)), "z must be"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16), z(8, dtype=f32)), "w_post must have shape"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16), W, z(6, dtype=f32)), "gate must have shape"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16), W, z(5, 1, dtype=f32)), "gate must have shape"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16), W, z(16)), "gate must be torch.float32"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16), W, W, 1.0, W), "on the GPU"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16), out=(z(6, 16), z(6, 16))), "u is not made"),
+    (lambda: M.residual_norm(z(6, 16), z(6, 16), w_next=W, out=(z(6, 16), None)), "u is required"),
+    (lambda: M.residual_norm_grad(z(6, 16), None, z(6, 16), z(6, 16), w_next=W), "du is required"),
+    (lambda: M.residual_norm_grad(z(6, 16), z(6, 16), z(6, 16), z(6, 16)), "du needs w_next"),
+    (lambda: M.residual_norm_grad(z(6, 8), None, z(6, 16), z(6, 16)), "dy must have shape"),
+    (lambda: M.quantize_rows_fp8(z(6)), "x must be a tensor of 2"),
+    (lambda: M.quantize_rows_fp8(z(6, 16, dtype=torch.float16)), "unsupported element type"),
+    (lambda: M.quantize_rows_fp8(z(6, 16)), "on the GPU"),
+    (lambda: M.quantize_experts_fp8(z(6, 16)), "w must be a tensor of 3"),
+    (lambda: M.grouped_mm_fp8(z(6, 32), XS, W8, WS, OFF), "xq must be torch.float8_e4m3fn"),
+    (lambda: M.grouped_mm_fp8(X8, z(6, 1, dtype=E8), W8, WS, OFF), "x_scale must have shape"),
+    (lambda: M.grouped_mm_fp8(X8, z(6, 4, dtype=f32), W8, WS, OFF), "x_scale must be torch.float8_e8m0fnu"),
+    (lambda: M.grouped_mm_fp8(X8, XS, z(4, 24, 48, dtype=E4), WS, OFF), "wq must have shape"),
+    (lambda: M.grouped_mm_fp8(X8, XS, W8, z(4, 24, 4, dtype=E8), OFF), "w_scale must have shape"),
+    (lambda: M.grouped_mm_fp8(X8, XS, W8, WS, z(4, dtype=i32)), "offsets must have shape"),
+    (lambda: M.grouped_mm_fp8(X8, XS, W8, WS, OFF, dtype=torch.float16), "unsupported output type"),
+    (lambda: M.grouped_mm_fp8(X8, XS, W8, WS, OFF, out=z(6, 32)), "out must have shape"),
+    (lambda: M.grouped_mm_fp8(X8, XS, W8, WS, OFF), "on the GPU"),
+    (lambda: M.gated_mm(z(6, 16), z(16, 24), z(16, 24), OFF), "w_in must be a tensor of 3"),
+    (lambda: M.gated_mm(z(6, 16), z(4, 16, 24), z(4, 16, 32), OFF), "w_up must have shape"),
+    (lambda: M.gated_mm(z(6, 16), z(4, 16, 24), None, OFF), "w_up is required"),
+    (lambda: M.gated_mm(z(6, 16), z(4, 16, 24, dtype=f32), z(4, 16, 24), OFF), "w_in must be torch.bfloat16"),
+    (lambda: M.gated_mm(z(6, 24), z(4, 16, 24), z(4, 16, 24), OFF), "x must have shape"),
+    (lambda: M.gated_mm(z(6, 16), z(4, 16, 24), z(4, 16, 24), z(4, dtype=i32)), "offsets must have shape"),
+    (lambda: M.gated_mm(z(6, 16), z(4, 16, 24), z(4, 16, 24), OFF, out=z(6, 16)), "out must have shape"),
+    (lambda: M.gated_mm(z(6, 16).requires_grad_(), z(4, 16, 24), z(4, 16, 24), OFF, out=z(6, 24)), "out cannot be given"),
+    (lambda: M.gated_mm(z(6, 16), z(4, 16, 24), z(4, 16, 24), OFF), "on the GPU"),
+    (lambda: M.gated_mm_grad(z(6, 16), z(6, 16), z(4, 16, 24), z(4, 16, 24), z(6, 24), z(6, 24), OFF), "dh must have shape"),
+    (lambda: M.gated_mm_grad(z(6, 24), z(6, 16), z(4, 16, 24), z(4, 16, 24), z(6, 16), z(6, 24), OFF), "a must have shape"),
+    (lambda: M.gated_mm_grad(z(6, 24), z(6, 16), z(4, 16, 24), z(4, 16, 24), z(6, 24), None, OFF), "b is required"),
+])
+def test_wrappers_refuse(call, msg):
+    with pytest.raises((ValueError, TypeError), match=msg):
+        call()
+
+
+T, H, E, F, K = 4, 32, 4, 48, 2
+
+
+def _fp8(h=H, e=E, f=F, up=True):
+    pair = lambda n, k: (z(e, n, k, dtype=E4), z(e, (n + 127) // 128, (k + 511) // 512 * 4, dtype=E8))
+    return M.Fp8Experts(pair(f, h), pair(f, h) if up else None, pair(h, f))
+
+
+GOOD, WIDE, FEW, THIN, LONG = _fp8(), _fp8(h=64), _fp8(e=3), _fp8(f=32), _fp8(h=528)
+
+
+@pytest.mark.parametrize("experts,msg", [
+    (GOOD._replace(w_out=WIDE.w_out), "w_out, 8-bit, must have shape"), (GOOD._replace(w_out=THIN.w_out), "w_out, 8-bit, must have"),
+    (GOOD._replace(w_up=WIDE.w_up), "w_up, 8-bit, must have shape"), (FEW, "w_in, 8-bit, must have shape"),
+    (GOOD._replace(w_out=(GOOD.w_out[0], LONG.w_out[1])), "w_out's scale must have shape"),
+    (GOOD._replace(w_in=(GOOD.w_in[0], z(E, 1, 4, dtype=f32))), "w_in's scale must be"),
+    (GOOD._replace(w_in=(z(E, F, H), GOOD.w_in[1])), "w_in, 8-bit, must be torch.float8_e4m3fn"),
+    (GOOD._replace(w_out=(None, GOOD.w_out[1])), "w_out, 8-bit, is required")])
+def test_fp8_layer_refuses_experts_that_do_not_fit(experts, msg):
+    for call in (lambda: M.forward_fp8(z(T, H), z(H, E, dtype=f32), experts, K),
+                 lambda: M.forward_fp8(z(0, H), z(H, E, dtype=f32), experts, K),
+                 lambda: M.grouped_ffn_fp8(z(T * K, H), z(E + 1, dtype=i32), experts),
+                 lambda: M.forward_block(z(T, H), z(T, H), z(H, E, dtype=f32), experts, K)):
+        with pytest.raises(ValueError, match=msg):
+            call()
+
+
+def test_block_refuses():
+    w, ex = z(H, E, dtype=f32), (z(E, H, F), z(E, H, F), z(E, F, H))
+    with pytest.raises(ValueError, match="no gradient"):
+        M.forward_block(z(T, H), z(T, H).requires_grad_(), w, GOOD, K)
+    with pytest.raises(ValueError, match="renormalised"):
+        M.forward_block(z(T, H), z(T, H).requires_grad_(), w, ex, K, flags=M.MOE_FLAG_NO_RENORM)
+    with pytest.raises(ValueError, match="at least one token"):
+        M.forward_block(z(0, H), z(0, H).requires_grad_(), w, ex, K)
+
+
+def _norm(**kw):
+    d = dict(T=8, ldx=64, ldz=64, H=64, dtype=1, gate=1, scale=1.0, eps=1e-6)
+    d.update(kw)
+    return ctypes.byref(_lib.NormShape(**d))
+
+
+SHAPES = [(dict(T=-1), 2), (dict(T=1 << 31), 3), (dict(H=0), 2), (dict(H=60), 3), (dict(H=16392, ldx=16392, ldz=16392), 3),
+          (dict(dtype=5), 3), (dict(ldx=56), 2), (dict(ldx=68), 3), (dict(ldz=56), 2), (dict(ldz=1 << 31), 3), (dict(gate=3), 3),
+          (dict(gate=-1), 3), (dict(gate=0), 1), (dict(eps=0.0), 2), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2),
+          (dict(eps=float("inf")), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2)]
+
+
+@pytest.mark.parametrize("kw,code", SHAPES)
+def test_norm_shapes(lib, kw, code):
+    assert lib.moe_residual_norm(_norm(**kw), *[FAKE] * 7, None) == code
+    assert lib.moe_last_error().decode() != ""
+    assert lib.moe_residual_norm_grad(_norm(**kw), *[FAKE] * 13, 1 << 40, None) == code
+
+
+def test_norm_pointers(lib):
+    fwd = lambda x=FAKE, zz=FAKE, w1=FAKE, g=FAKE, w2=FAKE, y=FAKE, u=FAKE, **kw: \
+        lib.moe_residual_norm(_norm(**kw), x, zz, w1, g, w2, y, u, None)
+    assert lib.moe_residual_norm(None, *[FAKE] * 7, None) == 1
+    for name in ("x", "y", "u", "w2", "g"):
+        assert fwd(**{name: None}) == 1, name
+    for name in ("x", "zz", "w1", "g", "w2", "y", "u"):
+        assert fwd(**{name: MIS}) == 4, name
+    assert fwd(zz=None, y=None) == 1 and fwd(zz=None, w1=None, g=None, gate=0) == 1
+    assert fwd(zz=None, w1=None, g=None, y=None, w2=None, u=None, gate=0) == 1
+    n = ctypes.c_size_t(0)
+    assert lib.moe_residual_norm_grad_workspace(_norm(), ctypes.byref(n)) == 0 and n.value == 8 // 4 * 3 * 64 * 4
+    assert lib.moe_residual_norm_grad_workspace(_norm(T=0), ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.moe_residual_norm_grad_workspace(_norm(H=60), ctypes.byref(n)) == 2
+    assert lib.moe_residual_norm_grad_workspace(None, ctypes.byref(n)) == 1
+    assert lib.moe_residual_norm_grad_workspace(_norm(), None) == 1
+    names = ["dy", "du", "x", "z", "w_post", "gate", "w_next", "dx", "dz", "dw_post", "dgate", "dw_next", "workspace"]
+
+    def grad(size=1 << 40, **kw):
+        return lib.moe_residual_norm_grad(_norm(), *[kw.get(n, FAKE) for n in names], size, None)
+
+    for name in names:
+        assert grad(**{name: MIS}) == 4, name
+        if name != "dy":
+            assert grad(**{name: None}) == 1, name
+    assert grad(size=8 // 4 * 3 * 64 * 4 - 1) == 5
+
+
+def _mm(**kw):
+    d = dict(rows=64, E=4, K=64, N=128, dtype=_lib.MOE_BF16, out_dtype=_lib.MOE_BF16, flags=0)
+    d.update(kw)
+    return ctypes.byref(_lib.MmShape(**d))
+
+
+BAD = [(dict(rows=-1), 2), (dict(E=0), 2), (dict(K=0), 2), (dict(N=-8), 2), (dict(E=257), 3), (dict(K=60), 3), (dict(N=4), 3),
+       (dict(K=(1 << 20) + 16), 3), (dict(rows=1 << 30), 3), (dict(flags=2), 3), (dict(out_dtype=9), 3)]
+
+
+@pytest.mark.parametrize("kw,code", BAD + [(dict(dtype=7, out_dtype=7), 3), (dict(dtype=_lib.MOE_F32), 3)])
+def test_gated_shapes(lib, kw, code):
+    assert lib.moe_gated_mm(_mm(**kw), *[FAKE] * 7, None) == code
+    assert lib.moe_gated_mm_dx(_mm(**kw), *[FAKE] * 6, None) == code
+    assert lib.moe_gated_mm_form(_mm(**kw), 0, 256) is None and lib.moe_last_error().decode() != ""
+
+
+@pytest.mark.parametrize("kw,code", BAD + [(dict(K=24), 3)])
+def test_fp8_shapes(lib, kw, code):
+    assert lib.moe_grouped_mm_fp8(_mm(**kw), *[FAKE] * 6, None) == code
+    assert lib.moe_grouped_mm_fp8_form(_mm(**kw), 256) is None
+
+
+def _null_and_misaligned(fn, args, names):
+    for i, name in enumerate(names):
+        for bad, code in ((None, 1), (MIS, 4)):
+            a = list(args)
+            a[i] = bad
+            assert fn(*a) == code, (name, bad)
+            assert name in _lib.load().moe_last_error().decode()
+
+
+def test_null_and_alignment(lib):
+    s = _mm()
+    _null_and_misaligned(lambda *a: lib.moe_gated_mm(s, *a, None, None, None), [FAKE] * 5, ["x", "w_in", "w_up", "offsets", "h"])
+    assert lib.moe_gated_mm(s, *[FAKE] * 5, FAKE, None, None) == 1 and lib.moe_gated_mm(s, *[FAKE] * 5, MIS, FAKE, None) == 4
+    assert lib.moe_gated_mm(s, *[FAKE] * 5, FAKE, MIS, None) == 4
+    _null_and_misaligned(lambda *a: lib.moe_gated_mm_dx(s, *a, None), [FAKE] * 6, ["da", "db", "w_in", "w_up", "offsets", "dx"])
+    _null_and_misaligned(lambda *a: lib.moe_grouped_mm_fp8(s, *a, None), [FAKE] * 6,
+                         ["xq", "x_scale", "wq", "w_scale", "offsets", "y"])
+    _null_and_misaligned(lambda *a: lib.moe_quantize_rows_fp8(1, 4, 64, *a, None), [FAKE] * 3, ["x", "q", "scale"])
+    _null_and_misaligned(lambda *a: lib.moe_quantize_experts_fp8(1, 4, 64, 64, *a, None), [FAKE] * 3, ["w", "q", "scale"])
+    assert lib.moe_gated_mm(None, *[FAKE] * 7, None) == 1 and lib.moe_grouped_mm_fp8(None, *[FAKE] * 6, None) == 1
+
+
+def test_quantize_fp8_refusals(lib):
+    q = lambda dtype=1, rows=4, k=64: lib.moe_quantize_rows_fp8(dtype, rows, k, FAKE, FAKE, FAKE, None)
+    assert q(rows=-1) == 2 and q(rows=1 << 24) == 3 and q(k=24) == 3 and q(k=0) == 2 and q(dtype=3) == 3
+    assert q(k=(1 << 20) + 16) == 3
+    e = lambda dtype=1, n_e=4, k=64, n=64: lib.moe_quantize_experts_fp8(dtype, n_e, k, n, FAKE, FAKE, FAKE, None)
+    assert e(n_e=0) == 2 and e(n_e=257) == 3 and e(k=24) == 3 and e(n=12) == 3 and e(dtype=4) == 3
+    assert e(n_e=256, k=1 << 20, n=1 << 10) == 3          # 2^24 blocks
+
+
+def test_nothing_to_do_is_ok(lib):
+    assert lib.moe_gated_mm(_mm(rows=0), *[None] * 7, None) == 0 and lib.moe_gated_mm_dx(_mm(rows=0), *[None] * 6, None) == 0
+    assert lib.moe_grouped_mm_fp8(_mm(rows=0), *[None] * 6, None) == 0
+    assert lib.moe_quantize_rows_fp8(1, 0, 64, None, None, None, None) == 0
+    assert lib.moe_residual_norm(_norm(T=0), *[None] * 7, None) == 0
+
+
+def test_struct_layout():
+    assert ctypes.sizeof(_lib.NormShape) == 48 and _lib.NormShape.eps.offset == 40
+
+
+def test_form_query_names():
+    for p in ("fp8", "gated", "gated dx"):
+        assert _lib.grouped_mm_form(p, 8192, 8, 4096, 14336, cus=256) == "256x256"
+        with pytest.raises(ValueError, match="rows"):
+            _lib.grouped_mm_form(p, -1, 8, 4096, 14336, cus=256)
