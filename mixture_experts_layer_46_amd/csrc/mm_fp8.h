@@ -30,11 +30,11 @@ using OpF8 = Op<3, Elem::i8>;             // addresses, tiles and groups are tho
 __host__ __device__ inline int fp8_scale_bytes(int K) { return (K + 511) / 512 * 4; }      // of a row of scales
 
 // 32-index block `blk` of a step's stage as a matrix operand: lane l holds index l & 31 and
-// contraction bytes 32 (l >> 5) .. + 31.
+// contraction bytes 32 (l >> 5) .. + 31.  With rows = 16, an operand of 16 indexes twice.
 struct Reader32 {
     int rd;
-    __device__ __forceinline__ explicit Reader32(int lane) {
-        const int m = lane & 31;
+    __device__ __forceinline__ explicit Reader32(int lane, int rows = 32) {
+        const int m = lane & (rows - 1);
         rd = m * 64 + (((lane >> 5) * 2 ^ swa32(m)) << 4);
     }
     __device__ __forceinline__ i32x8_t operator()(const lds_char* stage, int blk) const {
@@ -57,14 +57,15 @@ __device__ __forceinline__ void open16(u32x4_t q, bf16x8_t& lo, bf16x8_t& hi) {
     lo = bf16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
     hi = bf16x8_t{p[4][0], p[4][1], p[5][0], p[5][1], p[6][0], p[6][1], p[7][0], p[7][1]};
 }
-// A block's sums in fp32, of FM x FN pairs: two steps of 64 bytes, and the exponents (biased) of
-// each row block's and of the columns.  Lane l gets row l & 15 and columns 4 (l >> 4) .. + 3.
-template <int FM, int FN>
-__device__ __forceinline__ void block_f32(const u32x4_t (&a)[2][FM], const u32x4_t (&b)[2][FN], const uint32_t (&sx)[FM],
+// Sums in fp32 of U steps of 64 bytes within a block, of FM x FN pairs, scaled: sx, sw are the
+// exponents (biased) of each row block and of the columns.  Lane l gets row l & 15 and columns
+// 4 (l >> 4) .. + 3.
+template <int U, int FM, int FN>
+__device__ __forceinline__ void block_f32(const u32x4_t (&a)[U][FM], const u32x4_t (&b)[U][FN], const uint32_t (&sx)[FM],
                                           uint32_t sw, f32x4_t (&acc)[FM][FN]) {
     f32x4_t part[FM][FN];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < U; ++u) {
         bf16x8_t a0[FM], a1[FM];
 #pragma unroll
         for (int i = 0; i < FM; ++i) open16(a[u][i], a0[i], a1[i]);
