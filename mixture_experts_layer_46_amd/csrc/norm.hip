@@ -101,7 +101,7 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*red)[16], i
     return float2{a, b};
 }
 __device__ __forceinline__ void clear_red(float2 (*red)[16]) {
-    if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = float2{0.f, 0.f};
+    if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = float2{0.f, 0.f};      // at least a wavefront calls
     __syncthreads();
 }
 
@@ -191,84 +191,138 @@ __global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm(NormArgs a) 
     }
 }
 
-// HOLD: the parameters stay in registers; otherwise (rows above 8192) they are read again for
-// each row, since the sums over rows take the registers.
-template <typename T, int RPW, int C, bool HOLD>
-__global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm_grad(NormGradArgs g) {
+// Rows side by side in a workgroup of `rpw` rows, P threads (whole wavefronts) each: the sums over
+// rows then leave the workgroup once for all of them.  C = 2 (rows above 8192): two of the three
+// sums over rows live in LDS and the parameters are read again for each row, since registers hold
+// one row less far.
+template <typename T, int C>
+__global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int rpw) {
+    constexpr bool HOLD = C == 1, AHEAD = C == 1;       // the next row's loads ahead
     const NormArgs& a = g.f;
-    __shared__ float2 red[2][16];
-    __shared__ float sums[RPW > 1 ? 64 * C * 8 : 1];
-    if constexpr (RPW == 1) clear_red(red);
+    extern __shared__ float lds[];                      // sums of a row's columns: [P C 8], C = 2: twice
+    __shared__ float2 red[2][16][16];                   // [slot][row][wavefront of the row]
+    for (int i = threadIdx.x; i < 512; i += blockDim.x) red[i >> 8][(i >> 4) & 15][i & 15] = float2{0.f, 0.f};
     int slot = 0;
-    const int P = row_threads<RPW>(), t = row_thread<RPW>(), sub = RPW > 1 ? (int)(threadIdx.x >> 6) : 0, H = a.H;
-    const long long first = (long long)blockIdx.x * RPW + sub, step = (long long)gridDim.x * RPW;
+    const int H = a.H, wave = threadIdx.x >> 6, W = P >> 6;
+    const int sub = __builtin_amdgcn_readfirstlane(wave / W), t = threadIdx.x - sub * P;
+    const long long first = (long long)blockIdx.x * rpw + sub, step = (long long)gridDim.x * rpw;
     const float over = 1.f / (float)H;
     const T *x = (const T*)a.x, *z = (const T*)a.z, *dy = (const T*)g.dy, *du = (const T*)g.du;
     const bool need_z = z && (a.w_post || a.w_next || a.gate_kind), channel = a.gate_kind == 1;
     const float* gate_c = channel ? a.gate : nullptr;
-    float w1[C][8], gc[C][8], w2[C][8];
-    float s1[C][8] = {}, sg[C][8] = {}, s2[C][8] = {};
+    auto sum = [&](float p, float q) {
+        p = wave_sum(p);
+        q = wave_sum(q);
+        if (W > 1) {
+            if ((threadIdx.x & 63) == 0) red[slot][sub][wave - sub * W] = float2{p, q};
+            __syncthreads();
+            const float2 r = red[slot][sub][threadIdx.x & 15];
+            p = sum16(r.x);
+            q = sum16(r.y);
+            slot ^= 1;
+        }
+        return float2{p, q};
+    };
+    float w1[HOLD ? C : 1][8], gc[HOLD ? C : 1][8], w2[HOLD ? C : 1][8];
+    float s1[HOLD ? C : 1][8] = {}, sg[HOLD ? C : 1][8] = {}, s2[C][8] = {};
     if constexpr (HOLD) {
         get_params<C>(a.w_post, P, t, H, w1);
         get_params<C>(gate_c, P, t, H, gc);
         get_params<C>(a.w_next, P, t, H, w2);
+    } else {
+        for (int i = threadIdx.x; i < 2 * C * 8 * P; i += blockDim.x) lds[i] = 0.f;
     }
-    Chunk<T> xn[C], zn[C], dyn[C], dun[C];
+    __syncthreads();
+    // chunk c's parameters
+    auto param = [&](const float* w, const float (&held)[HOLD ? C : 1][8], int c, float (&v)[8]) {
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = held[c][j];
+        } else {
+            const int col = (c * P + t) * 8;
+            Chunk<float> k;
+            k.a = k.b = make_float4(1.f, 1.f, 1.f, 1.f);
+            asm volatile("" : "+s"(w));                   // read where they are used, not kept through the rows
+            if (w && col < H) k.get(w + col);
+            k.open(v);
+        }
+    };
+    auto weight = [&](int c, float (&v)[8]) {             // gate w_post
+        float q[8];
+        param(a.w_post, w1, c, v);
+        param(gate_c, gc, c, q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= q[j];
+    };
+    Chunk<T> xn[C], zn[C], gn[C], un[C];
     auto start = [&](long long r) {
         const bool live = r < a.T;
         get_row<C>(x + r * a.ldx, live && a.w_next, P, t, H, xn);
         get_row<C>(z + r * a.ldz, live && need_z, P, t, H, zn);
-        get_row<C>(dy + r * H, live && dy, P, t, H, dyn);
-        get_row<C>(du + r * H, live && a.w_next, P, t, H, dun);
+        get_row<C>(dy + r * H, live && dy, P, t, H, gn);
+        get_row<C>(du + r * H, live && a.w_next, P, t, H, un);
     };
-    start(first);
-    for (long long r0 = (long long)blockIdx.x * RPW; r0 < a.T; r0 += step) {
+    if constexpr (AHEAD) start(first);
+    // every row of threads runs the same number of rounds, so that the barriers match
+    for (long long r0 = (long long)blockIdx.x * rpw; r0 < a.T; r0 += step) {
         const long long r = r0 + sub;
         const bool live = r < a.T;
-        if constexpr (!HOLD) {
-            get_params<C>(a.w_post, P, t, H, w1);
-            get_params<C>(gate_c, P, t, H, gc);
-            get_params<C>(a.w_next, P, t, H, w2);
-        }
-        float xv[C][8], zv[C][8], gv[C][8], uv[C][8];
+        if constexpr (!AHEAD) start(r);
+        float xv[C][8], gv[C][8];
+        Chunk<T> zc[C], uc[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) xn[c].open(xv[c]), zn[c].open(zv[c]), dyn[c].open(gv[c]), dun[c].open(uv[c]);
+        for (int c = 0; c < C; ++c) xn[c].open(xv[c]), gn[c].open(gv[c]), zc[c] = zn[c], uc[c] = un[c];
         const float gt = a.gate_kind == 2 && live ? a.gate[r] : 1.f;
-        start(r + step);
+        if constexpr (AHEAD) start(r + step);
         float rz = 1.f;
         if (a.w_post) {
             float s = 0.f;
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c) {
+                float zv[8];
+                zc[c].open(zv);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(zv[c][j], zv[c][j], s);
-            rz = rsqrtf(row_sum<RPW>(s, 0.f, red, slot).x * over + a.eps);
+                for (int j = 0; j < 8; ++j) s = fmaf(zv[j], zv[j], s);
+            }
+            rz = rsqrtf(sum(s, 0.f).x * over + a.eps);
         }
         if (a.w_next) {
             float sy = 0.f, st = 0.f;
             if (z) {
                 const float f = rz * gt;
 #pragma unroll
-                for (int c = 0; c < C; ++c)
+                for (int c = 0; c < C; ++c) {
+                    float zv[8], w[8];
+                    zc[c].open(zv);
+                    weight(c, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) xv[c][j] = fmaf(a.scale, xv[c][j], zv[c][j] * f * (w1[c][j] * gc[c][j]));
+                    for (int j = 0; j < 8; ++j) xv[c][j] = fmaf(a.scale, xv[c][j], zv[j] * f * w[j]);
+                }
             }
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c) {
+                float uv[8], w[8];
+                uc[c].open(uv);
+                param(a.w_next, w2, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     sy = fmaf(xv[c][j], xv[c][j], sy);
-                    st = fmaf(uv[c][j] * w2[c][j], xv[c][j], st);
+                    st = fmaf(uv[j] * w[j], xv[c][j], st);
                 }
-            const float2 s = row_sum<RPW>(sy, st, red, slot);
+            }
+            const float2 s = sum(sy, st);
             const float ry = rsqrtf(s.x * over + a.eps), k = ry * ry * (s.y * over);
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c) {
+                float uv[8], w[8];
+                uc[c].open(uv);
+                param(a.w_next, w2, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    gv[c][j] += ry * (uv[c][j] * w2[c][j] - xv[c][j] * k);
-                    s2[c][j] = fmaf(uv[c][j], xv[c][j] * ry, s2[c][j]);
+                    gv[c][j] += ry * (uv[j] * w[j] - xv[c][j] * k);
+                    s2[c][j] = fmaf(uv[j], xv[c][j] * ry, s2[c][j]);
                 }
+            }
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -283,10 +337,14 @@ __global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm_grad(NormGra
             if (a.w_post || a.gate_kind == 2) {
                 float s = 0.f;
 #pragma unroll
-                for (int c = 0; c < C; ++c)
+                for (int c = 0; c < C; ++c) {
+                    float zv[8], w[8];
+                    zc[c].open(zv);
+                    weight(c, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s = fmaf(gv[c][j] * (w1[c][j] * gc[c][j]), zv[c][j], s);
-                s = row_sum<RPW>(s, 0.f, red, slot).x;
+                    for (int j = 0; j < 8; ++j) s = fmaf(gv[c][j] * w[j], zv[j], s);
+                }
+                s = sum(s, 0.f).x;
                 if (a.gate_kind == 2 && live && t == 0) g.dgate[r] = s * rz;
                 if (a.w_post) k = s * rz * rz * over;
             }
@@ -294,46 +352,72 @@ __global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm_grad(NormGra
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int col = (c * P + t) * 8;
-                float o[8];
+                float o[8], zv[8], p1[8], pg[8];
+                zc[c].open(zv);
+                param(a.w_post, w1, c, pg);
+                param(gate_c, gc, c, p1);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float q = gv[c][j] * (zv[c][j] * f);
-                    s1[c][j] = fmaf(q, gc[c][j], s1[c][j]);
-                    sg[c][j] = fmaf(q, w1[c][j], sg[c][j]);
-                    o[j] = f * (gv[c][j] * (w1[c][j] * gc[c][j]) - zv[c][j] * k);
+                    const float q = gv[c][j] * (zv[j] * f);
+                    o[j] = f * (gv[c][j] * (pg[j] * p1[j]) - zv[j] * k);
+                    p1[j] *= q;
+                    pg[j] *= q;
                 }
                 if (live && col < H) Chunk<T>::put((T*)g.dz + r * H + col, o);
+                if constexpr (HOLD) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s1[c][j] += p1[j], sg[c][j] += pg[j];
+                } else {
+                    // this thread's own places, 16 bytes a lane side by side
+                    float4* l = reinterpret_cast<float4*>(lds) + (c * 4) * P + t;
+                    auto add = [&](float4* at, const float* v) {
+                        const float4 o4 = *at;
+                        *at = make_float4(o4.x + v[0], o4.y + v[1], o4.z + v[2], o4.w + v[3]);
+                    };
+                    if (a.w_post) add(l, p1), add(l + P, p1 + 4);
+                    if (channel) add(l + 2 * P, pg), add(l + 3 * P, pg + 4);
+                }
             }
         }
     }
-    // this workgroup's sums: [3][H] of the workspace, those of its rows of threads added in order
+    // this workgroup's sums: [3][H] of the workspace, those of its rows added in order
     float* part = g.parts + (size_t)blockIdx.x * 3 * H;
-    auto put = [&](int which, float (&s)[C][8]) {
-        if constexpr (RPW == 1) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int col = (c * P + t) * 8;
-                if (col < H) Chunk<float>::put(part + (size_t)which * H + col, s[c]);
-            }
-        } else {
-            for (int k = 0; k < RPW; ++k) {
-                __syncthreads();
-                if (sub == k)
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float* p = sums + (c * P + t) * 8 + j;
-                            *p = k ? *p + s[c][j] : s[c][j];
-                        }
-            }
-            __syncthreads();
-            for (int i = threadIdx.x; i < H; i += 64 * RPW) part[(size_t)which * H + i] = sums[i];
+    auto put = [&](int which, const float (&s)[8], int c) {
+        const int col = (c * P + t) * 8;
+        if (rpw == 1) {
+            if (col < H) Chunk<float>::put(part + (size_t)which * H + col, s);
+            return;
         }
+        for (int k = 0; k < rpw; ++k) {
+            __syncthreads();
+            if (sub == k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float* p = lds + j * P + t;
+                    *p = k ? *p + s[j] : s[j];
+                }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 8 * P; i += blockDim.x)
+            if (i % P * 8 + i / P < H) part[(size_t)which * H + i % P * 8 + i / P] = lds[i];
     };
-    if (a.w_post) put(0, s1);
-    if (channel) put(1, sg);
-    if (a.w_next) put(2, s2);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if constexpr (HOLD) {
+            if (a.w_post) put(0, s1[c], c);
+            if (channel) put(1, sg[c], c);
+        } else {
+            const float4* l = reinterpret_cast<const float4*>(lds) + (c * 4) * P + t;
+            auto get = [&](int which) {
+                const float4 p = l[2 * which * P], q = l[(2 * which + 1) * P];
+                const float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+                put(which, v, c);
+            };
+            if (a.w_post) get(0);
+            if (channel) get(1);
+        }
+        if (a.w_next) put(2, s2[c], c);
+    }
 }
 
 // Adds the workgroups' sums: 64 columns per workgroup, its 16 wavefronts over the partial sums.
@@ -344,8 +428,17 @@ __global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ 
     float* d = which == 0 ? d0 : which == 1 ? d1 : d2;
     if (!d) return;
     float s = 0.f;
-    if (col < H)
-        for (int i = wave; i < n; i += 16) s += parts[((size_t)i * 3 + which) * H + col];
+    if (col < H) {
+        const float* p = parts + (size_t)which * H + col;
+        const size_t row = (size_t)3 * H;
+        for (int i = wave; i < n; i += 16 * 8) {              // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = i + 16 * k < n ? p[(i + 16 * k) * row] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
+    }
     sums[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && col < H) {
@@ -356,40 +449,58 @@ __global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ 
     }
 }
 
-// Rows up to 512: a wavefront each, four to a workgroup.  Longer ones: a workgroup each, a chunk
-// a thread up to 8192, then two.
-bool short_rows(int H) { return H <= 512; }
-int threads_for(int H) { return short_rows(H) ? 256 : ((H <= 8192 ? H / 8 : (H + 15) / 16) + 63) / 64 * 64; }
+// Threads of a row: a chunk each up to 8192 columns, then two.
+int row_threads_of(int H) { return ((H <= 8192 ? H / 8 : (H + 15) / 16) + 63) / 64 * 64; }
 
+constexpr int kMaxRow = 16384;
+
+// Rows up to 512 columns: a wavefront each, four to a workgroup; longer ones a workgroup each.
 template <typename T>
 hipError_t go(const NormArgs& a, hipStream_t st) {
-    const int NT = threads_for(a.H), rpw = short_rows(a.H) ? 4 : 1;
+    const bool waves = a.H <= 512;
+    const int NT = waves ? 256 : row_threads_of(a.H), rpw = waves ? 4 : 1;
     const long long want = (a.T + rpw - 1) / rpw, most = (long long)(1024 / NT < 1 ? 1 : 1024 / NT) * device_cu_count();
     const dim3 grid((unsigned)(want < most ? want : most));
-    if (short_rows(a.H)) hipLaunchKernelGGL((k_norm<T, 4, 1>), grid, dim3(NT), 0, st, a);
+    if (waves) hipLaunchKernelGGL((k_norm<T, 4, 1>), grid, dim3(NT), 0, st, a);
     else if (a.H <= 8192) hipLaunchKernelGGL((k_norm<T, 1, 1>), grid, dim3(NT), 0, st, a);
     else hipLaunchKernelGGL((k_norm<T, 1, 2>), grid, dim3(NT), 0, st, a);
     return hipGetLastError();
 }
 
+// The gradient has two workgroups of up to 512 threads for each of 256 CUs, or one of up to 1024;
+// with few rows, fewer rows side by side first.
+struct GradShape {
+    int P, rpw, parts;
+};
+GradShape grad_shape(long long T, int H) {
+    GradShape s;
+    s.P = row_threads_of(H);
+    const int most = s.P <= 512 ? 512 : 256;
+    const long long share = (T + most - 1) / most, fit = s.P <= 512 ? 512 / s.P : 1;
+    s.rpw = (int)(share < 1 ? 1 : share < fit ? share : fit);
+    const long long want = (T + s.rpw - 1) / s.rpw;
+    s.parts = (int)(want < most ? want : most);
+    return s;
+}
+
 template <typename T>
 hipError_t go_grad(const NormGradArgs& g, hipStream_t st) {
-    const dim3 grid((unsigned)norm_grad_parts(g.f.T, g.f.H));
-    const int H = g.f.H, NT = threads_for(H);
-    if (short_rows(H)) hipLaunchKernelGGL((k_norm_grad<T, 4, 1, true>), grid, dim3(NT), 0, st, g);
-    else if (H <= 8192) hipLaunchKernelGGL((k_norm_grad<T, 1, 1, true>), grid, dim3(NT), 0, st, g);
-    else hipLaunchKernelGGL((k_norm_grad<T, 1, 2, false>), grid, dim3(NT), 0, st, g);
+    const GradShape s = grad_shape(g.f.T, g.f.H);
+    const dim3 grid((unsigned)s.parts), threads((unsigned)(s.P * s.rpw));
+    if (g.f.H <= 8192) {
+        hipLaunchKernelGGL((k_norm_grad<T, 1>), grid, threads, (size_t)s.P * 8 * 4, st, g, s.P, s.rpw);
+    } else {
+        const size_t lds = (size_t)s.P * 2 * 8 * 4 * 2;
+        const hipError_t e = allow_lds<k_norm_grad<T, 2>>(2 * kMaxRow * sizeof(float));
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((k_norm_grad<T, 2>), grid, threads, lds, st, g, s.P, s.rpw);
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 
-// As many workgroups as 256 CUs hold at 1024 threads each, or as there are rows.
-int norm_grad_parts(long long T, int H) {
-    const int NT = threads_for(H), rpw = short_rows(H) ? 4 : 1, most = 256 * (1024 / NT < 1 ? 1 : 1024 / NT);
-    const long long want = (T + rpw - 1) / rpw;
-    return (int)(want < most ? want : most);
-}
+int norm_grad_parts(long long T, int H) { return grad_shape(T, H).parts; }
 
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t st) {
     return dtype == MOE_F32 ? go<float>(a, st) : go<bf16_t>(a, st);

@@ -54,13 +54,14 @@ def _args(x, z, w_post, gate, scale, w_next, eps):
         _dims(z, 2, "z")
         if z.dtype != x.dtype or z.shape != x.shape:
             raise ValueError(f"z must be {x.dtype} of shape {tuple(x.shape)}, got {z.dtype} {tuple(z.shape)}")
-        ldz = _row_stride(z, "z")
+        if not z.is_contiguous():
+            ldz = _row_stride(z, "z")
     if w_post is not None:
         _given(w_post, "w_post", torch.float32, (H,), dev)
     if w_next is not None:
         _given(w_next, "w_next", torch.float32, (H,), dev)
     kind = _gate_kind(gate, T, H, dev)
-    ldx = _row_stride(x, "x")
+    ldx = H if x.is_contiguous() else _row_stride(x, "x")
     if z is not None and z.get_device() != dev:
         _on(z, "z", dev)
     s, ws = _shape(T, ldx, ldz, H, code, kind, scale, eps)

@@ -154,7 +154,7 @@ def test_norm_pointers(lib):
     assert fwd(zz=None, y=None) == 1 and fwd(zz=None, w1=None, g=None, gate=0) == 1
     assert fwd(zz=None, w1=None, g=None, y=None, w2=None, u=None, gate=0) == 1
     n = ctypes.c_size_t(0)
-    assert lib.moe_residual_norm_grad_workspace(_norm(), ctypes.byref(n)) == 0 and n.value == 8 // 4 * 3 * 64 * 4
+    assert lib.moe_residual_norm_grad_workspace(_norm(), ctypes.byref(n)) == 0 and n.value == 8 * 3 * 64 * 4
     assert lib.moe_residual_norm_grad_workspace(_norm(T=0), ctypes.byref(n)) == 0 and n.value == 0
     assert lib.moe_residual_norm_grad_workspace(_norm(H=60), ctypes.byref(n)) == 2
     assert lib.moe_residual_norm_grad_workspace(None, ctypes.byref(n)) == 1
@@ -168,7 +168,7 @@ def test_norm_pointers(lib):
         assert grad(**{name: MIS}) == 4, name
         if name != "dy":
             assert grad(**{name: None}) == 1, name
-    assert grad(size=8 // 4 * 3 * 64 * 4 - 1) == 5
+    assert grad(size=8 * 3 * 64 * 4 - 1) == 5
 
 
 def _mm(**kw):
