@@ -52,23 +52,42 @@ constexpr Cost kRows32[FORMS] = {{}, {}, {1.05, .52, .10}, {3.95, .545, .45}, {2
 constexpr Cost kDw32[FORMS] = {{}, {}, {1.5, .68, .30}, {2.95, .44, .57}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
-// gated tiles: columns of h
-constexpr Shape kGatedShape[FORMS] = {{256, 128, 1, 1, 512, 5.0e6}, {128, 64, 2, 1, 256, 5.3e6}, {64, 64, 3, 1, 256, 5.4e6},
-                                      {32, 64, 1, 4, 256, 5.6e6}, {16, 64, 1, 4, 256, 4.9e6}};
-const Shape& shape_of(int kind, int form) { return kind == MM_GATED ? kGatedShape[form] : kShape[form]; }
+// The kinds of mm_launch.h have shapes and costs of their own, fitted in the same way: to some 4000
+// calls each of 1-256 groups, 1-60000 rows, 64-8192 by 64-16384 (fp8 10000), timed in every form.
+// Over as many others the form picked is slower than the best one by 1.7% (gated), 1.3% (gated,
+// fp32), 2.9% (two-pair dx), 1.9% (fp32), 2.2% (fp8) and 0.5% (fp8, fp32 output); the best single
+// form would be 16%, 29%, 28%, 23%, 23% and 13% slower.  (A gated tile's columns are those of h.)
+struct FormCost {
+    Shape s;
+    Cost c;
+};
+constexpr FormCost kGated16[FORMS] = {{{256, 128, 1, 1, 512, 5.0e6}, {14.7, .454, .30}}, {{128, 64, 2, 1, 256, 6.5e6}, {4.31, .331, .251}},
+                                  {{64, 64, 4, 1, 256, 6.5e6}, {3.86, .126, .183}}, {{32, 64, 2, 4, 256, 5.5e6}, {5.32, .30, .516}},
+                                  {{16, 64, 1, 4, 256, 5.5e6}, {3.91, .486, .30}}};
+constexpr FormCost kGated32[FORMS] = {{}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {4.92, .425, .215}}, {{32, 64, 2, 4, 256, 6.5e6}, {4.82, .30, .97}},
+                                  {{16, 64, 1, 4, 256, 5.5e6}, {5.22, .486, .30}}};
+constexpr FormCost kTwo16[FORMS] = {{{256, 256, 1, 1, 512, 4.5e6}, {7.89, .486, .30}}, {{128, 128, 2, 1, 256, 5.5e6}, {4.42, .0464, .236}},
+                                {{64, 64, 4, 1, 256, 6.0e6}, {3.45, .104, .0948}}, {{32, 64, 2, 4, 256, 6.0e6}, {3.36, .293, .297}},
+                                {{16, 64, 1, 8, 512, 4.5e6}, {4.19, .30, .30}}};
+constexpr FormCost kTwo32[FORMS] = {{}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {2.92, .325, .153}}, {{32, 64, 2, 4, 256, 6.5e6}, {5.78, .30, .39}},
+                                {{16, 64, 1, 8, 512, 4.5e6}, {4.84, .454, .30}}};
+constexpr FormCost kFp8[FORMS] = {{{256, 256, 1, 1, 512, 4.5e6}, {8.12, .423, .30}}, {{128, 128, 2, 1, 256, 6.5e6}, {3.90, .276, .231}},
+                              {{64, 64, 3, 1, 256, 6.5e6}, {3.89, .116, .11}}, {{32, 64, 2, 4, 256, 5.5e6}, {4.93, .262, .301}},
+                              {{16, 64, 1, 8, 512, 4.5e6}, {5.18, .30, .30}}};
+constexpr FormCost kFp8F32[FORMS] = {{}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {3.57, .238, .147}}, {{32, 64, 2, 4, 256, 6.5e6}, {4.68, .245, .455}},
+                                 {{16, 64, 1, 8, 512, 4.5e6}, {5.06, .30, .30}}};
 
-constexpr Cost kGated16[FORMS] = {{1.85, .38, .54}, {1.9, .38, .25}, {2.15, .24, .19}, {2.15, .40, .59}, {3.55, .60, .3}};
-constexpr Cost kGated32[FORMS] = {{}, {}, {1.05, .52, .20}, {3.95, .70, .9}, {2.15, .9, .45}};
-constexpr Cost kFp8F32[FORMS] = {{}, {}, {2.2, .21, .118}, {2.25, .25, .48}, {2.5, .69, .05}};
-
-const Cost* costs(int kind, int dtype) {
-    if (kind == MM_FP8) return kInt8;
-    if (kind == MM_FP8_F32) return kFp8F32;
-    if (kind == MM_GATED) return dtype == MOE_F32 ? kGated32 : kGated16;
-    if (kind == MM_DX_TWO) return dtype == MOE_F32 ? kRows32 : kDx16;
-    if (kind == 3) return kInt8;
-    if (dtype == MOE_F32) return kind == 2 ? kDw32 : kRows32;
-    return kind == 0 ? kY16 : kind == 1 ? kDx16 : kDw16;
+FormCost form_of(int kind, int dtype, int form) {
+    const bool f = dtype == MOE_F32;
+    switch (kind) {
+        case MM_FP8: return kFp8[form];
+        case MM_FP8_F32: return kFp8F32[form];
+        case MM_GATED: return f ? kGated32[form] : kGated16[form];
+        case MM_DX_TWO: return f ? kTwo32[form] : kTwo16[form];
+        case 3: return {kShape[form], kInt8[form]};
+    }
+    if (f) return {kShape[form], kind == 2 ? kDw32[form] : kRows32[form]};
+    return {kShape[form], kind == 0 ? kY16[form] : kind == 1 ? kDx16[form] : kDw16[form]};
 }
 
 long long blocks_of(int kind, const MmArgs& a, const Shape& s) {
@@ -78,14 +97,14 @@ long long blocks_of(int kind, const MmArgs& a, const Shape& s) {
     return ni * ((J + s.bn - 1) / s.bn);
 }
 
-// A launch holds at most 2^32 threads in a dimension.
-bool fits(int kind, const MmArgs& a, int form) {
-    return blocks_of(kind, a, shape_of(kind, form)) * shape_of(kind, form).threads < (1ll << 32);
+// Whether the form exists, and a launch (at most 2^32 threads) can hold the call's workgroups.
+bool fits(int kind, const FormCost& f, const MmArgs& a) {
+    return f.c.fixed != 0 && blocks_of(kind, a, f.s) * f.s.threads < (1ll << 32);
 }
 
-double estimate(int kind, int dtype, const MmArgs& a, int form, int cus) {
-    const Shape& s = shape_of(kind, form);
-    const Cost& c = costs(kind, dtype)[form];
+double estimate(int kind, int dtype, const MmArgs& a, const FormCost& f, int cus) {
+    const Shape& s = f.s;
+    const Cost& c = f.c;
     const bool dx = kind == 1 || kind == MM_DX_TWO;
     const int es = kind == 3 || kind == MM_FP8 || kind == MM_FP8_F32 ? 1 : dtype == MOE_F32 ? 4 : 2;
     const double E = a.E, K = a.K, N = a.N, R = std::max(a.rows, 1);
@@ -115,7 +134,7 @@ bool mm_fp8_fits(int out_dtype, const MmArgs& a) { return mm_fits(out_dtype == M
 
 bool mm_fits(int kind, int dtype, const MmArgs& a) {
     for (int f = 0; f < FORMS; ++f)
-        if (costs(kind, dtype)[f].fixed != 0 && fits(kind, a, f)) return true;
+        if (fits(kind, form_of(kind, dtype, f), a)) return true;
     return false;
 }
 
@@ -126,8 +145,9 @@ int pick(int kind, int dtype, const MmArgs& a, int cus) {
     int best = -1;
     double t_best = 0;
     for (int f = 0; f < FORMS; ++f) {
-        if (costs(kind, dtype)[f].fixed == 0 || !fits(kind, a, f)) continue;
-        const double t = estimate(kind, dtype, a, f, cus);
+        const FormCost form = form_of(kind, dtype, f);
+        if (!fits(kind, form, a)) continue;
+        const double t = estimate(kind, dtype, a, form, cus);
         if (best < 0 || t < t_best) best = f, t_best = t;
     }
     return best;

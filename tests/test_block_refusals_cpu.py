@@ -241,3 +241,17 @@ def test_form_query_names():
         assert _lib.grouped_mm_form(p, 8192, 8, 4096, 14336, cus=256) == "256x256"
         with pytest.raises(ValueError, match="rows"):
             _lib.grouped_mm_form(p, -1, 8, 4096, 14336, cus=256)
+
+
+def test_every_form_has_cases():
+    """The forms that the GPU tests name are all there are, and those cases take them."""
+    import test_fp8_gpu
+    import test_gated_gpu
+    tiles, thin, f32_forms = ["256x256", "128x128", "64x64"], ["32x64 thin", "16x64 thin"], ["64x64", "32x64 thin", "16x64 thin"]
+    want = {(t, f) for t, fs in ((bf, tiles + thin), (f32, f32_forms)) for f in fs}
+    assert {(c[1], c[0]) for c in test_fp8_gpu.FORMS} == want
+    for product in ("gated", "gated dx"):
+        assert {(c[1], c[2]) for c in test_gated_gpu.FORMS if c[0] == product} == want
+    cases = [("fp8", c[1], c[0], *c[2:]) for c in test_fp8_gpu.FORMS] + list(test_gated_gpu.FORMS)
+    for product, dtype, form, *sizes in cases:
+        assert _lib.grouped_mm_form(product, *sizes, dtype=_lib.MOE_F32 if dtype == f32 else _lib.MOE_BF16, cus=256) == form

@@ -190,14 +190,14 @@ def product_ref(xq, xs, wq, ws, off, dtype):
 
 
 # form, rows, groups, K, N: sizes that leave a remainder on every side, groups without rows and of one
-FORMS = [("256x256", bf, 4322, 1, 656, 2408), ("256x256", bf, 2815, 2, 400, 3152), ("256x256", bf, 3000, 3, 1168, 3152),
-         ("128x128", bf, 1609, 1, 464, 1912), ("128x128", bf, 3590, 2, 432, 1016),
-         ("64x64", bf, 799, 1, 496, 688), ("64x64", bf, 1343, 2, 400, 488), ("64x64", bf, 900, 1, 2064, 1000),
-         ("32x64 thin", bf, 2, 1, 752, 72), ("32x64 thin", bf, 10, 2, 592, 72), ("16x64 thin", bf, 2, 1, 432, 80),
-         ("16x64 thin", bf, 21, 2, 400, 72),
-         ("64x64", f32, 1609, 1, 464, 1912), ("64x64", f32, 1343, 3, 1168, 488), ("64x64", f32, 900, 1, 2064, 1000),
-         ("32x64 thin", f32, 2, 1, 752, 72), ("32x64 thin", f32, 10, 2, 592, 72), ("16x64 thin", f32, 2, 1, 432, 80),
-         ("16x64 thin", f32, 21, 2, 400, 72)]
+FORMS = [("16x64 thin", f32, 1, 1, 608, 48), ("16x64 thin", f32, 2, 2, 864, 40),
+         ("32x64 thin", f32, 2860, 1, 752, 88), ("32x64 thin", f32, 75, 5, 736, 2616),
+         ("64x64", f32, 2937, 1, 432, 72), ("64x64", f32, 5, 5, 528, 3304),
+         ("128x128", bf, 1975, 1, 432, 1160), ("128x128", bf, 634, 5, 432, 2976),
+         ("16x64 thin", bf, 1, 1, 1456, 40), ("16x64 thin", bf, 2, 2, 1440, 40),
+         ("256x256", bf, 2655, 1, 432, 3576), ("256x256", bf, 4543, 5, 432, 1888),
+         ("32x64 thin", bf, 5926, 1, 2192, 40), ("32x64 thin", bf, 6, 5, 2032, 3544),
+         ("64x64", bf, 1, 1, 816, 40), ("64x64", bf, 2, 2, 624, 40)]
 each_form = pytest.mark.parametrize("form,dtype,R,E,K,N", FORMS, ids=lambda v: {bf: "bf16", f32: "fp32"}.get(v, str(v)))
 
 

@@ -129,21 +129,22 @@ def test_gated_mm(M, counts, K, N, dtype):
 
 
 # product, type, form, rows, groups, K, N: a remainder on every side
-FORMS = [("gated", bf, "256x256", 1266, 1, 40, 3488), ("gated", bf, "256x256", 4490, 2, 40, 1128),
-         ("gated", bf, "128x128", 979, 1, 40, 1072), ("gated", bf, "128x128", 8, 5, 56, 3576),
-         ("gated", bf, "64x64", 3, 1, 40, 216), ("gated", bf, "64x64", 1, 5, 40, 72),
-         ("gated", bf, "32x64 thin", 1, 1, 72, 128), ("gated", bf, "32x64 thin", 2, 5, 104, 40),
-         ("gated", f32, "64x64", 3, 1, 40, 272), ("gated", f32, "64x64", 3, 3, 72, 40),
-         ("gated", f32, "32x64 thin", 332, 1, 184, 784), ("gated", f32, "32x64 thin", 6, 5, 504, 3104),
-         ("gated", f32, "16x64 thin", 1, 1, 392, 40), ("gated", f32, "16x64 thin", 1, 5, 104, 40),
-         ("gated dx", bf, "256x256", 5774, 1, 2200, 56), ("gated dx", bf, "256x256", 4639, 3, 1928, 40),
-         ("gated dx", bf, "128x128", 1952, 1, 1096, 40), ("gated dx", bf, "128x128", 879, 5, 2136, 40),
-         ("gated dx", bf, "64x64", 2, 1, 56, 216), ("gated dx", bf, "64x64", 5, 2, 40, 40),
-         ("gated dx", bf, "32x64 thin", 4462, 1, 40, 664), ("gated dx", bf, "32x64 thin", 7, 5, 2376, 976),
-         ("gated dx", bf, "16x64 thin", 1, 1, 40, 576), ("gated dx", bf, "16x64 thin", 1, 3, 56, 384),
-         ("gated dx", f32, "64x64", 181, 1, 1608, 48), ("gated dx", f32, "64x64", 165, 2, 1560, 40),
-         ("gated dx", f32, "32x64 thin", 554, 1, 680, 72), ("gated dx", f32, "32x64 thin", 117, 3, 1944, 64),
-         ("gated dx", f32, "16x64 thin", 1, 1, 40, 128), ("gated dx", f32, "16x64 thin", 1, 2, 40, 104)]
+FORMS = [("gated", f32, "16x64 thin", 1, 1, 312, 40), ("gated", f32, "16x64 thin", 2, 2, 232, 56),
+         ("gated", f32, "32x64 thin", 1697, 1, 232, 152), ("gated", f32, "32x64 thin", 92, 5, 208, 2216),
+         ("gated", f32, "64x64", 4596, 1, 200, 104), ("gated", f32, "64x64", 187, 5, 200, 2144),
+         ("gated", bf, "128x128", 1820, 1, 440, 608), ("gated", bf, "128x128", 270, 5, 464, 2768),
+         ("gated", bf, "16x64 thin", 1, 1, 280, 40), ("gated", bf, "16x64 thin", 2, 2, 200, 40),
+         ("gated", bf, "256x256", 1477, 1, 400, 3160), ("gated", bf, "256x256", 1963, 5, 400, 2128),
+         ("gated", bf, "32x64 thin", 2819, 1, 1208, 80), ("gated", bf, "32x64 thin", 62, 3, 1104, 3432),
+         ("gated", bf, "64x64", 4783, 1, 224, 48), ("gated", bf, "64x64", 6, 5, 1192, 2904),
+         ("gated dx", f32, "16x64 thin", 1, 1, 32, 392), ("gated dx", f32, "16x64 thin", 2, 2, 40, 264),
+         ("gated dx", f32, "32x64 thin", 337, 1, 808, 216), ("gated dx", f32, "32x64 thin", 6, 5, 2392, 968),
+         ("gated dx", f32, "64x64", 971, 1, 1160, 200), ("gated dx", f32, "64x64", 1244, 3, 880, 200),
+         ("gated dx", bf, "128x128", 3028, 1, 1136, 208), ("gated dx", bf, "128x128", 1849, 5, 1888, 208),
+         ("gated dx", bf, "16x64 thin", 1, 1, 24, 544), ("gated dx", bf, "16x64 thin", 2, 2, 24, 424),
+         ("gated dx", bf, "256x256", 5143, 1, 1784, 200), ("gated dx", bf, "256x256", 4827, 2, 1912, 200),
+         ("gated dx", bf, "32x64 thin", 1, 1, 40, 280), ("gated dx", bf, "32x64 thin", 3, 2, 24, 232),
+         ("gated dx", bf, "64x64", 3078, 1, 152, 216), ("gated dx", bf, "64x64", 199, 5, 2320, 208)]
 NAMES = {bf: "bf16", f32: "fp32"}
 each_form = pytest.mark.parametrize("product,dtype,form,R,E,K,N", FORMS,
                                     ids=lambda v: NAMES.get(v, str(v).replace(" ", "-")))
