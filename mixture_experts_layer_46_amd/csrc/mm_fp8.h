@@ -30,11 +30,11 @@ using OpF8 = Op<3, Elem::i8>;             // addresses, tiles and groups are tho
 __host__ __device__ inline int fp8_scale_bytes(int K) { return (K + 511) / 512 * 4; }      // of a row of scales
 
 // 32-index block `blk` of a step's stage as a matrix operand: lane l holds index l & 31 and
-// contraction bytes 32 (l >> 5) .. + 31.  With rows = 16, an operand of 16 indexes twice.
+// contraction bytes 32 (l >> 5) .. + 31.
 struct Reader32 {
     int rd;
-    __device__ __forceinline__ explicit Reader32(int lane, int rows = 32) {
-        const int m = lane & (rows - 1);
+    __device__ __forceinline__ explicit Reader32(int lane) {
+        const int m = lane & 31;
         rd = m * 64 + (((lane >> 5) * 2 ^ swa32(m)) << 4);
     }
     __device__ __forceinline__ i32x8_t operator()(const lds_char* stage, int blk) const {

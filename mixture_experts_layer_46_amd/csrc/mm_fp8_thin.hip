@@ -1,11 +1,10 @@
-// Grouped products of 8-bit floating-point rows and experts with few rows per group: 16 or 32
-// rows by 64 columns, the steps of the contraction dealt out to the workgroup's wavefronts (the
+// Grouped products of 8-bit floating-point rows and experts with few rows per group: 32 rows (fp32
+// output: or 16) by 64 columns, the steps of the contraction dealt out to the workgroup's wavefronts (the
 // mathematics: mm_fp8.h; the form: mm_thin.hip).
 //
 // What counts is the bytes in flight while the experts stream by, and that another workgroup's
 // fill the memory's time while one starts or ends.  A stage is one step: 64 bytes of every
-// index and one more load of the exponents, four bytes for each row and for the columns.  The
-// instruction takes 32 rows; 16 it gets twice.  (Stages of a whole block for the 16x16x128
+// index and one more load of the exponents, four bytes for each row and for the columns.  (Stages of a whole block for the 16x16x128
 // instruction leave room for one workgroup a CU: 64 experts of 2 rows, 4096 x 14336, 621 to 653 us
 // against 511.)
 #include "mm_fp8.h"
@@ -115,16 +114,17 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_fp8_thin(Fp8Args a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) *(lds_f4*)(sums + (wave * BM + 16 * i + l16) * kBN + 16 * j + 4 * lq) = acc[i][j];
     } else {
-        const Reader32 ra(lane, BM), rb(lane);
+        static_assert(BM == 32, "the instruction's rows");
+        const Reader32 rr(lane);
         f32x16_t acc[2] = {};
         for (int kt = wave; kt < KT; kt += W) {
             i32x8_t af, bf[2];
             uint32_t sx, sw;
             load_and_read<L, S>(ring + st * L::kStage, ring + nx * L::kStage, kt + (S - 1) * W, last, exps, oa, ob,
                                 [&](const lds_char* rd, lds_cu1* e) {
-                                    af = ra(rd, 0);
-                                    bf[0] = rb(rd + BM * 64, 0);
-                                    bf[1] = rb(rd + BM * 64, 1);
+                                    af = rr(rd, 0);
+                                    bf[0] = rr(rd + BM * 64, 0);
+                                    bf[1] = rr(rd + BM * 64, 1);
                                     sx = e[lane & 31];
                                     sw = e[32];
                                 });
@@ -138,13 +138,12 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_fp8_thin(Fp8Args a) {
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the last loads land before LDS is reused
         __syncthreads();
-        if ((lane & 31) < BM)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *(lds_f4*)(sums + (wave * BM + (lane & 31)) * kBN + 32 * j + 8 * q + 4 * (lane >> 5)) =
-                        f32x4_t{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+            for (int q = 0; q < 4; ++q)
+                *(lds_f4*)(sums + (wave * BM + (lane & 31)) * kBN + 32 * j + 8 * q + 4 * (lane >> 5)) =
+                    f32x4_t{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
     }
     __syncthreads();
     for (int c = tid; c < t.ni * (kBN / 8); c += W * 64) {
@@ -177,9 +176,10 @@ hipError_t go(const Fp8Args& a, hipStream_t st) {
 
 }  // namespace
 
-// 16 rows: eight wavefronts, for the fewest workgroups; 32 rows: four, and two workgroups a CU.
+// 16 rows (fp32 output): eight wavefronts, for the fewest workgroups; 32 rows: four, and two
+// workgroups a CU.
 hipError_t launch_fp8_thin(int rows, int out_dtype, const Fp8Args& a, hipStream_t st) {
-    if (rows == 16) return out_dtype == MOE_F32 ? go<16, 8, 3, float>(a, st) : go<16, 8, 3, bf16_t>(a, st);
+    if (rows == 16) return go<16, 8, 3, float>(a, st);
     return out_dtype == MOE_F32 ? go<32, 4, 3, float>(a, st) : go<32, 4, 3, bf16_t>(a, st);
 }
 

@@ -53,29 +53,37 @@ constexpr Cost kDw32[FORMS] = {{}, {}, {1.5, .68, .30}, {2.95, .44, .57}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
 // The kinds of mm_launch.h have shapes and costs of their own, fitted in the same way: to some 4000
-// calls each of 1-256 groups, 1-60000 rows, 64-8192 by 64-16384 (fp8 10000), timed in every form.
-// Over as many others the form picked is slower than the best one by 1.7% (gated), 1.3% (gated,
-// fp32), 2.9% (two-pair dx), 1.9% (fp32), 2.2% (fp8) and 0.5% (fp8, fp32 output); the best single
-// form would be 16%, 29%, 28%, 23%, 23% and 13% slower.  (A gated tile's columns are those of h.)
+// calls each of 1-256 groups, 1-60000 rows, 64-8192 by 64-16384 (fp8 9000), timed in every form,
+// with the operands of successive calls at different places, so that weights come from memory.
+// Over as many others the form picked is slower than the best one by 1.4% (gated), 1.5% (gated,
+// fp32), 3.2% (two-pair dx), 2.0% (fp32), 1.9% (fp8) and 0.5% (fp8, fp32 output); the best single
+// form would be 11%, 27%, 22%, 17%, 19% and 9% slower.  fp8 has no 16-row form with bf16 output:
+// it was the best one in 4% of the calls and its choice won nothing.  (A gated tile's columns are
+// those of h.)
 struct FormCost {
     Shape s;
     Cost c;
 };
-constexpr FormCost kGated16[FORMS] = {{{256, 128, 1, 1, 512, 5.0e6}, {14.7, .454, .30}}, {{128, 64, 2, 1, 256, 6.5e6}, {4.31, .331, .251}},
-                                  {{64, 64, 4, 1, 256, 6.5e6}, {3.86, .126, .183}}, {{32, 64, 2, 4, 256, 5.5e6}, {5.32, .30, .516}},
-                                  {{16, 64, 1, 4, 256, 5.5e6}, {3.91, .486, .30}}};
-constexpr FormCost kGated32[FORMS] = {{}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {4.92, .425, .215}}, {{32, 64, 2, 4, 256, 6.5e6}, {4.82, .30, .97}},
-                                  {{16, 64, 1, 4, 256, 5.5e6}, {5.22, .486, .30}}};
-constexpr FormCost kTwo16[FORMS] = {{{256, 256, 1, 1, 512, 4.5e6}, {7.89, .486, .30}}, {{128, 128, 2, 1, 256, 5.5e6}, {4.42, .0464, .236}},
-                                {{64, 64, 4, 1, 256, 6.0e6}, {3.45, .104, .0948}}, {{32, 64, 2, 4, 256, 6.0e6}, {3.36, .293, .297}},
-                                {{16, 64, 1, 8, 512, 4.5e6}, {4.19, .30, .30}}};
-constexpr FormCost kTwo32[FORMS] = {{}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {2.92, .325, .153}}, {{32, 64, 2, 4, 256, 6.5e6}, {5.78, .30, .39}},
-                                {{16, 64, 1, 8, 512, 4.5e6}, {4.84, .454, .30}}};
-constexpr FormCost kFp8[FORMS] = {{{256, 256, 1, 1, 512, 4.5e6}, {8.12, .423, .30}}, {{128, 128, 2, 1, 256, 6.5e6}, {3.90, .276, .231}},
-                              {{64, 64, 3, 1, 256, 6.5e6}, {3.89, .116, .11}}, {{32, 64, 2, 4, 256, 5.5e6}, {4.93, .262, .301}},
-                              {{16, 64, 1, 8, 512, 4.5e6}, {5.18, .30, .30}}};
-constexpr FormCost kFp8F32[FORMS] = {{}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {3.57, .238, .147}}, {{32, 64, 2, 4, 256, 6.5e6}, {4.68, .245, .455}},
-                                 {{16, 64, 1, 8, 512, 4.5e6}, {5.06, .30, .30}}};
+constexpr FormCost kGated16[FORMS] = {
+    {{256, 128, 1, 1, 512, 5.0e6}, {15.3, .395, .30}}, {{128, 64, 2, 1, 256, 6.5e6}, {3.93, .362, .281}},
+    {{64, 64, 4, 1, 256, 6.5e6}, {3.54, .293, .196}},  {{32, 64, 2, 4, 256, 5.5e6}, {5.38, .30, .706}},
+    {{16, 64, 1, 4, 256, 4.5e6}, {4.20, .321, .456}}};
+constexpr FormCost kGated32[FORMS] = {
+    {}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {4.10, .426, .23}}, {{32, 64, 2, 4, 256, 6.5e6}, {4.69, .775, .894}},
+    {{16, 64, 1, 4, 256, 5.0e6}, {5.07, .486, .30}}};
+constexpr FormCost kTwo16[FORMS] = {
+    {{256, 256, 1, 1, 512, 4.5e6}, {8.80, .559, .30}}, {{128, 128, 2, 1, 256, 5.0e6}, {3.61, .273, .274}},
+    {{64, 64, 4, 1, 256, 5.5e6}, {3.31, .122, .112}},  {{32, 64, 2, 4, 256, 5.5e6}, {3.21, .293, .339}},
+    {{16, 64, 1, 8, 512, 4.5e6}, {4.11, .369, .30}}};
+constexpr FormCost kTwo32[FORMS] = {
+    {}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {3.38, .233, .133}}, {{32, 64, 2, 4, 256, 6.0e6}, {3.86, .326, .51}},
+    {{16, 64, 1, 8, 512, 4.5e6}, {4.13, .559, .30}}};
+constexpr FormCost kFp8[FORMS] = {
+    {{256, 256, 1, 1, 512, 4.5e6}, {9.95, .486, .30}}, {{128, 128, 2, 1, 256, 5.0e6}, {3.81, .266, .257}},
+    {{64, 64, 3, 1, 256, 5.0e6}, {3.71, .15, .128}},   {{32, 64, 2, 4, 256, 5.0e6}, {4.57, .291, .376}}, {}};
+constexpr FormCost kFp8F32[FORMS] = {
+    {}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {3.62, .257, .156}}, {{32, 64, 2, 4, 256, 6.5e6}, {4.63, .30, .507}},
+    {{16, 64, 1, 8, 512, 4.5e6}, {5.25, .321, .30}}};
 
 FormCost form_of(int kind, int dtype, int form) {
     const bool f = dtype == MOE_F32;
@@ -177,7 +185,7 @@ hipError_t launch_mm_fp8(int out_dtype, const Fp8Args& a, hipStream_t st) {
         case MID128: return launch_fp8_mid(128, a, st);
         case MID64: return kind == MM_FP8 ? launch_fp8_mid(64, a, st) : launch_fp8_exact(a, st);
         case THIN32: return launch_fp8_thin(32, out_dtype, a, st);
-        case THIN16: return launch_fp8_thin(16, out_dtype, a, st);
+        case THIN16: return launch_fp8_thin(16, out_dtype, a, st);     // fp32 output
     }
     return hipErrorInvalidConfiguration;
 }
