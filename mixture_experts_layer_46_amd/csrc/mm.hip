@@ -111,30 +111,34 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
     typedef __attribute__((address_space(3))) u32x2_t lds_u2;
     if constexpr (O::kGated) {
         // h, then the projections where they are kept; each through LDS as whole rows
-        for (int which = 0; which < (a.ca ? 3 : 1); ++which) {
-            if (which) __syncthreads();                       // the tensor before has been read
+        auto put = [&](auto value, void* to) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (i >= nblk) break;
                 const int r = row0 + 16 * i + l16;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    f32x4_t x = which == 1 ? acc[i][j] : acc[i][2 + j];
-                    if (which == 0)
+                    f32x4_t x;
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) x[v] = gated<O::ELEM>(acc[i][j][v], acc[i][2 + j][v]);
+                    for (int v = 0; v < 4; ++v) x[v] = value(acc[i][j][v], acc[i][2 + j][v]);
                     *(lds_u2*)(lds + (r * kCS + wn * 32 + 16 * j + 4 * lq) * 2) =
                         u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
                 }
             }
             __syncthreads();
-            bf16_t* out = (bf16_t*)(which == 0 ? a.c : which == 1 ? a.ca : a.cb);
             for (int c = tid; c < t.ni * 16; c += 512) {
                 const int r = c >> 4, cc = (c & 15) * 8;
                 if (cc < t.nj)
                     __builtin_nontemporal_store(*(const __attribute__((address_space(3))) u32x4_t*)(lds + (r * kCS + cc) * 2),
-                                                reinterpret_cast<u32x4_t*>(out + (t.crow + r) * J + t.j0 + cc));
+                                                reinterpret_cast<u32x4_t*>((bf16_t*)to + (t.crow + r) * J + t.j0 + cc));
             }
+        };
+        put([](float p, float q) { return gated<O::ELEM>(p, q); }, a.c);
+        if (a.ca) {
+            __syncthreads();                                  // the tensor before has been read
+            put([](float p, float) { return p; }, a.ca);
+            __syncthreads();
+            put([](float, float q) { return q; }, a.cb);
         }
         return;
     }

@@ -4,6 +4,13 @@
 // Both kernels are shaped as those of the other grouped products: 256 x 256 tiles by two groups
 // of four wavefronts half a step apart (mm.hip), and smaller tiles by four wavefronts with
 // several workgroups a CU (mm_mid.hip).
+//
+// The large tiles run at 2600 TFLOP/s on 8192^3, where the card's library reaches 2890 with one
+// scale per tensor and a loop of nothing but this instruction 3900: matrix units are busy two
+// thirds of the time at a clock that the card's power limit holds at 1.6 to 1.8 of 2.4 GHz:
+// schedules of 765, 797 and 814 thousand cycles (loads in the matrix phase, column operands read
+// one phase early) all took 440 us.  Four wavefronts of 128 x 128, which read a third
+// less from LDS, were slower by 6 to 9%: with one wavefront per SIMD the loads' issue shows.
 #include "mm_fp8.h"
 #include "mm_large.h"
 
@@ -17,11 +24,58 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) u32x2_t lds_u2;
 typedef const __attribute__((address_space(3))) u32x4_t lds_cu4;
 
-using OpA8 = Operand<1, false, kT, kLoads, true>;
+// An operand of the large tiles, two steps at a time: lines of 128 bytes of memory, eight rows to a
+// load, so that L2 is asked for whole lines.  Steps of 64 bytes ask for each line twice, which
+// a card at its power limit pays for: 8192^3 448 -> 420 us, 8 experts, 8192 rows, 4096 x 14336 498 ->
+// 479, with half the requests.  In LDS an index keeps its 128 bytes as eight 16-byte chunks,
+// chunk q of index m at q ^ ((m >> 1) & 7): the 16 lanes that one cycle of a ds_read_b128 serves
+// (see swa4) have eight even and eight odd indexes, whose m / 2 differ modulo 8.
+struct Wide {
+    static constexpr int kLoads = 4, kBytes = kT * 128;       // loads per wavefront; bytes of a stage
+    uint64_t base;
+    uint32_t ld, n, cbytes;
+    uint32_t off[kLoads], kq;     // kq: this lane's byte within the two steps, of its even loads
+    __device__ __forceinline__ void plan(uint64_t base_, int C, int valid, int wave, int lane) {
+        base = base_;
+        ld = cbytes = (uint32_t)C;
+        n = (uint32_t)valid;
+        kq = (uint32_t)((lane & 7) ^ (lane >> 4)) * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = (wave * kLoads + i) * 8 + (lane >> 3);
+            off[i] = r < valid ? (uint32_t)r * ld + (kq ^ (i & 1) * 64) : kOOB;
+        }
+    }
+    // loads i0 .. i0 + NL - 1 of double step d
+    template <int NL>
+    __device__ __forceinline__ void load(lds_char* stage, int wave, int d, int i0) const {
+        const uint32_t k0 = min((uint32_t)d * 128, cbytes), left = cbytes - k0;
+        const __amdgpu_buffer_rsrc_t r = make_rsrc((const void*)base, n * ld);
+#pragma unroll
+        for (int i = i0; i < i0 + NL; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(stage + (wave * kLoads + i) * 1024), 16,
+                                                     (kq ^ (i & 1) * 64) < left ? off[i] : kOOB, (int)k0, 0, 0);
+    }
+};
+// 32-index block `blk` of step `s` (0, 1) of a stage as a matrix operand (see Reader32).
+struct WideReader {
+    int rd;
+    __device__ __forceinline__ explicit WideReader(int lane) {
+        const int m = lane & 31;
+        rd = m * 128 + (((lane >> 5) * 2 ^ ((m >> 1) & 7)) << 4);
+    }
+    __device__ __forceinline__ i32x8_t operator()(const lds_char* stage, int blk, int s) const {
+        typedef const __attribute__((address_space(3))) i32x4_t lds_i4;
+        const int at = rd ^ s * 64;
+        const i32x4_t lo = *(lds_i4*)(stage + blk * 4096 + at), hi = *(lds_i4*)(stage + blk * 4096 + (at ^ 16));
+        return i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+};
+constexpr int kPair = 2 * Wide::kBytes;       // bytes of a double step: the A operand, then the B operand
 
 constexpr int kCS = kT + 8;                   // bf16 per row of the output staging tile
 constexpr size_t kLds = (size_t)kT * kCS * 2; // staging tile; the stages (128 KB) and the exponents' slots lie inside
-static_assert(kStages * kStage + ExpLoads<8>::kBytes <= (int)kLds, "stages and exponents fit below the staging tile's end");
+static_assert(2 * kPair + ExpLoads<8>::kBytes <= (int)kLds, "stages and exponents fit below the staging tile's end");
 
 // The 32 x 32 block `c`: lane l holds row l & 31 and columns 8 q + 4 (l >> 5) .. + 3, q = 0 .. 3.
 __device__ __forceinline__ void put_block(const f32x16_t& c, lds_char* stage, int cs, int r, int col) {
@@ -58,43 +112,76 @@ __device__ __attribute__((always_inline)) inline void read_and_load8(const lds_c
     ob.load(wr + TA * 64, wave * (TB / 16 / W), kt);
 }
 
-__device__ __forceinline__ void wait_stage(int kt) {
-    if (((kt - 4) & 7) < 2) wait_vmcnt<kVmcnt + 1>();
-    else wait_vmcnt<kVmcnt>();
+// The steps of one of the two wavefront groups.  Between two barriers one group is in its read
+// phase (R) and the other in its matrix phase (M):
+//   group 0:  R0 | M0 | R1 | M1 | ... | M(KT-1) | (idle)
+//   group 1: (idle) | R0 | M0 | R1 | ... | R(KT-1) | M(KT-1)
+// Loads are of double steps, into two stages that take turns, between the matrix instructions: the
+// stage of the steps 2d - 2 and 2d - 1 has been read when group 1 enters M(2d-1); there it starts its
+// loads of double step d + 1, and group 0 in M(2d).  They are waited for before the barrier that
+// opens group 0's R(2d+2), by group 0 at the end of M(2d+1), by group 1 at the end of R(2d+1).
+// Exponents are loaded in M(k), k = 4 (mod 8), and read in R(k), k = 0 (mod 8).
+__device__ __attribute__((always_inline)) inline void phase_r(const lds_char* __restrict__ rd, int s, int ablk, int bblk,
+                                                              const WideReader& rr, i32x8_t (&af)[4], i32x8_t (&bf)[2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) af[i] = rr(rd, ablk + i, s);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) bf[j] = rr(rd + Wide::kBytes, bblk + j, s);
+    wait_lds();
+}
+// `wr`: the stage that loads of double step d go into (LOADS)
+template <bool LOADS>
+__device__ __attribute__((always_inline)) inline void phase_m(lds_char* __restrict__ wr, int d, int nblk, int wave, const Wide& oa,
+                                                              const Wide& ob, const Exps<4>& ex, const i32x8_t (&af)[4],
+                                                              const i32x8_t (&bf)[2], f32x16_t (&acc)[4][2]) {
+    asm volatile("" : "+s"(nblk));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (__builtin_expect(i < nblk, 1)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = mma32(bf[j], af[i], acc[i][j], ex.w, ex.x[i]);
+        }
+        if constexpr (LOADS) {
+            if (i < 2) oa.load<2>(wr, wave, d, 2 * i);
+            else ob.load<2>(wr + Wide::kBytes, wave, d, 2 * i - 4);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
-// The steps of one of the two wavefront groups; barriers and waits as in mm.hip.  An exponents'
-// load goes out between the stage loads of steps kt - 1 and kt = 4 (mod 8): there and one step
-// later it may be in flight too when the stage of step kt + 1 is waited for.
 template <int GROUP>
 __device__ __attribute__((always_inline)) inline void steps(lds_char* lds, int KT, int nblk, int ablk, int wn, int wave,
-                                                            const OpA8& oa, const OpA8& ob, const Reader32& rr,
+                                                            const Wide& oa, const Wide& ob, const WideReader& rr,
                                                             const ExpLoads<8>& el, int lane, f32x16_t (&acc)[4][2]) {
     i32x8_t af[4], bf[2];
     Exps<4> ex;
-    lds_char* slots = lds + kStages * kStage;
+    lds_char* slots = lds + 2 * kPair;
     if constexpr (GROUP == 1) lds_barrier();
-    for (int kt = 0; kt < KT; ++kt) {
-        ex.step(el, slots, kt, ablk, wn >> 1, lane);
-        if ((kt & 7) == 4) el.load(slots, wave, kt + 4);
-        read_and_load8<kT, kT, 8>(lds + (kt % kStages) * kStage, lds + ((kt + 3) % kStages) * kStage, kt + 3, ablk, wn * 2,
-                                  wave, oa, ob, rr, af, bf);
-        wait_lds();
-        if constexpr (GROUP == 1) wait_stage(kt);
-        lds_barrier();
-        asm volatile("" : "+s"(nblk));
+    for (int k0 = 0; k0 < KT; k0 += 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (__builtin_expect(i < nblk, 1)) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mma32(bf[j], af[i], acc[i][j], ex.w, ex.x[i]);
+        for (int q = 0; q < 4; ++q) {                         // stages as constants: no addresses to compute
+            const int kt = k0 + q;
+            if (kt >= KT) break;
+            ex.step(el, slots, kt, ablk, wn >> 1, lane);
+            phase_r(lds + q / 2 * kPair, q % 2, ablk, wn * 2, rr, af, bf);
+            if constexpr (GROUP == 1)
+                if (q % 2 == 1) wait_vmcnt<0>();
+            lds_barrier();
+            if (q == 0 && (kt & 7) == 4) el.load(slots, wave, kt + 4);
+            if constexpr (GROUP == 0) {
+                if (q == 0 && kt == 0) phase_m<false>(lds, 0, nblk, wave, oa, ob, ex, af, bf, acc);      // double step 1 is on its way
+                else if (q % 2 == 0) phase_m<true>(lds + (q / 2 + 1) % 2 * kPair, kt / 2 + 1, nblk, wave, oa, ob, ex, af, bf, acc);
+                else phase_m<false>(lds, 0, nblk, wave, oa, ob, ex, af, bf, acc);
+                if (q % 2 == 1) wait_vmcnt<0>();
+            } else {
+                if (q % 2 == 1) phase_m<true>(lds + q / 2 * kPair, kt / 2 + 2, nblk, wave, oa, ob, ex, af, bf, acc);
+                else phase_m<false>(lds, 0, nblk, wave, oa, ob, ex, af, bf, acc);
             }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) asm volatile("" : "+a"(acc[i][j]));
-        if constexpr (GROUP == 0) wait_stage(kt);
-        lds_barrier();
+            lds_barrier();
+        }
     }
     if constexpr (GROUP == 0) lds_barrier();
 }
@@ -110,10 +197,9 @@ __global__ __launch_bounds__(512, 1) void k_mm_fp8(Fp8Args a) {
     if (w >= count_items<O, kT, kT, bf16_t>(a.m, groups)) return;
     Tile2 t;
     tile_of_item<O, kT, kT>(a.m, groups, w, t);
-    auto oa = operand_a<O, kT, kLoads, true>(a.m, t);
-    auto ob = operand_b<O, kT, kLoads, true>(a.m, t);
-    oa.plan(wave * kLoads, lane, t.ni);
-    ob.plan(wave * kLoads, lane, t.nj);
+    Wide oa, ob;
+    oa.plan(t.abase, t.C, t.ni, wave, lane);
+    ob.plan(t.bbase, t.C, t.nj, wave, lane);
 
     // this wavefront's rows, in 32-row blocks: the tile's, split evenly over the two groups
     const int half = min(128, (t.ni + 63) / 64 * 32), row0 = uni(wm * half);
@@ -126,16 +212,16 @@ __global__ __launch_bounds__(512, 1) void k_mm_fp8(Fp8Args a) {
 
     const int KT = (t.C + 63) / 64;
     {
-        const Reader32 rr(lane);
+        const WideReader rr(lane);
         ExpLoads<8> el;
         el.plan(a, t, wave, lane);
-        el.load(lds + kStages * kStage, wave, 0);
+        el.load(lds + 2 * kPair, wave, 0);
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
-            oa.load(lds + s * kStage, wave * kLoads, s);
-            ob.load(lds + s * kStage + kT * 64, wave * kLoads, s);
+        for (int d = 0; d < 2; ++d) {
+            oa.load<4>(lds + d * kPair, wave, d, 0);
+            ob.load<4>(lds + d * kPair + Wide::kBytes, wave, d, 0);
         }
-        wait_vmcnt<kVmcnt>();
+        wait_vmcnt<2 * Wide::kLoads>();                       // double step 0
         lds_barrier();
         if (wm == 0) steps<0>(lds, KT, nblk, row0 / 32, wn, wave, oa, ob, rr, el, lane, acc);
         else steps<1>(lds, KT, nblk, row0 / 32, wn, wave, oa, ob, rr, el, lane, acc);
