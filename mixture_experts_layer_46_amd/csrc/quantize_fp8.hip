@@ -97,6 +97,36 @@ __global__ __launch_bounds__(256) void k_quantize_rows_fp8(const T* __restrict__
     }
 }
 
+// Rows of at most B = 1 or 2 blocks: 4 / B of them to a wavefront, which has two such sets in flight.
+// 60000 x 128 bf16 12.1 -> 8.3 us, the host's call.
+template <typename T, int B>
+__global__ __launch_bounds__(256) void k_quantize_short_rows_fp8(const T* __restrict__ x, long long rows, int K,
+                                                                 uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+    constexpr int C = 2, RW = 4 / B;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, blk = lane >> 4, k = blk % B * 128 + (lane & 15) * 8;
+    const long long r0 = ((long long)blockIdx.x * 4 + wave) * (C * RW) + blk / B;
+    float v[C][8];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        if (r0 + i * RW < rows && k < K) get8(x + (r0 + i * RW) * K + k, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const long long r = r0 + i * RW;
+        const uint32_t b = exponent_of(max16(max8(v[i])));
+        const bool live = r < rows;
+        if (live && k < K) *reinterpret_cast<uint2*>(q + r * K + k) = pack8(v[i], factor_of(b));
+        uint32_t pad = 127u;                                  // the second block's byte
+        if constexpr (B == 2) {
+            const uint32_t up = lane < 32 ? __builtin_amdgcn_readlane(b, 16) : __builtin_amdgcn_readlane(b, 48);
+            if (K > 128) pad = up;
+        }
+        if (live && lane % (16 * B) == 0) *reinterpret_cast<uint32_t*>(scale + r * 4) = b | pad << 8 | 0x7f7f0000u;
+    }
+}
+
 // One block of 128 x 128 of w [E, K, N] per workgroup, transposed through LDS into q [E, N, K].
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_experts_fp8(const T* __restrict__ w, int K, int N, uint8_t* __restrict__ q,
@@ -149,7 +179,11 @@ hipError_t rows(const T* x, long long n, int K, uint8_t* q, uint8_t* scale, hipS
     const int chunks = (K + 511) / 512;
 #define GO(W, C) \
     hipLaunchKernelGGL((k_quantize_rows_fp8<T, W, C>), dim3((unsigned)((n + 4 / W - 1) / (4 / W))), dim3(256), 0, st, x, n, K, q, scale)
-    if (chunks <= 1) GO(1, 1);
+    if (K <= 256) {
+        const dim3 grid((unsigned)(K <= 128 ? (n + 31) / 32 : (n + 15) / 16));
+        if (K <= 128) hipLaunchKernelGGL((k_quantize_short_rows_fp8<T, 1>), grid, dim3(256), 0, st, x, n, K, q, scale);
+        else hipLaunchKernelGGL((k_quantize_short_rows_fp8<T, 2>), grid, dim3(256), 0, st, x, n, K, q, scale);
+    } else if (chunks <= 1) GO(1, 1);
     else if (chunks <= 2) GO(1, 2);
     else if (chunks <= 4) GO(2, 2);
     else GO(4, 2);

@@ -79,7 +79,7 @@ def exps(scale):
     return scale.cpu().view(torch.uint8).to(f64) - 127
 
 
-QUANT = [(1, 16), (3, 112), (2, 128), (5, 144), (4, 512), (3, 528), (2, 1040), (7, 2048), (3, 4112), (2, 8208), (1000, 64)]
+QUANT = [(1, 16), (3, 112), (2, 128), (5, 144), (4, 512), (3, 528), (2, 1040), (7, 2048), (3, 4112), (2, 8208), (1000, 64), (33, 128), (31, 256), (130, 208), (17, 272)]
 
 
 @pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "fp32"])
