@@ -54,6 +54,8 @@ def forward_block(x, u, w_gate, experts, top_k, w_post=None, gate=None, scale=1.
         w_in, w_up, w_out = experts
         if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (u, w_gate, bias, w_in, w_up, w_out)):
             z = _layer_train(u, w_gate, w_in, w_up, w_out, top_k, bias, flags, capacity_factor)
+        elif M._check_layer(u, w_gate, bias, w_in, w_up, w_out, None, top_k)[0] == 0:
+            z = torch.empty_like(u)
         else:
             z = M.forward(u, w_gate, w_in, w_up, w_out, top_k, bias=bias, flags=flags, capacity_factor=capacity_factor)
     return residual_norm(x, z, w_post, gate, scale, w_next, eps)

@@ -42,8 +42,8 @@ def quantize_rows_fp8(x):
     code = _code(x, "x")
     R, K = x.shape
     dev = _dense(x, "x")
-    q = torch.empty((R, K), dtype=_Q, device=x.device)
-    scale = torch.empty((R, _scales(K)), dtype=_S, device=x.device)
+    q = torch.empty_like(x, dtype=_Q)                       # (the quickest of torch's calls: the host's time counts)
+    scale = x.new_empty((R, _scales(K)), dtype=_S)
     _launch(dev, "moe_quantize_rows_fp8", code, R, K, x.data_ptr(), q.data_ptr(), scale.data_ptr())
     return q, scale
 
@@ -90,7 +90,7 @@ def grouped_mm_fp8(xq, x_scale, wq, w_scale, offsets, dtype=torch.bfloat16, out=
         _apart(out, "out", xq=xq, x_scale=x_scale, wq=wq, w_scale=w_scale, offsets=offsets)
     _on(xq, "xq", None)
     if rest:
-        out = torch.empty((R, N), dtype=dtype, device=xq.device)
+        out = xq.new_empty((R, N), dtype=dtype)
     _launch(dev, "moe_grouped_mm_fp8", _mm_shape(R, E, K, N, MOE_BF16, _CODES[dtype], rest), xq.data_ptr(),
             x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
     if not rest:

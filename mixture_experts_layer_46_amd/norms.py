@@ -77,8 +77,8 @@ def _forward(x, z, w_post, gate, scale, w_next, eps, out):
     y = u = None
     if out is None:
         _on(x, "x", None)
-        y = None if z is None else x.new_empty((T, H))
-        u = None if w_next is None else x.new_empty((T, H))
+        y = None if z is None else torch.empty_like(z)
+        u = None if w_next is None else torch.empty_like(x)
     else:
         y, u = out
         for o, name, wanted in ((y, "y", z is not None), (u, "u", w_next is not None)):
@@ -105,10 +105,10 @@ def _backward(dy, du, x, z, w_post, gate, scale, w_next, eps):
     elif du is not None:
         raise ValueError("du needs w_next")
     _on(x, "x", None)
-    dx = x.new_empty((T, H))
-    dz = None if z is None else x.new_empty((T, H))
+    dx = torch.empty_like(x)
+    dz = None if z is None else torch.empty_like(z)
     dw_post, dgate, dw_next = (None if t is None else torch.empty_like(t) for t in (w_post, gate, w_next))
-    part = torch.empty(ws // 4, dtype=torch.float32, device=x.device)
+    part = x.new_empty(ws // 4, dtype=torch.float32)
     _launch(dev, "moe_residual_norm_grad", s, _ptr(dy), _ptr(du), x.data_ptr(), _ptr(z), _ptr(w_post), _ptr(gate),
             _ptr(w_next), dx.data_ptr(), _ptr(dz), _ptr(dw_post), _ptr(dgate), _ptr(dw_next), part.data_ptr(), ws)
     return dx, dz, dw_post, dgate, dw_next

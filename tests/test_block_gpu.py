@@ -138,9 +138,12 @@ def test_captured_training_block(M):
             assert torch.equal(a, b)
 
 
-def test_no_tokens_served(M):
+@pytest.mark.parametrize("kind", ["full", "int8", "fp8"])
+def test_no_tokens_served(M, kind):
     p = {n: None if t is None else t.cuda() for n, t in block(64, 4, 96, bf, True, "channel", 0, 6).items()}
     x = torch.zeros(0, 64, dtype=bf, device="cuda")
-    ex = M.quantize_ffn_fp8(p["w_in"], p["w_up"], p["w_out"])
+    ex = (p["w_in"], p["w_up"], p["w_out"])
+    if kind != "full":
+        ex = (M.quantize_ffn if kind == "int8" else M.quantize_ffn_fp8)(*ex)
     y, u = M.forward_block(x, x, p["w_gate"], ex, 2, p["w_post"], p["gate"], 1.0, p["w_next"])
     assert y.shape == u.shape == (0, 64)
