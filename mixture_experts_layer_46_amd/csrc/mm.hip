@@ -110,7 +110,8 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
     typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
     typedef __attribute__((address_space(3))) u32x2_t lds_u2;
     if constexpr (O::kGated) {
-        // h, then the projections where they are kept; each through LDS as whole rows
+        // h, then the projections where they are kept; each through LDS as whole rows.  (Three
+        // copies of the code: a loop over the three keeps the sums in scratch memory.)
         auto put = [&](auto value, void* to) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

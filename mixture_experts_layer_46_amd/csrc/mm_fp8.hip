@@ -1,9 +1,10 @@
 // Grouped products of 8-bit floating-point rows and experts, tiles of 256, 128 and 64 (the
 // mathematics and the operands: mm_fp8.h).
 //
-// Both kernels are shaped as those of the other grouped products: 256 x 256 tiles by two groups
+// The kernels are shaped as those of the other grouped products: 256 x 256 tiles by two groups
 // of four wavefronts half a step apart (mm.hip), and smaller tiles by four wavefronts with
-// several workgroups a CU (mm_mid.hip).
+// several workgroups a CU (mm_mid.hip).  Of the smaller ones, 1 expert of 512 rows of 4096 x 4096
+// takes 19 us (917 TFLOP/s), 64 experts of 256 rows of 2048 x 1408 68 us (1390).
 //
 // The large tiles run at 2600 TFLOP/s on 8192^3, where the card's library reaches 2890 with one
 // scale per tensor and a loop of nothing but this instruction 3900: matrix units are busy two
@@ -27,9 +28,10 @@ typedef const __attribute__((address_space(3))) u32x4_t lds_cu4;
 // An operand of the large tiles, two steps at a time: lines of 128 bytes of memory, eight rows to a
 // load, so that L2 is asked for whole lines.  Steps of 64 bytes ask for each line twice, which
 // a card at its power limit pays for: 8192^3 448 -> 420 us, 8 experts, 8192 rows, 4096 x 14336 498 ->
-// 479, with half the requests.  In LDS an index keeps its 128 bytes as eight 16-byte chunks,
-// chunk q of index m at q ^ ((m >> 1) & 7): the 16 lanes that one cycle of a ds_read_b128 serves
-// (see swa4) have eight even and eight odd indexes, whose m / 2 differ modulo 8.
+// 479, with half the requests.  (bf16 tiles in this way were 10% slower.)  In LDS an index keeps
+// its 128 bytes as eight 16-byte chunks, chunk q of index m at q ^ ((m >> 1) & 7): the 16 lanes that
+// one cycle of a ds_read_b128 serves (see swa4) have eight even and eight odd indexes, whose m / 2
+// differ modulo 8.
 struct Wide {
     static constexpr int kLoads = 4, kBytes = kT * 128;       // loads per wavefront; bytes of a stage
     uint64_t base;
@@ -330,7 +332,9 @@ __global__ __launch_bounds__(256, 2) void k_mm_fp8_mid(Fp8Args a) {
 #endif
 }
 
-// fp32 output: tiles of 64 x 64, a block of 128 (two steps) a stage, with exact operands.
+// fp32 output: tiles of 64 x 64, a block of 128 (two steps) a stage, with exact operands (mm_fp8.h).
+// The conversions and a block's scaling are vector instructions beside the matrix ones: 8192^3
+// 1517 us, 725 TFLOP/s, half of a bf16 product's rate.
 struct Exact8 {
     static constexpr int B = 64, S = 3, kSub = 2 * B * 64, kStage = 2 * kSub;
     static constexpr size_t kLds = (size_t)S * kStage + ExpLoads<4>::kBytes;

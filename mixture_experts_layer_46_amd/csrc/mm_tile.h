@@ -14,6 +14,11 @@
 //   kind 1, two      dx[r, k] = sum_f da[r, f] w_in[e, k, f] + db[r, f] w_up[e, k, f]: one contraction, whose
 //                    steps run through the first pair of operands, then through the second
 //
+// The first reads x once for both projections and writes neither where no gradient is to follow;
+// the second adds in fp32 what two products would round and add again.  64 experts, 16384 rows,
+// 2048 x 1408, bf16: h 209 us (two products and the activation 293), dx 190 (two products and their
+// sum 254); 8192^3 1607 us, 1370 TFLOP/s (1578), and dx 1626 (1695).
+//
 // All are C[i, j] = sum_c A[i, c] B[c, j] on tiles of C, in steps of the contraction that
 // take 64 bytes of each index (32 bf16, 64 int8, 16 fp32).  An operand lies in memory in
 // one of two layouts:

@@ -10,6 +10,9 @@
 // with an infinity or a NaN gets the byte 255, which the product's instruction takes for NaN,
 // and q 0.  A row of scales is padded to a multiple of 4 bytes (so that a product reads four at
 // once); padding is 127 (a scale of 1).
+//
+// Memory bounds both kernels.  Rows: 65536 x 7168 bf16 248 us (5.7 TB/s), 8192 x 4096 bf16 20 us
+// (5.0).  Experts, which the weights' layout asks to be transposed: 64 of 4096 x 1408 210 us (5.3).
 #include "common.h"
 #include "launch.h"
 #include "mm_fp8.h"
@@ -98,7 +101,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows_fp8(const T* __restrict__
 }
 
 // Rows of at most B = 1 or 2 blocks: 4 / B of them to a wavefront, which has two such sets in flight.
-// 60000 x 128 bf16 12.1 -> 8.3 us, the host's call.
+// 100000 x 256 bf16 15 us (5.2 TB/s; a row to a wavefront 22), 60000 x 128 bf16 8 us, the host's call.
 template <typename T, int B>
 __global__ __launch_bounds__(256) void k_quantize_short_rows_fp8(const T* __restrict__ x, long long rows, int K,
                                                                  uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
@@ -127,7 +130,8 @@ __global__ __launch_bounds__(256) void k_quantize_short_rows_fp8(const T* __rest
     }
 }
 
-// One block of 128 x 128 of w [E, K, N] per workgroup, transposed through LDS into q [E, N, K].
+// One block of 128 x 128 of w [E, K, N] per workgroup, read once, transposed through LDS into
+// q [E, N, K] as whole lines.
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_experts_fp8(const T* __restrict__ w, int K, int N, uint8_t* __restrict__ q,
                                                               uint8_t* __restrict__ scale) {
