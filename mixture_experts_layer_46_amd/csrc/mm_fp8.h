@@ -57,38 +57,56 @@ __device__ __forceinline__ void open16(u32x4_t q, bf16x8_t& lo, bf16x8_t& hi) {
     lo = bf16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
     hi = bf16x8_t{p[4][0], p[4][1], p[5][0], p[5][1], p[6][0], p[6][1], p[7][0], p[7][1]};
 }
-// Sums in fp32 of U steps of 64 bytes within a block, of FM x FN pairs, scaled: sx, sw are the
-// exponents (biased) of each row block and of the columns.  Lane l gets row l & 15 and columns
-// 4 (l >> 4) .. + 3.
+// Sums in fp32 of U steps of 64 bytes within a block, of FM x FN pairs (the first `rows` of FM),
+// scaled: sx, sw are the exponents (biased) of each row block and of the columns.  Lane l gets row
+// l & 15 and columns 4 (l >> 4) .. + 3.  A block's sum meets the others in one fused multiply-add
+// with its scale; scales outside fp32's range are applied in two steps.
 template <int U, int FM, int FN>
 __device__ __forceinline__ void block_f32(const u32x4_t (&a)[U][FM], const u32x4_t (&b)[U][FN], const uint32_t (&sx)[FM],
-                                          uint32_t sw, f32x4_t (&acc)[FM][FN]) {
+                                          uint32_t sw, int rows, f32x4_t (&acc)[FM][FN]) {
     f32x4_t part[FM][FN];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        bf16x8_t a0[FM], a1[FM];
+        bf16x8_t b0[FN], b1[FN];
 #pragma unroll
-        for (int i = 0; i < FM; ++i) open16(a[u][i], a0[i], a1[i]);
+        for (int j = 0; j < FN; ++j) open16(b[u][j], b0[j], b1[j]);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            bf16x8_t b0, b1;
-            open16(b[u][j], b0, b1);
+        for (int i = 0; i < FM; ++i)
+            if (i < rows) {
+                bf16x8_t a0, a1;
+                open16(a[u][i], a0, a1);
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0, a0[i], u ? part[i][j] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-                part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1, a1[i], part[i][j], 0, 0, 0);
+                for (int j = 0; j < FN; ++j)
+                    part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[j], a0, u ? part[i][j] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j], a1, part[i][j], 0, 0, 0);
             }
-        }
     }
+    float f[FM];
+    int far[FM], any = 0;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const bool bad = sx[i] == 255u || sw == 255u;
-        const int e = (int)(sx[i] + sw) - 254;
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[i][j][v] += bad ? __uint_as_float(0x7fc00000u) : __builtin_amdgcn_ldexpf(part[i][j][v], e);
+        const int e = (int)(sx[i] + sw) - 254, e1 = min(max(e, -126), 127);
+        f[i] = sx[i] == 255u || sw == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e1 + 127) << 23);
+        far[i] = e - e1;
+        any |= far[i];
     }
+    if (__builtin_expect(__any(any), 0)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) part[i][j][v] = __builtin_amdgcn_ldexpf(part[i][j][v], far[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        if (i < rows) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(part[i][j][v], f[i], acc[i][j][v]);
+        }
 }
 
 // sums += a b, 32 x 32; sa, sb: the exponents (biased by 127) in the lowest byte

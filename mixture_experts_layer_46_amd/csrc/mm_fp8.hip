@@ -332,30 +332,36 @@ __global__ __launch_bounds__(256, 2) void k_mm_fp8_mid(Fp8Args a) {
 #endif
 }
 
-// fp32 output: tiles of 64 x 64, a block of 128 (two steps) a stage, with exact operands (mm_fp8.h).
-// The conversions and a block's scaling are vector instructions beside the matrix ones: 8192^3
-// 1517 us, 725 TFLOP/s, half of a bf16 product's rate.
+// fp32 output: tiles of B x B, a block of 128 (two steps) a stage, with exact operands (mm_fp8.h).
+// Opening an operand (8 conversions for 16 indexes and 64 contraction bytes) and adding a block's
+// scaled sums are vector instructions beside the matrix ones, and bound it: the wider a
+// wavefront's share, the fewer.  8192^3: 64 1423 us (773 TFLOP/s), 128 986 (1115), in which a
+// wavefront opens 8 operands for 32 matrix instructions, not 4 for 8.
+template <int B, int S>
 struct Exact8 {
-    static constexpr int B = 64, S = 3, kSub = 2 * B * 64, kStage = 2 * kSub;
+    static constexpr int F = B / 32, NL = B / 64;             // 16-index blocks of a wavefront; loads per operand and step
+    static constexpr int kSub = 2 * B * 64, kStage = 2 * kSub;
     static constexpr size_t kLds = (size_t)S * kStage + ExpLoads<4>::kBytes;
 };
 
+template <int B, int F>
 __device__ __attribute__((always_inline)) inline void read_and_load_exact(const lds_char* __restrict__ rd,
                                                                           lds_char* __restrict__ wr, int kt, int ablk, int bblk,
-                                                                          int wave, const Operand<1, false, 64, 1>& oa,
-                                                                          const Operand<1, false, 64, 1>& ob,
-                                                                          const Reader<1, false, 64>& rr, u32x4_t (&af)[2],
-                                                                          u32x4_t (&bf)[2]) {
-    read_stage<64>(rd, ablk, bblk, rr, rr, af, bf);
+                                                                          int wave, const Operand<1, false, B, B / 64>& oa,
+                                                                          const Operand<1, false, B, B / 64>& ob,
+                                                                          const Reader<1, false, B>& rr, u32x4_t (&af)[F],
+                                                                          u32x4_t (&bf)[F]) {
+    read_stage<B>(rd, ablk, bblk, rr, rr, af, bf);
     __builtin_amdgcn_sched_barrier(0);
-    oa.load(wr, wave, kt);
-    ob.load(wr + 64 * 64, wave, kt);
+    oa.load(wr, wave * (B / 64), kt);
+    ob.load(wr + B * 64, wave * (B / 64), kt);
 }
 
+template <int B, int S>
 __global__ __launch_bounds__(256, 2) void k_mm_fp8_exact(Fp8Args a) {
 #ifdef __HIP_DEVICE_COMPILE__          // the host pass needs the signature only
-    using L = Exact8;
-    constexpr int B = L::B, S = L::S;
+    using L = Exact8<B, S>;
+    constexpr int F = L::F;
     extern __shared__ uint4 smem[];
     __shared__ Groups groups;
     lds_char* lds = (lds_char*)smem;
@@ -365,16 +371,20 @@ __global__ __launch_bounds__(256, 2) void k_mm_fp8_exact(Fp8Args a) {
     if (w >= count_items<O, B, B, float>(a.m, groups)) return;
     Tile2 t;
     tile_of_item<O, B, B>(a.m, groups, w, t);
-    auto oa = operand_a<O, B, 1>(a.m, t);
-    auto ob = operand_b<O, B, 1>(a.m, t);
-    oa.plan(wave, lane, t.ni);
-    ob.plan(wave, lane, t.nj);
+    auto oa = operand_a<O, B, L::NL>(a.m, t);
+    auto ob = operand_b<O, B, L::NL>(a.m, t);
+    oa.plan(wave * L::NL, lane, t.ni);
+    ob.plan(wave * L::NL, lane, t.nj);
     const Reader<1, false, B> rr(lane);
-    f32x4_t acc[2][2];
+
+    // rows split evenly over the two wavefront rows, in 16-row blocks
+    const int half = min(B / 2, (t.ni + 31) / 32 * 16), row0 = uni(wm * half);
+    const int nblk = uni(max(0, min(half, t.ni - row0) + 15) / 16);
+    f32x4_t acc[F][F];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < F; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     const int KT = (t.C + 63) / 64;
     ExpLoads<4> el;
@@ -383,45 +393,52 @@ __global__ __launch_bounds__(256, 2) void k_mm_fp8_exact(Fp8Args a) {
     el.load(slots, wave, 0);
 #pragma unroll
     for (int q = 0; q < (S - 1) * 2; ++q) {
-        oa.load(lds + q * L::kSub, wave, q);
-        ob.load(lds + q * L::kSub + B * 64, wave, q);
+        oa.load(lds + q * L::kSub, wave * L::NL, q);
+        ob.load(lds + q * L::kSub + B * 64, wave * L::NL, q);
     }
-    uint32_t ex[2] = {}, ew = 0;
+    uint32_t ex[F] = {}, ew = 0;
     for (int kt = 0; kt < KT;) {
 #pragma unroll
         for (int st = 0; st < S; ++st) {
             if (kt >= KT) break;
-            wait_vmcnt<(S - 2) * 2 * 2>();
+            wait_vmcnt<(S - 2) * 2 * 2 * L::NL>();
             lds_barrier();
             if ((kt & 7) == 4) el.load(slots, wave, kt + 4);
-            u32x4_t af[2][2], bf[2][2];
+            u32x4_t af[2][F], bf[2][F];
             const int nx = (st + S - 1) % S;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-                read_and_load_exact(lds + st * L::kStage + u * L::kSub, lds + nx * L::kStage + u * L::kSub, kt + (S - 1) * 2 + u,
-                                    wm * 2, wn * 2, wave, oa, ob, rr, af[u], bf[u]);
+                read_and_load_exact<B>(lds + st * L::kStage + u * L::kSub, lds + nx * L::kStage + u * L::kSub,
+                                       kt + (S - 1) * 2 + u, row0 / 16, wn * F, wave, oa, ob, rr, af[u], bf[u]);
             if ((kt & 7) == 0) {
                 typedef const __attribute__((address_space(3))) uint32_t lds_cu1;
                 lds_cu1* s = (lds_cu1*)(slots + ((kt >> 3) & 1) * ExpLoads<4>::kSlot);
-                ex[0] = s[wm * 64 + (lane & 15)];
-                ex[1] = s[wm * 64 + 16 + (lane & 15)];
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    const int r = min(row0 + 16 * i, B - 16);
+                    ex[i] = s[r / 32 * 64 + r % 32 + (lane & 15)];
+                }
                 ew = s[32];
             }
             wait_lds();
             const int shift = (kt & 6) * 4;
-            const uint32_t sx[2] = {ex[0] >> shift & 255, ex[1] >> shift & 255};
-            block_f32(af, bf, sx, ew >> shift & 255, acc);
+            uint32_t sx[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) sx[i] = ex[i] >> shift & 255;
+            block_f32(af, bf, sx, ew >> shift & 255, F > 2 ? nblk : F, acc);
             kt += 2;
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // no load is left on its way to LDS
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < F; ++i) {
+        if (i >= nblk) break;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = wm * 32 + 16 * i + (lane & 15), col = wn * 32 + 16 * j + 4 * (lane >> 4);
+        for (int j = 0; j < F; ++j) {
+            const int r = row0 + 16 * i + (lane & 15), col = wn * (B / 2) + 16 * j + 4 * (lane >> 4);
             if (r < t.ni && col < t.nj) *reinterpret_cast<f32x4_t*>((float*)a.m.c + (t.crow + r) * a.m.N + t.j0 + col) = acc[i][j];
         }
+    }
 #endif
 }
 
@@ -442,6 +459,9 @@ hipError_t launch_fp8_mid(int tile, const Fp8Args& a, hipStream_t st) {
                       : go<k_mm_fp8_mid<128, 4, 1>, 128>(a, 256, Mid8<128, 4, 1>::kLds, st);
 }
 
-hipError_t launch_fp8_exact(const Fp8Args& a, hipStream_t st) { return go<k_mm_fp8_exact, 64>(a, 256, Exact8::kLds, st); }
+hipError_t launch_fp8_exact(int tile, const Fp8Args& a, hipStream_t st) {
+    return tile == 64 ? go<k_mm_fp8_exact<64, 3>, 64>(a, 256, Exact8<64, 3>::kLds, st)
+                      : go<k_mm_fp8_exact<128, 2>, 128>(a, 256, Exact8<128, 2>::kLds, st);
+}
 
 }  // namespace moe

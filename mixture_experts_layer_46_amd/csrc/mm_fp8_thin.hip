@@ -104,7 +104,7 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_fp8_thin(Fp8Args a) {
                                 });
 #pragma unroll
             for (int i = 0; i < L::NA; ++i) sx[i] = sx[i] >> shift & 255;
-            block_f32(af, bf, sx, sw >> shift & 255, acc);
+            block_f32(af, bf, sx, sw >> shift & 255, L::NA, acc);
             st = st + 1 == S ? 0 : st + 1;
             nx = nx + 1 == S ? 0 : nx + 1;
         }

@@ -84,7 +84,7 @@ const char* mm_fp8_form(int out_dtype, const MmArgs& a, int cus);
 hipError_t launch_mm_fp8(int out_dtype, const Fp8Args& a, hipStream_t st);
 hipError_t launch_fp8_large(const Fp8Args& a, hipStream_t st);                // bf16 output
 hipError_t launch_fp8_mid(int tile, const Fp8Args& a, hipStream_t st);
-hipError_t launch_fp8_exact(const Fp8Args& a, hipStream_t st);                // fp32 output, tiles of 64
+hipError_t launch_fp8_exact(int tile, const Fp8Args& a, hipStream_t st);      // fp32 output
 hipError_t launch_fp8_thin(int rows, int out_dtype, const Fp8Args& a, hipStream_t st);
 hipError_t launch_quantize_rows_fp8(const void* x, int dtype, long long rows, int K, uint8_t* q, uint8_t* scale,
                                     hipStream_t st);

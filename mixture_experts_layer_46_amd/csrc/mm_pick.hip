@@ -56,8 +56,8 @@ constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, 
 // calls each of 1-256 groups, 1-60000 rows, 64-8192 by 64-16384 (fp8 9000), timed in every form,
 // with the operands of successive calls at different places, so that weights come from memory.
 // Over as many others the form picked is slower than the best one by 1.4% (gated), 1.5% (gated,
-// fp32), 3.2% (two-pair dx), 2.0% (fp32), 1.9% (fp8) and 0.5% (fp8, fp32 output); the best single
-// form would be 11%, 27%, 22%, 17%, 19% and 9% slower.  fp8 has no 16-row form with bf16 output:
+// fp32), 3.2% (two-pair dx), 2.0% (fp32), 1.9% (fp8) and 0.9% (fp8, fp32 output); the best single
+// form would be 11%, 27%, 22%, 17%, 19% and 18% slower.  fp8 has no 16-row form with bf16 output:
 // it was the best one in 4% of the calls and its choice won nothing.  (A gated tile's columns are
 // those of h.)
 struct FormCost {
@@ -82,8 +82,8 @@ constexpr FormCost kFp8[FORMS] = {
     {{256, 256, 1, 1, 512, 4.5e6}, {9.95, .486, .30}}, {{128, 128, 2, 1, 256, 5.0e6}, {3.81, .266, .257}},
     {{64, 64, 3, 1, 256, 5.0e6}, {3.71, .15, .128}},   {{32, 64, 2, 4, 256, 5.0e6}, {4.57, .291, .376}}, {}};
 constexpr FormCost kFp8F32[FORMS] = {
-    {}, {}, {{64, 64, 2, 1, 256, 6.5e6}, {3.62, .257, .156}}, {{32, 64, 2, 4, 256, 6.5e6}, {4.63, .30, .507}},
-    {{16, 64, 1, 8, 512, 4.5e6}, {5.25, .321, .30}}};
+    {}, {{128, 128, 2, 1, 256, 6.5e6}, {3.36, .60, .269}}, {{64, 64, 4, 1, 256, 5.5e6}, {3.67, .212, .19}},
+    {{32, 64, 2, 4, 256, 6.5e6}, {5.27, .337, .392}}, {{16, 64, 1, 8, 512, 4.5e6}, {5.02, .452, .30}}};
 
 FormCost form_of(int kind, int dtype, int form) {
     const bool f = dtype == MOE_F32;
@@ -182,8 +182,8 @@ hipError_t launch_mm_fp8(int out_dtype, const Fp8Args& a, hipStream_t st) {
     const int kind = out_dtype == MOE_F32 ? MM_FP8_F32 : MM_FP8;
     switch (pick(kind, MOE_BF16, a.m, device_cu_count())) {
         case LARGE: return launch_fp8_large(a, st);
-        case MID128: return launch_fp8_mid(128, a, st);
-        case MID64: return kind == MM_FP8 ? launch_fp8_mid(64, a, st) : launch_fp8_exact(a, st);
+        case MID128: return kind == MM_FP8 ? launch_fp8_mid(128, a, st) : launch_fp8_exact(128, a, st);
+        case MID64: return kind == MM_FP8 ? launch_fp8_mid(64, a, st) : launch_fp8_exact(64, a, st);
         case THIN32: return launch_fp8_thin(32, out_dtype, a, st);
         case THIN16: return launch_fp8_thin(16, out_dtype, a, st);     // fp32 output
     }

@@ -249,7 +249,7 @@ def test_every_form_has_cases():
     import test_gated_gpu
     tiles, thin, f32_forms = ["256x256", "128x128", "64x64"], ["32x64 thin", "16x64 thin"], ["64x64", "32x64 thin", "16x64 thin"]
     want = {(t, f) for t, fs in ((bf, tiles + thin), (f32, f32_forms)) for f in fs}
-    assert {(c[1], c[0]) for c in test_fp8_gpu.FORMS} == want - {(bf, "16x64 thin")}
+    assert {(c[1], c[0]) for c in test_fp8_gpu.FORMS} == want - {(bf, "16x64 thin")} | {(f32, "128x128")}
     for product in ("gated", "gated dx"):
         assert {(c[1], c[2]) for c in test_gated_gpu.FORMS if c[0] == product} == want
     cases = [("fp8", c[1], c[0], *c[2:]) for c in test_fp8_gpu.FORMS] + list(test_gated_gpu.FORMS)

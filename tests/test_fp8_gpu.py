@@ -190,9 +190,10 @@ def product_ref(xq, xs, wq, ws, off, dtype):
 
 
 # form, rows, groups, K, N: sizes that leave a remainder on every side, groups without rows and of one
-FORMS = [("16x64 thin", f32, 1, 1, 608, 48), ("16x64 thin", f32, 2, 2, 864, 40),
-         ("32x64 thin", f32, 1638, 1, 688, 152), ("32x64 thin", f32, 66, 3, 672, 3184),
+FORMS = [("16x64 thin", f32, 1, 1, 880, 40), ("16x64 thin", f32, 2, 2, 864, 40),
+         ("32x64 thin", f32, 352, 1, 1040, 784), ("32x64 thin", f32, 2219, 5, 1232, 80),
          ("64x64", f32, 4961, 1, 496, 80), ("64x64", f32, 5, 5, 528, 3304),
+         ("128x128", f32, 2150, 1, 432, 1112), ("128x128", f32, 696, 5, 432, 2832),
          ("128x128", bf, 1975, 1, 432, 1160), ("128x128", bf, 634, 5, 432, 2976),
          ("256x256", bf, 2655, 1, 432, 3576), ("256x256", bf, 4543, 5, 432, 1888),
          ("32x64 thin", bf, 1, 1, 1456, 40), ("32x64 thin", bf, 2, 2, 1440, 40),
@@ -243,6 +244,26 @@ def test_product(M, counts, K, N, dtype):
     check(y, ref, tol, "product")
 
 
+@pytest.mark.parametrize("form,dtype,R,E,K,N", [c for c in FORMS if c[1] == f32], ids=str)
+def test_scales_of_any_size(M, form, dtype, R, E, K, N):
+    """Scales whose product lies in or out of fp32's range, each row of xq with one of its own: the
+    products of positive numbers against 64 bits, where they overflow infinite, where they are
+    subnormal off by at most the least step for each 64 products."""
+    g = torch.Generator().manual_seed(R + K)
+    xq, wq = ((torch.rand(*s, generator=g) + 0.5).to(E4) for s in ((R, K), (E, N, K)))
+    S = 4 * ((K + 511) // 512)
+    xs = torch.randint(0, 255, (R, 1), generator=g).expand(R, S).contiguous().to(torch.uint8).view(E8)
+    ws = torch.randint(0, 255, (E, (N + 127) // 128, 1), generator=g).expand(-1, -1, S).contiguous().to(torch.uint8).view(E8)
+    off, _ = groups_of(R, E)
+    y = M.grouped_mm_fp8(*(t.cuda() for t in (xq, xs, wq, ws, off)), dtype=dtype).double().cpu()
+    ref, tol = product_ref(xq, xs, wq, ws, off, dtype)
+    top = ref > torch.finfo(f32).max * 1.01
+    assert bool(torch.isinf(y[top]).all())
+    rest = ref < torch.finfo(f32).max * 0.99
+    bad = (y - ref).abs() > tol + (K + 63) // 64 * 2.0 ** -149
+    assert not bool(bad[rest].any())
+
+
 @each_form
 def test_not_finite_stays(M, form, dtype, R, E, K, N):
     """A NaN scale or value spoils its row; one of an expert its block of columns (scale) or its
@@ -265,7 +286,7 @@ def test_not_finite_stays(M, form, dtype, R, E, K, N):
 
 @pytest.mark.parametrize("off", [[5, 3, 9], [-4, 2, 100], [0, 100, 2], [9, 9, 9], [100, 100, 100], [-1, -1, -1]])
 @pytest.mark.parametrize("dtype,R,K,N", [(bf, 9, 144, 136), (f32, 9, 144, 136), (bf, 700, 464, 1912), (bf, 2815, 400, 3152),
-                                        (f32, 1343, 400, 488)], ids=str)
+                                        (f32, 1343, 400, 488), (f32, 2150, 432, 1112)], ids=str)
 def test_malformed_offsets_stay_inside(M, off, dtype, R, K, N):
     """Whatever the offsets hold, guard rows around the output keep what they held."""
     off = [v * R // 9 for v in off]
