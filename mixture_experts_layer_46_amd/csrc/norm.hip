@@ -198,15 +198,21 @@ __global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm(NormArgs a) 
 }
 
 // Rows side by side in a workgroup of `rpw` rows, P threads (whole wavefronts) each: the sums over
-// rows then leave the workgroup once for all of them.  C = 2 (rows above 8192): two of the three
-// sums over rows live in LDS and the parameters are read again for each row (from L2), since the
-// registers of 1024 threads do not hold them beside two chunks of four tensors: 4000 x 12288 bf16
-// 222 us (2.7 TB/s), with all in registers, which spill, 820.
+// rows then leave the workgroup once for all of them.  A thread has C chunks.
+//   C = 1  parameters and all sums in registers, the next row's loads ahead.
+//   C = 3  (rows above 8192, to 12288; 512 threads, for 256 registers each) two of the three sums over
+//          rows live in LDS; parameters are read again for each row, from L2, all chunks' at once
+//          and kept from one phase to the next.  4000 x 12288 bf16 184 us (3.2 TB/s), fp32 267
+//          (4.4); with the next row's loads ahead and parameters read at each use 202 and 309,
+//          with both, which spills, 334; with C = 2 223 and 397.
+//   C = 2  (longer rows; up to 1024 threads of 128 registers) as 3, but each parameter is read where
+//          it is used.  3000 x 16384 bf16 218 us (2.7 TB/s), fp32 386 (3.1); C = 4 in 512 threads
+//          spills: 229 to 383 and 435 to 458.
 template <typename T, int C>
-__global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int rpw) {
-    constexpr bool HOLD = C == 1, AHEAD = C == 1;       // the next row's loads ahead
+__global__ __launch_bounds__(C == 3 ? 512 : 1024) void k_norm_grad(NormGradArgs g, int P, int rpw) {
+    constexpr bool HOLD = C == 1, KEEP = C == 3;        // parameters through all rows; through a row's phases
     const NormArgs& a = g.f;
-    extern __shared__ float lds[];                      // sums of a row's columns: [P C 8], C = 2: twice
+    extern __shared__ float lds[];                      // sums of a row's columns: [P C 8], C > 1: twice
     __shared__ float2 red[2][16][16];                   // [slot][row][wavefront of the row]
     for (int i = threadIdx.x; i < 512; i += blockDim.x) red[i >> 8][(i >> 4) & 15][i & 15] = float2{0.f, 0.f};
     int slot = 0;
@@ -254,13 +260,6 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int r
             k.open(v);
         }
     };
-    auto weight = [&](int c, float (&v)[8]) {             // gate w_post
-        float q[8];
-        param(a.w_post, w1, c, v);
-        param(gate_c, gc, c, q);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= q[j];
-    };
     Chunk<T> xn[C], zn[C], gn[C], un[C];
     auto start = [&](long long r) {
         const bool live = r < a.T;
@@ -269,19 +268,41 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int r
         get_row<C>(dy + r * H, live && dy, P, t, H, gn);
         get_row<C>(du + r * H, live && a.w_next, P, t, H, un);
     };
-    if constexpr (AHEAD) start(first);
+    if constexpr (HOLD) start(first);
     // every row of threads runs the same number of rounds, so that the barriers match
     for (long long r0 = (long long)blockIdx.x * rpw; r0 < a.T; r0 += step) {
         const long long r = r0 + sub;
         const bool live = r < a.T;
-        if constexpr (!AHEAD) start(r);
+        if constexpr (!HOLD) start(r);
         float xv[C][8], gv[C][8];
         Chunk<T> zc[C], uc[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) xn[c].open(xv[c]), gn[c].open(gv[c]), zc[c] = zn[c], uc[c] = un[c];
         const float gt = a.gate_kind == 2 && live ? a.gate[r] : 1.f;
-        if constexpr (AHEAD) start(r + step);
+        if constexpr (HOLD) start(r + step);
         float rz = 1.f;
+        float k1[KEEP ? C : 1][8], k2[KEEP ? C : 1][8];
+        auto keep_weights = [&] {                         // w_post and gate, before each phase that needs them
+            if constexpr (KEEP)
+#pragma unroll
+                for (int c = 0; c < C; ++c) param(a.w_post, w1, c, k1[c]), param(gate_c, gc, c, k2[c]);
+        };
+        auto row_params = [&](int c, float (&p)[8], float (&q)[8]) {
+            if constexpr (KEEP) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] = k1[c][j], q[j] = k2[c][j];
+            } else {
+                param(a.w_post, w1, c, p);
+                param(gate_c, gc, c, q);
+            }
+        };
+        auto row_weight = [&](int c, float (&v)[8]) {     // gate w_post
+            float q[8];
+            row_params(c, v, q);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= q[j];
+        };
+        if (a.w_next && z) keep_weights();
         if (a.w_post) {
             float s = 0.f;
 #pragma unroll
@@ -301,16 +322,28 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int r
                 for (int c = 0; c < C; ++c) {
                     float zv[8], w[8];
                     zc[c].open(zv);
-                    weight(c, w);
+                    row_weight(c, w);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) xv[c][j] = fmaf(a.scale, xv[c][j], zv[j] * f * w[j]);
                 }
             }
+            float k3[KEEP ? C : 1][8];
+            if constexpr (KEEP)
+#pragma unroll
+                for (int c = 0; c < C; ++c) param(a.w_next, w2, c, k3[c]);
+            auto next_weight = [&](int c, float (&v)[8]) {
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = k3[c][j];
+                } else {
+                    param(a.w_next, w2, c, v);
+                }
+            };
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 float uv[8], w[8];
                 uc[c].open(uv);
-                param(a.w_next, w2, c, w);
+                next_weight(c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     sy = fmaf(xv[c][j], xv[c][j], sy);
@@ -323,7 +356,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int r
             for (int c = 0; c < C; ++c) {
                 float uv[8], w[8];
                 uc[c].open(uv);
-                param(a.w_next, w2, c, w);
+                next_weight(c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     gv[c][j] += ry * (uv[j] * w[j] - xv[c][j] * k);
@@ -340,6 +373,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int r
             if (live && col < H) Chunk<T>::put((T*)g.dx + r * H + col, o);
         }
         if (z) {
+            keep_weights();
             float k = 0.f;
             if (a.w_post || a.gate_kind == 2) {
                 float s = 0.f;
@@ -347,7 +381,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int r
                 for (int c = 0; c < C; ++c) {
                     float zv[8], w[8];
                     zc[c].open(zv);
-                    weight(c, w);
+                    row_weight(c, w);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) s = fmaf(gv[c][j] * w[j], zv[j], s);
                 }
@@ -361,8 +395,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs g, int P, int r
                 const int col = (c * P + t) * 8;
                 float o[8], zv[8], p1[8], pg[8];
                 zc[c].open(zv);
-                param(a.w_post, w1, c, pg);
-                param(gate_c, gc, c, p1);
+                row_params(c, pg, p1);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float q = gv[c][j] * (zv[j] * f);
@@ -458,8 +491,9 @@ __global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ 
     }
 }
 
-// Threads of a row: a chunk each up to 8192 columns, then two.
+// Threads of a row (forward): a chunk each up to 8192 columns, then two.
 int row_threads_of(int H) { return ((H <= 8192 ? H / 8 : (H + 15) / 16) + 63) / 64 * 64; }
+int grad_chunks_of(int H) { return H <= 8192 ? 1 : H <= 12288 ? 3 : 2; }      // (reasons: k_norm_grad)
 
 constexpr int kMaxRow = 16384;
 
@@ -476,17 +510,20 @@ hipError_t go(const NormArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// The gradient has two workgroups of up to 512 threads for each of 256 CUs, or one of up to 1024;
-// with few rows, fewer rows side by side first.  Rows side by side leave one set of partial sums for
-// all of them: 4999 x 1032 fp32 58 -> 43 us against one row a workgroup.
+// The gradient has two workgroups of up to 512 threads for each of 256 CUs, or one: of up to 1024
+// threads, or whose sums fill LDS.  With few rows, fewer rows side by side first.  Rows side by side
+// leave one set of partial sums for all of them: 4999 x 1032 fp32 58 -> 43 us against one row a
+// workgroup.
 struct GradShape {
     int P, rpw, parts;
 };
 GradShape grad_shape(long long T, int H) {
     GradShape s;
-    s.P = row_threads_of(H);
-    const int most = s.P <= 512 ? 512 : 256;
-    const long long share = (T + most - 1) / most, fit = s.P <= 512 ? 512 / s.P : 1;
+    const int C = grad_chunks_of(H);
+    s.P = (H / 8 + 64 * C - 1) / (64 * C) * 64;
+    const bool two = C == 1 && s.P <= 512;
+    const int most = two ? 512 : 256;
+    const long long share = (T + most - 1) / most, fit = two ? 512 / s.P : 1;
     s.rpw = (int)(share < 1 ? 1 : share < fit ? share : fit);
     const long long want = (T + s.rpw - 1) / s.rpw;
     s.parts = (int)(want < most ? want : most);
@@ -500,10 +537,13 @@ hipError_t go_grad(const NormGradArgs& g, hipStream_t st) {
     if (g.f.H <= 8192) {
         hipLaunchKernelGGL((k_norm_grad<T, 1>), grid, threads, (size_t)s.P * 8 * 4, st, g, s.P, s.rpw);
     } else {
-        const size_t lds = (size_t)s.P * 2 * 8 * 4 * 2;
-        const hipError_t e = allow_lds<k_norm_grad<T, 2>>(2 * kMaxRow * sizeof(float));
+        const int C = grad_chunks_of(g.f.H);
+        const size_t lds = (size_t)s.P * C * 8 * 4 * 2;
+        const hipError_t e = C == 3 ? allow_lds<k_norm_grad<T, 3>>(2 * 12288 * sizeof(float))
+                                    : allow_lds<k_norm_grad<T, 2>>(2 * kMaxRow * sizeof(float));
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((k_norm_grad<T, 2>), grid, threads, lds, st, g, s.P, s.rpw);
+        if (C == 3) hipLaunchKernelGGL((k_norm_grad<T, 3>), grid, threads, lds, st, g, s.P, s.rpw);
+        else hipLaunchKernelGGL((k_norm_grad<T, 2>), grid, threads, lds, st, g, s.P, s.rpw);
     }
     return hipGetLastError();
 }

@@ -110,7 +110,7 @@ def gpu(d):
 
 # one row; rows of one chunk; around a wavefront's, a workgroup's and two chunks' lengths; more rows
 # than workgroups; odd counts
-SIZES = [(1, 8), (3, 64), (9, 504), (5, 512), (4, 520), (7, 1032), (2, 4096), (3, 8192), (2, 8200), (1, 16384), (2100, 256),
+SIZES = [(1, 8), (3, 64), (9, 504), (5, 512), (4, 520), (7, 1032), (2, 4096), (3, 8192), (2, 8200), (1, 16384), (260, 12288), (259, 12296), (3, 10240), (2100, 256),
          (1300, 1048), (1030, 520)]
 
 
