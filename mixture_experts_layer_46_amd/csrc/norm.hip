@@ -19,7 +19,7 @@
 // fixed order, without atomics.
 //
 // Measured (bytes read and written once; a large copy moves 4.9 TB/s): forward 8192 x 4096 bf16
-// 43 us (6.2 TB/s), 8192 x 7168 fp32 181 us (5.2), 32768 x 512 bf16 26 us (5.1); gradient
+// 51 us (5.2 TB/s), 8192 x 7168 fp32 181 us (5.2), 32768 x 512 bf16 26 us (5.1); gradient
 // 8192 x 7168 bf16 149 us (4.7), 8192 x 4096 fp32 173 us (4.7), 4999 x 1032 fp32 43 us (2.9: 129
 // of a row's 192 threads have columns, and the second kernel is 5 us of it).
 #include "common.h"
