@@ -3,7 +3,7 @@
  * the layer and serving it with 8-bit experts need.
  *
  *   grouped products   y = x W_e over ragged row groups, and both gradients
- *   gated products     h = SiLU(x W_in) * (x W_up) in one kernel, and the gradient by x
+ *   gated products     h = SiLU(x W_in) * (x W_up) in one kernel, and its products' gradients
  *   8-bit integers     per-token and per-channel quantisation, and the grouped product
  *   8-bit floats       quantisation with a scale for each block of 128, and the grouped product
  *   dropout            counter-based, its mask never stored; alone or with the experts'
@@ -89,10 +89,15 @@ moe_status moe_gated_mm(const moe_mm_shape* shape, const void* x, const void* w_
 
 /* The gradient of its two projections by x, in one product: dx[r] = da[r] W_in_e^T + db[r] W_up_e^T.
  *   da, db [rows, N], w_in and w_up [E, K, N], dx [rows, K] out.  (da and db are those of
- *   moe_gated_act_grad with the kept a and b; the matrices' gradients moe_grouped_mm_dw of x with
- *   each.) */
+ *   moe_gated_act_grad with the kept a and b.) */
 moe_status moe_gated_mm_dx(const moe_mm_shape* shape, const void* da, const void* db, const void* w_in, const void* w_up,
                            const int32_t* offsets, void* dx, hipStream_t stream);
+
+/* The matrices' gradients in one launch: dw_in[e] = x_e^T da_e, dw_up[e] = x_e^T db_e, each as
+ * moe_grouped_mm_dw has it (shape's out_dtype and empty groups too).
+ *   x [rows, K], da, db [rows, N], dw_in and dw_up [E, K, N] out. */
+moe_status moe_gated_mm_dw(const moe_mm_shape* shape, const void* x, const void* da, const void* db, const int32_t* offsets,
+                           void* dw_in, void* dw_up, hipStream_t stream);
 
 /* The kernel forms that they take (see moe_grouped_mm_form); dx: that of moe_gated_mm_dx. */
 const char* moe_gated_mm_form(const moe_mm_shape* shape, int32_t dx, int32_t cus);

@@ -31,7 +31,7 @@ EXPORTS = ["moe_workspace_size", "moe_workspace_layout", "moe_capacity_rows", "m
            "moe_gated_act_grad", "moe_combine_grad",
            "moe_quantize_rows_fp8", "moe_quantize_experts_fp8", "moe_grouped_mm_fp8",
            "moe_grouped_mm_fp8_form",
-           "moe_gated_mm", "moe_gated_mm_dx", "moe_gated_mm_form",
+           "moe_gated_mm", "moe_gated_mm_dx", "moe_gated_mm_dw", "moe_gated_mm_form",
            "moe_residual_norm", "moe_residual_norm_grad_workspace", "moe_residual_norm_grad"]
 
 MOE_MM_ZERO_REST = 0x1
@@ -123,6 +123,7 @@ def load(path: str = LIB_PATH):
         "moe_grouped_mm_fp8": [mp, vp, vp, vp, vp, i32p, vp, st],
         "moe_gated_mm": [mp, vp, vp, vp, i32p, vp, vp, vp, st],
         "moe_gated_mm_dx": [mp, vp, vp, vp, vp, i32p, vp, st],
+        "moe_gated_mm_dw": [mp, vp, vp, vp, i32p, vp, vp, st],
         "moe_residual_norm": [np, vp, vp, f32p, f32p, f32p, vp, vp, st],
         "moe_residual_norm_grad_workspace": [np, ctypes.POINTER(sz)],
         "moe_residual_norm_grad": [np, vp, vp, vp, vp, f32p, f32p, f32p, vp, vp, f32p, f32p, f32p, vp, sz, st],

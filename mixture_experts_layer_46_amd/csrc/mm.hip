@@ -68,6 +68,7 @@ __global__ __launch_bounds__(512, 1) void k_mm(MmArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), wm = wave >> 2, wn = wave & 3;
     const int l16 = lane & 15, lq = lane >> 4;
 
+    take_pair<O>(a);
     const int w = item_of_block(blockIdx.x, gridDim.x);
     constexpr int kCols = tile_cols<O>(kT);
     if (w >= count_items<O, kT, kCols, OUT>(a, groups)) return;
@@ -188,7 +189,8 @@ template <typename O, typename OUT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
     hipError_t e = allow_lds<k_mm<O, OUT>>(kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mm<O, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, kT, tile_cols<O>(kT))), dim3(512), kLds, st, a);
+    hipLaunchKernelGGL((k_mm<O, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, kT, tile_cols<O>(kT)), pair_rows<O>(a)), dim3(512),
+                       kLds, st, a);
     return hipGetLastError();
 }
 

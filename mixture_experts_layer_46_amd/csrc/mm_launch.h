@@ -16,8 +16,10 @@ struct MmArgs {
     const float *xs, *ws;         // int8: row and column scales
     int rows, E, K, N;
     int zero_rest;
-    const void *a2 = nullptr, *b2 = nullptr;      // MM_GATED: w_up; MM_DX_TWO: db and w_up
-    void *ca = nullptr, *cb = nullptr;            // MM_GATED: where the projections are kept, or NULL
+    // MM_GATED: b2 is w_up, ca and cb where the projections are kept, or NULL; MM_DX_TWO: a2 and b2 are
+    // db and w_up; kind 2: b2 a second dy, or NULL, and ca its dW
+    const void *a2 = nullptr, *b2 = nullptr;
+    void *ca = nullptr, *cb = nullptr;
 };
 
 // kinds beyond mm_tile.h's: h = SiLU(x W_in) * (x W_up), dx = da W_in^T + db W_up^T, and 8-bit

@@ -71,6 +71,7 @@ __global__ __launch_bounds__(256, 2) void k_mm_mid(MmArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, lq = lane >> 4;
 
+    take_pair<O>(a);
     Tile2 t;
     const int w = item_of_block(blockIdx.x, gridDim.x);
     if (w >= count_items<O, BM, L::kCols, OUT>(a, groups)) return;
@@ -234,7 +235,8 @@ hipError_t go(const MmArgs& a, hipStream_t st) {
     constexpr size_t lds = Mid<O, BM, BN, S, U>::kLds;
     hipError_t e = allow_lds<k_mm_mid<O, BM, BN, S, U, OUT>>(lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mm_mid<O, BM, BN, S, U, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, BM, tile_cols<O>(BN))), dim3(256), lds, st, a);
+    hipLaunchKernelGGL((k_mm_mid<O, BM, BN, S, U, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, BM, tile_cols<O>(BN)), pair_rows<O>(a)),
+                       dim3(256), lds, st, a);
     return hipGetLastError();
 }
 

@@ -118,6 +118,7 @@ __global__ __launch_bounds__(512, 1) void k_mm_stream(MmArgs a) {
     const Reader<O::ES, O::kACols, kT> ra(lane);
     const Reader<O::ES, O::kBCols, kT> rb(lane);
 
+    take_pair<O>(a);
     // this workgroup's item in round r; the last, partial round is dealt block by block
     const int total = count_items<O, kT, kT, OUT>(a, groups), G = gridDim.x;
     auto item = [&](int r) {
@@ -189,7 +190,7 @@ hipError_t go(const MmArgs& a, hipStream_t st) {
     const hipError_t e = allow_lds<k_mm_stream<OUT>>(kLds);
     if (e != hipSuccess) return e;
     const long long items = mm_blocks(a, O::KIND, kT, kT), cus = device_cu_count();
-    hipLaunchKernelGGL((k_mm_stream<OUT>), dim3((unsigned)(items < cus ? items : cus)), dim3(512), kLds, st, a);
+    hipLaunchKernelGGL((k_mm_stream<OUT>), dim3((unsigned)(items < cus ? items : cus), pair_rows<O>(a)), dim3(512), kLds, st, a);
     return hipGetLastError();
 }
 

@@ -73,6 +73,7 @@ __global__ __launch_bounds__(W * 64, 2) void k_mm_thin(MmArgs a) {
     lds_char* lds = (lds_char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), l16 = lane & 15, lq = lane >> 4;
 
+    take_pair<O>(a);
     Tile2 t;
     const int w = item_of_block(blockIdx.x, gridDim.x);
     if (w >= count_items<O, L::BM, kBN, OUT>(a, groups)) return;
@@ -169,7 +170,8 @@ hipError_t go(const MmArgs& a, hipStream_t st) {
     constexpr size_t lds = Thin<O, RB, W, S>::kLds;
     hipError_t e = allow_lds<k_mm_thin<O, RB, W, S, OUT>>(lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_mm_thin<O, RB, W, S, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, 16 * RB, kBN)), dim3(W * 64), lds, st, a);
+    hipLaunchKernelGGL((k_mm_thin<O, RB, W, S, OUT>), dim3((unsigned)mm_blocks(a, O::KIND, 16 * RB, kBN), pair_rows<O>(a)), dim3(W * 64),
+                       lds, st, a);
     return hipGetLastError();
 }
 

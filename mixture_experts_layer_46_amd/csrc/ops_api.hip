@@ -242,6 +242,23 @@ moe_status moe_gated_mm_dx(const moe_mm_shape* shape, const void* da, const void
     return run_mm(MM_DX_TWO, *shape, m, stream, "gated_mm_dx");
 }
 
+moe_status moe_gated_mm_dw(const moe_mm_shape* shape, const void* x, const void* da, const void* db, const int32_t* offsets,
+                           void* dw_in, void* dw_up, hipStream_t stream) {
+    CHECK(check_mm(shape, false, true));
+    if (shape->rows > 0) {
+        REQ(x, "x");
+        REQ(da, "da");
+        REQ(db, "db");
+    }
+    REQ(offsets, "offsets");
+    REQ(dw_in, "dw_in");
+    REQ(dw_up, "dw_up");
+    MmArgs m = mm_args(*shape, x, da, dw_in, offsets);
+    m.b2 = shape->rows > 0 ? db : offsets;    // not NULL, and not read without rows
+    m.ca = dw_up;
+    return run_mm(MOE_MM_DW, *shape, m, stream, "gated_mm_dw");
+}
+
 const char* moe_gated_mm_form(const moe_mm_shape* shape, int32_t dx, int32_t cus) {
     if (cus < 0) return fail(MOE_ERR_SHAPE, "cus = %d < 0", cus), nullptr;
     if (check_mm(shape, false, false) != MOE_OK) return nullptr;

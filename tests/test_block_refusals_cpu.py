@@ -185,6 +185,7 @@ BAD = [(dict(rows=-1), 2), (dict(E=0), 2), (dict(K=0), 2), (dict(N=-8), 2), (dic
 def test_gated_shapes(lib, kw, code):
     assert lib.moe_gated_mm(_mm(**kw), *[FAKE] * 7, None) == code
     assert lib.moe_gated_mm_dx(_mm(**kw), *[FAKE] * 6, None) == code
+    assert lib.moe_gated_mm_dw(_mm(**kw), *[FAKE] * 6, None) == code
     assert lib.moe_gated_mm_form(_mm(**kw), 0, 256) is None and lib.moe_last_error().decode() != ""
 
 
@@ -209,6 +210,9 @@ def test_null_and_alignment(lib):
     assert lib.moe_gated_mm(s, *[FAKE] * 5, FAKE, None, None) == 1 and lib.moe_gated_mm(s, *[FAKE] * 5, MIS, FAKE, None) == 4
     assert lib.moe_gated_mm(s, *[FAKE] * 5, FAKE, MIS, None) == 4
     _null_and_misaligned(lambda *a: lib.moe_gated_mm_dx(s, *a, None), [FAKE] * 6, ["da", "db", "w_in", "w_up", "offsets", "dx"])
+    _null_and_misaligned(lambda *a: lib.moe_gated_mm_dw(s, *a, None), [FAKE] * 6, ["x", "da", "db", "offsets", "dw_in", "dw_up"])
+    _null_and_misaligned(lambda *a: lib.moe_gated_mm_dw(_mm(rows=0), None, None, None, *a, None), [FAKE] * 3,
+                         ["offsets", "dw_in", "dw_up"])
     _null_and_misaligned(lambda *a: lib.moe_grouped_mm_fp8(s, *a, None), [FAKE] * 6,
                          ["xq", "x_scale", "wq", "w_scale", "offsets", "y"])
     _null_and_misaligned(lambda *a: lib.moe_quantize_rows_fp8(1, 4, 64, *a, None), [FAKE] * 3, ["x", "q", "scale"])

@@ -295,3 +295,29 @@ def test_no_rows(M):
     assert h.shape == (0, 24)
     dx, d1, d2 = M.gated_mm_grad(h, x, w, w, h, h, off)
     assert dx.shape == (0, 48) and d1.shape == d2.shape == w.shape and not bool(d1.any() or d2.any())
+
+
+# form, type, rows, groups, K, N of the two weight gradients
+DW = [("256x256 stream", bf, 600, 2, 2312, 2312), ("256x256", bf, 900, 1, 3592, 3592), ("128x128", bf, 1500, 3, 1160, 1160),
+      ("64x64", bf, 500, 3, 392, 520), ("32x64 thin", bf, 900, 5, 136, 264), ("64x64", f32, 70, 5, 72, 40),
+      ("32x64 thin", f32, 4000, 2, 72, 136)]
+
+
+@pytest.mark.parametrize("form,dtype,R,E,K,N", DW, ids=str)
+def test_both_weight_gradients(M, form, dtype, R, E, K, N):
+    """One launch for both: bit for bit those of the grouped products, empty groups and rows of no
+    group included, in x's type and (bf16) in fp32."""
+    from mixture_experts_layer_46_amd.ops import _launch, _mm_shape
+    code = M._lib.MOE_F32 if dtype == f32 else M._lib.MOE_BF16
+    assert M._lib.grouped_mm_form("dw", R, E, K, N, dtype=code, cus=256) == form
+    x, da, db = (rand((R, n), dtype, 60 + i).cuda() for i, n in enumerate((K, N, N)))
+    counts = [R // E] * E
+    if E > 2:
+        counts[1] = 0
+    off = offs(counts).cuda()
+    for out, out_code in ((dtype, code), (f32, M._lib.MOE_F32)):
+        both = [torch.full((E, K, N), 7.0, dtype=out, device="cuda") for _ in range(2)]
+        _launch(0, "moe_gated_mm_dw", _mm_shape(R, E, K, N, code, out_code, False), x.data_ptr(), da.data_ptr(), db.data_ptr(),
+                off.data_ptr(), both[0].data_ptr(), both[1].data_ptr())
+        for d, dw in zip((da, db), both):
+            assert torch.equal(dw, M.grouped_mm_dw(x, d, off, dtype=out))
