@@ -13,7 +13,7 @@ from . import _lib
 from ._lib import MOE_FLAG_NO_RENORM
 from .fp8 import Fp8Experts, forward_fp8
 from .gated import gated_mm
-from .norms import residual_norm
+from .norms import _number, residual_norm
 from .ops import QuantizedExperts, _Combine, _current, _Permute, _Route, forward_int8, gated_act, grouped_mm
 
 __all__ = ["forward_block"]
@@ -45,6 +45,7 @@ def forward_block(x, u, w_gate, experts, top_k, w_post=None, gate=None, scale=1.
     8-bit ones (quantize_ffn, quantize_ffn_fp8).  Differentiable in x, u, w_gate, bias, the
     experts' matrices (not 8-bit ones), w_post, gate and w_next."""
     import mixture_experts_layer_46_amd as M
+    scale, eps = _number(scale, "scale"), _number(eps, "eps")
     if isinstance(experts, (QuantizedExperts, Fp8Experts)):
         if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (u, w_gate, bias)):
             raise ValueError("8-bit experts have no gradient: use torch.no_grad()")

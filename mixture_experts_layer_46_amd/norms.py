@@ -72,6 +72,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _number(v, name):
+    """A number of the caller's; not a tensor, whose gradient would be lost and whose value would
+    have to be waited for."""
+    if isinstance(v, torch.Tensor):
+        raise ValueError(f"{name} must be a number, not a tensor (it has no gradient)")
+    return float(v)
+
+
 def _forward(x, z, w_post, gate, scale, w_next, eps, out):
     T, H, dev, s, _ = _args(x, z, w_post, gate, scale, w_next, eps)
     y = u = None
@@ -149,14 +157,14 @@ def norm(x, w, eps=1e-6, out=None):
     and w (without `out`)."""
     if w is None:
         raise ValueError("w is required")
-    return _run(x, None, None, None, 1.0, w, float(eps), None if out is None else (None, out))[1]
+    return _run(x, None, None, None, 1.0, w, _number(eps, "eps"), None if out is None else (None, out))[1]
 
 
 def norm_grad(du, x, w, eps=1e-6):
     """(dx, dw) of norm for the gradient du [T, H]."""
     if w is None:
         raise ValueError("w is required")
-    dx, _, _, _, dw = _backward(None, du, x, None, None, None, 1.0, w, float(eps))
+    dx, _, _, _, dw = _backward(None, du, x, None, None, None, 1.0, w, _number(eps, "eps"))
     return dx, dw
 
 
@@ -167,13 +175,13 @@ def residual_norm(x, z, w_post=None, gate=None, scale=1.0, w_next=None, eps=1e-6
 
     x, z [T, H] bf16 or fp32 (the stream and the block's output), dense along H, rows may be
     apart; w_post, w_next [H] fp32; gate fp32, [H] (a number per channel) or [T, 1] (per
-    token); scale a number.  Without w_post v = z, without gate it is 1, without w_next u is
-    None.  All in fp32, u from the unrounded y; y and u [T, H] in x's type, each rounded once.
-    H a multiple of 8, at most 16384.  `out` = (y, u): tensors to write.  Differentiable in x,
-    z, w_post, gate and w_next (without `out`)."""
+    token); scale a number, not a tensor.  Without w_post v = z, without gate it is 1, without
+    w_next u is None.  All in fp32, u from the unrounded y; y and u [T, H] in x's type, each
+    rounded once.  H a multiple of 8, at most 16384.  `out` = (y, u): tensors to write.
+    Differentiable in x, z, w_post, gate and w_next (without `out`)."""
     if z is None:
         raise ValueError("z is required")
-    return _run(x, z, w_post, gate, float(scale), w_next, float(eps), out)
+    return _run(x, z, w_post, gate, _number(scale, "scale"), w_next, _number(eps, "eps"), out)
 
 
 def residual_norm_grad(dy, du, x, z, w_post=None, gate=None, scale=1.0, w_next=None, eps=1e-6):
@@ -181,4 +189,4 @@ def residual_norm_grad(dy, du, x, z, w_post=None, gate=None, scale=1.0, w_next=N
     and du [T, H] (None without w_next); None for a parameter that is not there."""
     if z is None:
         raise ValueError("z is required")
-    return _backward(dy, du, x, z, w_post, gate, float(scale), w_next, float(eps))
+    return _backward(dy, du, x, z, w_post, gate, _number(scale, "scale"), w_next, _number(eps, "eps"))
