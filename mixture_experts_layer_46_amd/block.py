@@ -14,7 +14,8 @@ from ._lib import MOE_FLAG_NO_RENORM
 from .fp8 import Fp8Experts, forward_fp8
 from .gated import gated_mm
 from .norms import _number, residual_norm
-from .ops import QuantizedExperts, _Combine, _current, _Permute, _Route, forward_int8, gated_act, grouped_mm
+from .ops import (QuantizedExperts, _Combine, _current, _Permute, _recorded, _Route, forward_int8, gated_act,
+                  grouped_mm)
 
 __all__ = ["forward_block"]
 
@@ -47,13 +48,13 @@ def forward_block(x, u, w_gate, experts, top_k, w_post=None, gate=None, scale=1.
     import mixture_experts_layer_46_amd as M
     scale, eps = _number(scale, "scale"), _number(eps, "eps")
     if isinstance(experts, (QuantizedExperts, Fp8Experts)):
-        if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (u, w_gate, bias)):
+        if _recorded(u, w_gate, bias):
             raise ValueError("8-bit experts have no gradient: use torch.no_grad()")
         layer = forward_int8 if isinstance(experts, QuantizedExperts) else forward_fp8
         z = layer(u, w_gate, experts, top_k, bias=bias, flags=flags, capacity_factor=capacity_factor)
     else:
         w_in, w_up, w_out = experts
-        if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (u, w_gate, bias, w_in, w_up, w_out)):
+        if _recorded(u, w_gate, bias, w_in, w_up, w_out):
             z = _layer_train(u, w_gate, w_in, w_up, w_out, top_k, bias, flags, capacity_factor)
         elif M._check_layer(u, w_gate, bias, w_in, w_up, w_out, None, top_k)[0] == 0:
             z = torch.empty_like(u)

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from .ops import _apart, _code, _dense, _dims, _given, _grad, _launch, _mm_shape, _spec, _wrote
+from .ops import _apart, _code, _dense, _dims, _given, _grad, _launch, _mm_shape, _recorded, _spec, _wrote
 
 __all__ = ["gated_mm", "gated_mm_grad"]
 
@@ -67,7 +67,7 @@ def gated_mm(x, w_in, w_up, offsets, out=None):
     type, computed in fp32 and rounded once.  Rows that lie in no group are zeros, or with `out`
     given left as they were.  K and N multiples of 8.  Differentiable in x, w_in and w_up (without
     `out`); the two projections are then kept, in x's type, for the gradient."""
-    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, w_in, w_up)):
+    if _recorded(x, w_in, w_up):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is recorded")
         return _GatedMM.apply(x, w_in, w_up, offsets)

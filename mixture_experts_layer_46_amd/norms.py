@@ -16,7 +16,7 @@ import torch
 
 from . import _lib
 from ._lib import NormShape
-from .ops import _apart, _code, _dims, _given, _grad, _launch, _on, _row_stride, _wrote
+from .ops import _apart, _code, _dims, _given, _grad, _launch, _on, _recorded, _row_stride, _wrote
 
 __all__ = ["norm", "norm_grad", "residual_norm", "residual_norm_grad"]
 
@@ -142,7 +142,7 @@ class _Norm(torch.autograd.Function):
 
 
 def _run(x, z, w_post, gate, scale, w_next, eps, out):
-    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, z, w_post, gate, w_next)):
+    if _recorded(x, z, w_post, gate, w_next):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is recorded")
         return _Norm.apply(x, z, w_post, gate, scale, w_next, eps)

@@ -20,7 +20,8 @@ and the layers made of them:
 
 Work is enqueued on the current stream of the tensors' device, which need not be the
 current device.  An `out` may not overlap an input (dropout's may be its input) and counts as
-modified for autograd.  Tensors that another stream wrote or will use are the caller's to order,
+modified for autograd.  There is no forward-mode derivative: the differentiable operators refuse an
+input with a tangent.  Tensors that another stream wrote or will use are the caller's to order,
 as everywhere in torch.
 """
 from __future__ import annotations
@@ -31,6 +32,7 @@ import operator
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import (MOE_BF16, MOE_F32, MOE_FLAG_BIAS_SELECT_ONLY, MOE_FLAG_NO_RENORM, MOE_MM_ZERO_REST, DropoutSpec,
@@ -125,6 +127,20 @@ def _wrote(*outs):
             torch.autograd.graph.increment_version(t)
 
 
+def _recorded(*inputs):
+    """Whether autograd records a call with these inputs (some may be None, or no tensors yet); raises
+    where one carries a forward-mode tangent, which no operator has a derivative for."""
+    if forward_ad._current_level >= 0:
+        for t in inputs:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("an input carries a forward-mode tangent (there is no forward-mode derivative)")
+    if torch.is_grad_enabled():
+        for t in inputs:
+            if getattr(t, "requires_grad", False):
+                return True
+    return False
+
+
 def _grad(g):
     """A gradient as autograd hands it over, dense and at an address the kernels take: it may be
     any view, such as a stack's slice that starts off 16 bytes."""
@@ -216,7 +232,7 @@ def grouped_mm(x, w, offsets, out=None):
     x [R, K] and w [E, K, N] bf16 or fp32, offsets [E+1] int32 (permute's); y [R, N] in x's
     type, summed in fp32 and rounded once.  Rows that lie in no group are zeros, or with
     `out` given left as they were.  Differentiable in x and w (without `out`)."""
-    if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(w, "requires_grad", False)):
+    if _recorded(x, w):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is recorded")
         return _GroupedMM.apply(x, w, offsets)
@@ -378,7 +394,7 @@ def dropout(x, p, seed, step=0, out=None):
     x (without `out`)."""
     if not isinstance(x, torch.Tensor):
         raise ValueError("x is required")
-    if torch.is_grad_enabled() and x.requires_grad:
+    if _recorded(x):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is recorded")
         return _Dropout.apply(x, p, seed, step)
@@ -442,7 +458,7 @@ def gated_act(a, b=None, p=0.0, seed=0, step=0, out=None):
     """h = SiLU(a) * b with counter-based dropout (p, seed, step as in dropout): the experts'
     activation; b None: SiLU(a).  a, b [R, F] bf16 or fp32, dense along F, rows may be apart
     (halves of a packed tensor); h [R, F] dense.  Differentiable in a and b (without `out`)."""
-    if torch.is_grad_enabled() and (getattr(a, "requires_grad", False) or getattr(b, "requires_grad", False)):
+    if _recorded(a, b):
         if out is not None:
             raise ValueError("out cannot be given where a gradient is recorded")
         return _GatedAct.apply(a, b, p, seed, step)
@@ -681,6 +697,7 @@ def forward_train(x, w_gate, w_in, w_up, w_out, top_k, bias=None, dropout_p=0.0,
     an uncaptured pass over the same leaves still alive (delete earlier outputs first)."""
     import mixture_experts_layer_46_amd as M
     T, H, E, F = M._check_layer(x, w_gate, bias, w_in, w_up, w_out, None, top_k)
+    _recorded(x, w_gate, bias, w_in, w_up, w_out)            # (a forward-mode tangent is refused)
     if flags & MOE_FLAG_NO_RENORM:
         raise ValueError("forward_train has the gradient of renormalised gates only")
     if T == 0:

@@ -40,3 +40,48 @@ def test_scale_and_eps_are_numbers(name, call, value):
 def test_numbers_of_any_kind_pass(value):
     with pytest.raises(ValueError, match="on the GPU"):
         M.residual_norm(z(T, H), z(T, H), W, None, value, W, eps=value)
+
+
+def _dual(*shape, dtype=f32):
+    return torch.autograd.forward_ad.make_dual(z(*shape, dtype=dtype), z(*shape, dtype=dtype))
+
+
+OFF = torch.zeros(E + 1, dtype=i32)
+FP8 = M.Fp8Experts(*((torch.zeros(E, n, k, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                      torch.zeros(E, 1, 4, dtype=torch.uint8).view(torch.float8_e8m0fnu)) for n, k in ((F, H), (F, H), (H, F))))
+
+
+@pytest.mark.parametrize("call", [
+    lambda: M.norm(_dual(T, H), W), lambda: M.norm(z(T, H), _dual(H)),
+    lambda: M.residual_norm(z(T, H), _dual(T, H, dtype=bf)), lambda: M.residual_norm(z(T, H), z(T, H), W, _dual(H), 1.0, W),
+    lambda: M.residual_norm(z(T, H), z(T, H), _dual(H)), lambda: M.residual_norm(z(T, H), z(T, H), w_next=_dual(H)),
+    lambda: M.gated_mm(_dual(T, H, dtype=bf), EXPERTS[0], EXPERTS[1], OFF),
+    lambda: M.gated_mm(z(T, H), _dual(E, H, F, dtype=bf), EXPERTS[1], OFF),
+    lambda: M.gated_mm(z(T, H), EXPERTS[0], _dual(E, H, F, dtype=bf), OFF),
+    lambda: M.grouped_mm(_dual(T, H, dtype=bf), EXPERTS[0], OFF), lambda: M.grouped_mm(z(T, H), _dual(E, H, F, dtype=bf), OFF),
+    lambda: M.gated_act(_dual(T, F, dtype=bf), z(T, F)), lambda: M.gated_act(z(T, F), _dual(T, F, dtype=bf)),
+    lambda: M.dropout(_dual(T, F, dtype=bf), 0.5, 1),
+    lambda: M.forward_block(z(T, H), _dual(T, H, dtype=bf), GATE, EXPERTS, K),
+    lambda: M.forward_block(z(T, H), z(T, H), _dual(H, E), EXPERTS, K),
+    lambda: M.forward_block(z(T, H), z(T, H), GATE, (EXPERTS[0], EXPERTS[1], _dual(E, F, H, dtype=bf)), K),
+    lambda: M.forward_block(z(T, H), z(T, H), GATE, EXPERTS, K, bias=_dual(E)),
+    lambda: M.forward_block(z(T, H), _dual(T, H, dtype=bf), GATE, FP8, K),
+    lambda: M.forward_block(z(T, H), z(T, H), _dual(H, E), FP8, K),
+    lambda: M.forward_train(_dual(T, H, dtype=bf), GATE, *EXPERTS, K)])
+@pytest.mark.parametrize("recorded", [True, False])
+def test_forward_mode_tangents_are_refused(call, recorded):
+    """No operator has a forward-mode derivative: a tangent that came in would be missing from what goes
+    out, with no sign of it."""
+    with torch.autograd.forward_ad.dual_level(), torch.set_grad_enabled(recorded):
+        with pytest.raises(ValueError, match="forward-mode"):
+            call()
+        with pytest.raises(ValueError, match="on the GPU"):               # without a tangent nothing is refused
+            M.norm(z(T, H), W)
+        with pytest.raises(ValueError, match="on the GPU"):
+            M.gated_mm(z(T, H).requires_grad_(), EXPERTS[0], EXPERTS[1], OFF)
+
+
+def test_jvp_is_refused():
+    for f in (lambda t: M.norm(t, W), lambda t: M.residual_norm(t, t)[0], lambda t: M.gated_act(t, t)):
+        with pytest.raises(ValueError, match="forward-mode"):
+            torch.func.jvp(f, (z(T, H),), (z(T, H),))
