@@ -59,5 +59,6 @@ def forward_block(x, u, w_gate, experts, top_k, w_post=None, gate=None, scale=1.
         elif M._check_layer(u, w_gate, bias, w_in, w_up, w_out, None, top_k)[0] == 0:
             z = torch.empty_like(u)
         else:
-            z = M.forward(u, w_gate, w_in, w_up, w_out, top_k, bias=bias, flags=flags, capacity_factor=capacity_factor)
+            with _current(u=u, w_gate=w_gate, bias=bias, w_in=w_in, w_up=w_up, w_out=w_out):
+                z = M.forward(u, w_gate, w_in, w_up, w_out, top_k, bias=bias, flags=flags, capacity_factor=capacity_factor)
     return residual_norm(x, z, w_post, gate, scale, w_next, eps)

@@ -85,3 +85,31 @@ def test_jvp_is_refused():
     for f in (lambda t: M.norm(t, W), lambda t: M.residual_norm(t, t)[0], lambda t: M.gated_act(t, t)):
         with pytest.raises(ValueError, match="forward-mode"):
             torch.func.jvp(f, (z(T, H),), (z(T, H),))
+
+
+@pytest.mark.parametrize("T_", [T, 0])
+def test_served_block_runs_on_its_tensors_gpu(monkeypatch, T_):
+    """The layer's own stages take the current device's stream: forward_block makes the tensors' GPU the
+    current one around them (whatever kind of experts), and refuses tensors of two GPUs.  Without a second
+    GPU: the context is a mark, the layer a look at it."""
+    from contextlib import contextmanager
+
+    from mixture_experts_layer_46_amd import block
+    inside, seen = [], []
+
+    @contextmanager
+    def current(**ts):
+        inside.append({n for n, t in ts.items() if t is not None})
+        yield
+        inside.pop()
+
+    def layer(x, *args, **kw):
+        seen.append(set(inside[-1]) if inside else None)
+        return x
+
+    monkeypatch.setattr(block, "_current", current, raising=False)
+    monkeypatch.setattr(M, "forward", layer)
+    monkeypatch.setattr(block, "residual_norm", lambda *a: a[:2])
+    u = z(T_, H)
+    M.forward_block(z(T_, H), u, GATE, EXPERTS, K, bias=z(E, dtype=f32))
+    assert seen == ([{"u", "w_gate", "bias", "w_in", "w_up", "w_out"}] if T_ else [])
