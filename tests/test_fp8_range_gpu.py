@@ -1,5 +1,5 @@
-"""The 8-bit floating-point products over long contractions, scales of every size and blocks of zeros, in
-every form; the tolerances are those of test_fp8_gpu.py.
+"""The 8-bit floating-point products over long contractions, scales of every size, blocks of zeros and
+products that cancel, in every form; the tolerances are those of test_fp8_gpu.py.
 
 A form brings the exponents of a row's blocks in words of four, so that contractions from 512 on take
 several of them, and from 1536 on each of the words' two places more than once.
@@ -99,3 +99,24 @@ def test_blocks_of_zeros(M, counts, K, N, dtype):
     y = M.grouped_mm_fp8(q, s, wq, ws, off.cuda(), dtype=dtype)
     check(y, *product_ref(q.cpu(), s.cpu(), wq.cpu(), ws.cpu(), off, dtype), "product")
     assert not bool(y[R // 2].any())
+
+
+@pytest.mark.parametrize("R,E,K,N", [(1, 1, 880, 40), (352, 1, 1040, 784), (634, 5, 432, 2976), (2655, 1, 432, 3576),
+                                     (1300, 1, 1552, 1400)])
+def test_products_that_cancel(M, R, E, K, N):
+    """In every block of 128 two large products cancel, beside small ones of 2^-14 or 1.5 2^-14 of them: with
+    fp32 output those are summed in fp32, so that nothing of them is lost; bf16 output may lose what
+    lies below 2^-13 of the largest product of a group of 8, 8 2^-13 of it for each group at most."""
+    g = torch.Generator().manual_seed(K)
+    x = torch.where(torch.rand(R, K, generator=g) < 0.5, 1.0, 1.5) * 2.0 ** -6
+    x[:, ::128], x[:, 1::128] = 256.0, -256.0
+    w = torch.ones(E, N, K) * 2.0 ** -1
+    xq, wq = x.to(E4), w.to(E4)
+    S = 4 * ((K + 511) // 512)
+    xs, ws = torch.full((R, S), 127, dtype=torch.uint8).view(E8), torch.full((E, -(-N // 128), S), 127, dtype=torch.uint8).view(E8)
+    off, rest = groups_of(R, E)
+    args = [t.cuda() for t in (xq, xs, wq, ws, off)]
+    ref, _ = product_ref(xq, xs, wq, ws, off, f32)
+    # all products and sums are multiples of 2^-8 below 2^12, 20 bits, and exact in fp32 in any order
+    assert torch.equal(M.grouped_mm_fp8(*args, dtype=f32).cpu().to(f64), ref)
+    check(M.grouped_mm_fp8(*args, dtype=bf), *product_ref(xq, xs, wq, ws, off, bf), "bf16 output")
