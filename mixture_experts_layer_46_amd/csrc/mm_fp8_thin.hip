@@ -5,9 +5,11 @@
 // What counts is the bytes in flight while the experts stream by, and that another workgroup's
 // fill the memory's time while one starts or ends.  A stage is one step: 64 bytes of every
 // index and one more load of the exponents, four bytes for each row and for the columns.
-// 64 experts of 2 rows, 4096 x 14336: 511 to 545 us, 6.2 TB/s, what pure reading reaches; one
-// row of 4096 x 14336 14 us (4.2 TB/s).  (Stages of a whole block for the 16x16x128 instruction
-// leave room for one workgroup a CU: 621 to 653 us.)
+// 64 experts of 2 rows each, 4096 x 14336: 606 us, 6.2 TB/s, what pure reading reaches; with the 128
+// rows drawn at random, so that 53 to 57 of the experts have any, 510 to 545 us at the same rate.
+// One row of 4096 x 14336 14 us (4.2 TB/s): its 224 tiles do not fill 256 CUs that hold two
+// workgroups each.  (Stages of a whole block for the 16x16x128 instruction leave room for one
+// workgroup a CU: 621 to 653 us on the drawn groups.)
 #include "mm_fp8.h"
 
 namespace moe {

@@ -52,12 +52,14 @@ constexpr Cost kRows32[FORMS] = {{}, {}, {1.05, .52, .10}, {3.95, .545, .45}, {2
 constexpr Cost kDw32[FORMS] = {{}, {}, {1.5, .68, .30}, {2.95, .44, .57}, {}};
 constexpr double kWriteRate = 5.2e6;      // bytes per us of a weight gradient, in every form
 
-// The kinds of mm_launch.h have shapes and costs of their own, fitted in the same way: to some 4000
-// calls each of 1-256 groups, 1-60000 rows, 64-8192 by 64-16384 (fp8 9000), timed in every form,
-// with the operands of successive calls at different places, so that weights come from memory.
-// Over as many others the form picked is slower than the best one by 1.4% (gated), 1.5% (gated,
-// fp32), 3.2% (two-pair dx), 2.0% (fp32), 1.9% (fp8) and 0.9% (fp8, fp32 output); the best single
-// form would be 11%, 27%, 22%, 17%, 19% and 18% slower.  fp8 has no 16-row form with bf16 output:
+// The kinds of mm_launch.h have shapes and costs of their own, fitted in the same way to random
+// calls of 1-256 groups, 1-60000 rows, 64-8192 by 64-16384, timed in every form with the operands
+// of successive calls at different places, so that weights come from memory.  Over 8100 to 9300
+// calls each (fp8 18800, with fp32 output 92000), a part of them those of the fit, the form picked is
+// slower than the best one by 1.4% (gated), 1.3% (gated, fp32), 3.2% (two-pair dx), 2.0% (fp32),
+// 1.9% (fp8) and 0.9% (fp8, fp32 output); the best single form would be 11%, 27%, 22%, 17%, 19%
+// and 18% slower.  A pair of weight gradients in one launch is estimated as one of them; and the
+// forms are not compared with two products and the activation.  fp8 has no 16-row form with bf16 output:
 // it was the best one in 4% of the calls and its choice won nothing.  (A gated tile's columns are
 // those of h.)
 struct FormCost {

@@ -20,8 +20,10 @@
 //
 // Measured (bytes read and written once; a large copy moves 4.9 TB/s): forward 8192 x 4096 bf16
 // 51 us (5.2 TB/s), 8192 x 7168 fp32 181 us (5.2), 32768 x 512 bf16 26 us (5.1); gradient
-// 8192 x 7168 bf16 149 us (4.7), 8192 x 4096 fp32 173 us (4.7), 4999 x 1032 fp32 43 us (2.9: 129
-// of a row's 192 threads have columns, and the second kernel is 5 us of it).
+// 8192 x 7168 bf16 149 us (4.7), 8192 x 4096 fp32 173 us (4.7).  Rows of 264 to 1032 columns are
+// slower: 4999 x 1032 fp32 43 us (2.9: 129 of a row's 192 threads have columns, and the second
+// kernel is 5 us of it), bf16 28 (2.2: half the bytes on their way, one row ahead of 16 bytes a
+// thread and input).
 #include "common.h"
 #include "launch.h"
 #include "mm_launch.h"
@@ -202,9 +204,9 @@ __global__ __launch_bounds__(RPW > 1 ? 64 * RPW : 1024) void k_norm(NormArgs a) 
 //   C = 1  parameters and all sums in registers, the next row's loads ahead.
 //   C = 3  (rows above 8192, to 12288; 512 threads, for 256 registers each) two of the three sums over
 //          rows live in LDS; parameters are read again for each row, from L2, all chunks' at once
-//          and kept from one phase to the next.  4000 x 12288 bf16 184 us (3.2 TB/s), fp32 267
-//          (4.4); with the next row's loads ahead and parameters read at each use 202 and 309,
-//          with both, which spills, 334; with C = 2 223 and 397.
+//          and kept from one phase to the next.  4000 x 12288 bf16 183 us (3.2 TB/s), fp32 278
+//          (4.2; measured beside the next three, 267); with the next row's loads ahead and parameters
+//          read at each use 202 and 309, with both, which spills, 334; with C = 2 223 and 397.
 //   C = 2  (longer rows; up to 1024 threads of 128 registers) as 3, but each parameter is read where
 //          it is used.  3000 x 16384 bf16 218 us (2.7 TB/s), fp32 386 (3.1); C = 4 in 512 threads
 //          spills: 229 to 383 and 435 to 458.
